@@ -545,3 +545,9 @@ gemm_mainloop = pipe_gemm_mainloop
 query_kernel = pipe_query_kernel
 kernel_resources = pipe_kernel_resources
 device_status = pipe_device_status
+
+# The operators of a quantised linear layer (pipe_linear.h).
+from .linear import (  # noqa: E402
+    PIPE_BF16, PIPE_E4M3, PIPE_FP16, PIPE_FP32, PIPE_RMSNORM_MAX_N, linear_symbols, pipe_gemm_fp8,
+    pipe_gemm_fp8_workspace_bytes, pipe_gemm_w4, pipe_rmsnorm, pipe_rmsnorm_backward,
+    pipe_rmsnorm_backward_workspace_bytes)

@@ -1,6 +1,7 @@
 """Build the tile-stream library for gfx950 with hipcc, in-tree.
 
-libpipetile.so -- the tile stream: all kernels + the C ABI of include/pipe_tile.h.
+libpipetile.so -- all kernels + the C ABI of include/pipe_tile.h (the tile stream)
+and include/pipe_linear.h (the quantised linear layer's operators).
 
 Every translation unit compiles to its own object, in parallel; the stream
 kernel source is compiled once per group of stage counts. Then the library
@@ -34,6 +35,10 @@ UNITS = [
     ("pipe_unified.hip", "pipe_unified.o", []),
     ("pipe_gemm.hip", "pipe_gemm_ring.o", ["PIPE_GEMM_PART=1"]),
     ("pipe_gemm.hip", "pipe_gemm_unified.o", ["PIPE_GEMM_PART=2"]),
+    ("pipe_linear_api.hip", "pipe_linear_api.o", []),
+    ("pipe_norm.hip", "pipe_norm.o", []),
+    ("pipe_gemm_fp8.hip", "pipe_gemm_fp8.o", []),
+    ("pipe_gemm_w4.hip", "pipe_gemm_w4.o", []),
 ]
 # Kept for callers that list the tile-stream sources.
 SOURCES = sorted({u[0] for u in UNITS})

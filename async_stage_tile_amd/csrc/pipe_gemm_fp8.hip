@@ -1,0 +1,399 @@
+// Products of e4m3 rows with e4m3 weights: C = (A B) * a_scales * b_scales, on
+// the 8-bit MFMAs (v_mfma_f32_16x16x128_f8f6f4 and 32x32x64, twice the rate of
+// the 16-bit and of the older 8-bit forms), fp32 sums.
+//
+// An MFMA multiplies the bytes that the two operands hold at the same place of
+// a lane, so any assignment of k's to places gives the same product as long as
+// both operands use it; the loads below choose the one that reads memory or
+// LDS in the best order.
+//
+// Few rows: the call is bound by reading B once, so B goes from memory straight
+// into registers (gemm_fp8_skinny_kernel). Many rows: A and B tiles pass
+// through an LDS ring (gemm_fp8_tile_kernel).
+#include "pipe_device.hpp"
+#include "pipe_linear.hpp"
+
+namespace pipe {
+
+namespace {
+
+__device__ __forceinline__ i32x8 join(u32x4 a, u32x4 b) {
+  return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
+}
+
+// ---------------------------------------------------------------------------
+// Few rows. A wave holds 16 NT rows of B and 16 MT of A; the waves of a
+// workgroup split K in steps of 128 bytes, each next step going to the next
+// wave, so that the workgroup as a whole reads long runs of each row. Their
+// sums meet in LDS, in wave order. Rows of A and B past the end are read from
+// the last row and dropped; bytes past K are zeros in both.
+// ---------------------------------------------------------------------------
+template <int MT, int NT, int WAVES, int OUT>
+__global__ void __launch_bounds__(64 * WAVES) gemm_fp8_skinny_kernel(Fp8Params p) {
+  constexpr int kTiles = MT * NT;
+  __shared__ f32x4 red[WAVES][kTiles][64];
+  const int lane = (int)(threadIdx.x & 63);
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int li = lane & 15, lq = lane >> 4;
+  const int m_tiles = (p.M + 16 * MT - 1) / (16 * MT);
+  const int64_t wg = long_block();
+  if (wg >= (int64_t)m_tiles * ((p.N + 16 * NT - 1) / (16 * NT))) return;
+  const int n0 = (int)(wg / m_tiles) * (16 * NT), m0 = (int)(wg % m_tiles) * (16 * MT);
+  const uint8_t *b_row[NT], *a_row[MT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+    b_row[j] = p.B + (int64_t)min(n0 + 16 * j + li, p.N - 1) * p.ldb + 16 * lq;
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+    a_row[i] = p.A + (int64_t)min(m0 + 16 * i + li, p.M - 1) * p.lda + 16 * lq;
+  f32x4 acc[NT][MT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  const int steps = (p.K + 127) >> 7;
+#pragma unroll 4
+  for (int st = wave; st < steps; st += WAVES) {
+    const int k0 = st << 7;
+    const bool in0 = k0 + 16 * lq < p.K, in1 = k0 + 64 + 16 * lq < p.K;
+    i32x8 b[NT], a[MT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      u32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
+      if (in0) lo = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(b_row[j] + k0));
+      if (in1) hi = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(b_row[j] + k0 + 64));
+      b[j] = join(lo, hi);
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      u32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
+      if (in0) lo = *reinterpret_cast<const u32x4*>(a_row[i] + k0);
+      if (in1) hi = *reinterpret_cast<const u32x4*>(a_row[i] + k0 + 64);
+      a[i] = join(lo, hi);
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j], a[i], acc[j][i], 0, 0, 0,
+                                                                     0, 0, 0);
+  }
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) red[wave][j * MT + i][lane] = acc[j][i];
+  __syncthreads();
+  // Lane l of a tile holds columns n = 4 (l / 16) .. + 3 of row m = l % 16.
+  for (int u = (int)threadIdx.x; u < kTiles * 64; u += 64 * WAVES) {
+    const int tile = u >> 6, l = u & 63;
+    f32x4 v = red[0][tile][l];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) v += red[w][tile][l];
+    const int m = m0 + 16 * (tile % MT) + (l & 15), n = n0 + 16 * (tile / MT) + 4 * (l >> 4);
+    if (m < p.M && n < p.N) {
+      const float sa = p.a_scales[m];
+      // b_scales may start at any 4-byte boundary: four single loads.
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = v[e] * sa * p.b_scales[n + e];
+      store4<OUT>(p.C, (int64_t)m * p.ldc + n, v);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows. Workgroups of WM x WN waves compute tiles of 32 WM FM x 32 WN FN,
+// each wave FM x FN MFMA blocks of 32 x 32. A stage of the LDS ring holds 64 k
+// (64 bytes) of the tile's A rows and B rows; S stages. 16 rows of 64 bytes are
+// one direct-to-LDS block; 16-byte chunk c of row r lies at place
+// c ^ ((r >> 2) & 3), which spreads the reads of one chunk of 16 consecutive
+// rows over all 64 banks. Half h (32 lanes) of a fragment takes chunks h and
+// 2 + h.
+//
+// One barrier a stage: at its top a wave's own loads of the next stage have
+// landed and its fragments of this stage are in registers. After the barrier
+// that holds for every wave, so this stage's slot is free and takes the stage S
+// ahead, and the next stage's fragments may be read; both go out between the
+// stage's MFMAs.
+//
+// Rows past M and N are read from the last row and dropped. Chunks past K come
+// from a buffer of zeros.
+// ---------------------------------------------------------------------------
+__device__ uint8_t g_fp8_zeros[16];
+
+template <int FM, int FN, int WM, int WN, int S>
+struct Fp8Tile {
+  static constexpr int kWaves = WM * WN;
+  static constexpr int kRowsA = 32 * FM * WM, kRowsB = 32 * FN * WN;
+  static constexpr int kBlocksA = kRowsA / 16, kBlocksB = kRowsB / 16;
+  static constexpr int kLoads = (kBlocksA + kBlocksB) / kWaves;
+  static constexpr int kStage = (kRowsA + kRowsB) * 64;
+  static_assert((kBlocksA + kBlocksB) % kWaves == 0, "whole blocks a wave");
+  static_assert(S * kStage <= 163840, "the ring fits");
+};
+
+// Output tile and K range of a work item. Workgroups go to the 8 XCDs in turn:
+// the items are dealt so that each XCD walks one contiguous run of the order,
+// and the order runs down bands of 4 tile rows, column by column, so that the
+// tiles an XCD holds at once share few A and B rows.
+__device__ __forceinline__ void fp8_item(const Fp8Params& p, int item, int items, int& tm, int& tn,
+                                         int& split) {
+  constexpr int kBand = 4;
+  const int per = items >> 3, odd = items & 7, xcd = item & 7;
+  int q = xcd * per + min(xcd, odd) + (item >> 3);
+  split = q % p.splits;
+  q /= p.splits;
+  const int band = kBand * p.tiles_n;
+  const int first = q / band * kBand;
+  const int rows = min(p.tiles_m - first, kBand);
+  const int local = q % band;
+  tm = first + local % rows;
+  tn = local / rows;
+}
+
+template <int FM, int FN, int WM, int WN, int S, int PER_CU, int OUT>
+__global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_fp8_tile_kernel(Fp8Params p) {
+  using Tile = Fp8Tile<FM, FN, WM, WN, S>;
+  __shared__ __align__(1024) uint8_t ring[S][Tile::kStage];
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int lane = lane_id();
+  const int li = lane & 31, lh = lane >> 5;
+  const int wm = wave / WN, wn = wave % WN;
+  const uint32_t base = uniform(lds_addr(&ring[0][0]));
+  const int items = p.tiles_m * p.tiles_n * p.splits;  // < 2^31, checked by the host
+  // In a block, lane l loads the chunk that lies at place l % 4 of row l / 4.
+  const int chunk = (lane & 3) ^ ((lane >> 4) & 3);
+
+  const int64_t wg = long_block();
+  if (wg >= items) return;
+  int tm, tn, split;
+  fp8_item(p, (int)wg, items, tm, tn, split);
+  const int per = (p.steps + p.splits - 1) / p.splits;
+  const int first = split * per;
+  const int count = min(per, p.steps - first);   // >= 1: the host leaves no split empty
+
+  const uint8_t* src[Tile::kLoads];
+#pragma unroll
+  for (int j = 0; j < Tile::kLoads; ++j) {
+    const int q = wave * Tile::kLoads + j;       // blocks of A, then of B
+    if (q < Tile::kBlocksA) {
+      const int r = min(tm * Tile::kRowsA + q * 16 + (lane >> 2), p.M - 1);
+      src[j] = p.A + (int64_t)r * p.lda + chunk * 16;
+    } else {
+      const int r = min(tn * Tile::kRowsB + (q - Tile::kBlocksA) * 16 + (lane >> 2), p.N - 1);
+      src[j] = p.B + (int64_t)r * p.ldb + chunk * 16;
+    }
+  }
+  auto load = [&](int ks, int slot, int j) {
+    const int64_t k = (int64_t)(first + ks) * 64;
+    const uint8_t* g = src[j] + k;
+    if (k + chunk * 16 >= p.K) g = g_fp8_zeros;
+    dma_block(g, base + slot * Tile::kStage + (wave * Tile::kLoads + j) * kBlockBytes);
+  };
+  const uint8_t* frag_a = &ring[0][0] + (wm * FM * 32 + li) * 64;
+  const uint8_t* frag_b = &ring[0][0] + (Tile::kRowsA + wn * FN * 32 + li) * 64;
+  const int x0 = (lh ^ ((li >> 2) & 3)) * 16, x1 = ((2 + lh) ^ ((li >> 2) & 3)) * 16;
+  auto read = [&](const uint8_t* row) {
+    return join(*reinterpret_cast<const u32x4*>(row + x0), *reinterpret_cast<const u32x4*>(row + x1));
+  };
+
+  f32x16 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+
+  const int ahead = min(count, S);
+  for (int g = 0; g < ahead; ++g)
+#pragma unroll
+    for (int j = 0; j < Tile::kLoads; ++j) load(g, g, j);
+  if (ahead == S) wait_vmcnt<(S - 1) * Tile::kLoads>();
+  else wait_vmcnt<0>();
+  __syncthreads();
+  i32x8 fa[2][FM], fb[2][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i) fa[0][i] = read(frag_a + i * 2048);
+#pragma unroll
+  for (int j = 0; j < FN; ++j) fb[0][j] = read(frag_b + j * 2048);
+
+  int slot = 0;
+  auto stage = [&](int ks, i32x8 (&a)[FM], i32x8 (&b)[FN], i32x8 (&na)[FM], i32x8 (&nb)[FN]) {
+    // This wave's loads of stage ks + 1 have landed: at most those of the
+    // stages ks + 2 .. ks + S - 1 are younger. Near the end fewer were issued.
+    if (ks + S <= count) wait_vmcnt<(S - 2) * Tile::kLoads>();
+    else wait_vmcnt<0>();
+    wait_lgkmcnt0();
+    __syncthreads();
+    const int next = slot + 1 == S ? 0 : slot + 1;
+    const bool fill = ks + S < count;
+    const uint8_t* sa = frag_a + next * Tile::kStage;
+    const uint8_t* sb = frag_b + next * Tile::kStage;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        constexpr int kBlocks = FM * FN;
+        const int at = i * FN + j;
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[i], b[j], acc[i][j], 0, 0, 0,
+                                                                    0, 0, 0);
+        // After the last stage these reads take a slot nobody uses.
+#pragma unroll
+        for (int f = at * (FM + FN) / kBlocks; f < (at + 1) * (FM + FN) / kBlocks; ++f) {
+          if (f < FM) na[f] = read(sa + f * 2048);
+          else nb[f - FM] = read(sb + (f - FM) * 2048);
+        }
+#pragma unroll
+        for (int l = at * Tile::kLoads / kBlocks; l < (at + 1) * Tile::kLoads / kBlocks; ++l)
+          if (fill) load(ks + S, slot, l);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    slot = next;
+  };
+  int ks = 0;
+  for (; ks + 1 < count; ks += 2) {
+    stage(ks, fa[0], fb[0], fa[1], fb[1]);
+    stage(ks + 1, fa[1], fb[1], fa[0], fb[0]);
+  }
+  if (ks < count) stage(ks, fa[0], fb[0], fa[1], fb[1]);
+  wait_vmcnt<0>();
+
+  // As in the 16-bit GEMM's epilogue: the wave sleeps once before the first
+  // accumulator is read, which was seen to come too early there.
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_sleep(1);
+  __builtin_amdgcn_sched_barrier(0);
+  // Lane l holds column l % 32 and rows 8 (e / 4) + 4 (l / 32) + e % 4 of a block.
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const int col = tn * Tile::kRowsB + (wn * FN + j) * 32 + li;
+      const int row0 = tm * Tile::kRowsA + (wm * FM + i) * 32 + 4 * lh;
+      if (col >= p.N) continue;
+      if (p.splits > 1) {
+        float* out = p.partials + (int64_t)split * p.M * p.N + col;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int row = row0 + 8 * (e >> 2) + (e & 3);
+          if (row < p.M) out[(int64_t)row * p.N] = acc[i][j][e];
+        }
+        continue;
+      }
+      const float sb = p.b_scales[col];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int row = row0 + 8 * (e >> 2) + (e & 3);
+        if (row < p.M) {
+          const float v = acc[i][j][e] * p.a_scales[row] * sb;
+          const int64_t at = (int64_t)row * p.ldc + col;
+          if constexpr (OUT == 0) static_cast<__bf16*>(p.C)[at] = (__bf16)v;
+          else if constexpr (OUT == 1) static_cast<_Float16*>(p.C)[at] = (_Float16)v;
+          else static_cast<float*>(p.C)[at] = v;
+        }
+      }
+    }
+}
+
+// Sum of the splits' partial products in split order, scaled and rounded: four
+// columns a thread.
+template <int OUT>
+__global__ void __launch_bounds__(256) gemm_fp8_join_kernel(Fp8Params p) {
+  const int quads = p.N >> 2;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (int64_t)p.M * quads) return;
+  const int m = (int)(i / quads), n = (int)(i % quads) * 4;
+  const int64_t plane = (int64_t)p.M * p.N;
+  const float* src = p.partials + (int64_t)m * p.N + n;
+  f32x4 v = *reinterpret_cast<const f32x4*>(src);
+  for (int s = 1; s < p.splits; ++s) v += *reinterpret_cast<const f32x4*>(src + s * plane);
+  const float sa = p.a_scales[m];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = v[e] * sa * p.b_scales[n + e];
+  store4<OUT>(p.C, (int64_t)m * p.ldc + n, v);
+}
+
+// ---------------------------------------------------------------------------
+// Choice of kernel.
+// ---------------------------------------------------------------------------
+enum Fp8Kind { kSkinny, kTile128, kTile256 };
+
+struct Fp8Plan {
+  Fp8Kind kind;
+  int tiles_m, tiles_n, splits, steps;
+};
+
+int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K) {
+  Fp8Plan c{kSkinny, 0, 0, 1, ceil_div(K, 64)};
+  if (M <= 64) return c;
+  const int64_t big = (int64_t)ceil_div(M, 256) * ceil_div(N, 256);
+  const int tile = big >= 256 ? 256 : 128;
+  c.kind = tile == 256 ? kTile256 : kTile128;
+  c.tiles_m = ceil_div(M, tile);
+  c.tiles_n = ceil_div(N, tile);
+  if (tile == 128) {
+    // Fill the 512 places for workgroups (two a CU) by splitting K, 8 stages a
+    // split at least.
+    const int64_t tiles = (int64_t)c.tiles_m * c.tiles_n;
+    int splits = (int)(512 / tiles);
+    splits = splits < c.steps / 8 ? splits : c.steps / 8;
+    splits = splits > 16 ? 16 : splits;
+    if (splits > 1) {
+      const int per = ceil_div(c.steps, splits);
+      c.splits = ceil_div(c.steps, per);  // no empty split
+    }
+  }
+  return c;
+}
+
+template <int OUT>
+hipError_t launch_fp8_out(const Fp8Params& p, Fp8Kind kind, hipStream_t stream) {
+  if (kind == kSkinny) {
+    const auto grid = [&](int mt, int nt) {
+      return long_grid((int64_t)ceil_div(p.N, 16 * nt) * ceil_div(p.M, 16 * mt));
+    };
+    if (p.M <= 16)
+      hipLaunchKernelGGL((gemm_fp8_skinny_kernel<1, 1, 8, OUT>), grid(1, 1), dim3(512), 0, stream, p);
+    else if (p.M <= 32)
+      hipLaunchKernelGGL((gemm_fp8_skinny_kernel<2, 2, 8, OUT>), grid(2, 2), dim3(512), 0, stream, p);
+    else
+      hipLaunchKernelGGL((gemm_fp8_skinny_kernel<4, 2, 8, OUT>), grid(4, 2), dim3(512), 0, stream, p);
+    return hipGetLastError();
+  }
+  const int64_t items = (int64_t)p.tiles_m * p.tiles_n * p.splits;
+  if (kind == kTile256)
+    hipLaunchKernelGGL((gemm_fp8_tile_kernel<4, 4, 2, 2, 4, 1, OUT>), long_grid(items), dim3(256), 0,
+                       stream, p);
+  else
+    hipLaunchKernelGGL((gemm_fp8_tile_kernel<2, 2, 2, 2, 4, 2, OUT>), long_grid(items), dim3(256), 0,
+                       stream, p);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
+  const int64_t quads = (int64_t)p.M * (p.N / 4);
+  hipLaunchKernelGGL(gemm_fp8_join_kernel<OUT>, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0,
+                     stream, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t gemm_fp8_partials(int64_t M, int64_t N, int64_t K) {
+  const Fp8Plan c = fp8_plan(M, N, K);
+  return c.splits > 1 ? (int64_t)c.splits * M * N : 0;
+}
+
+hipError_t launch_gemm_fp8(Fp8Params p, int out_type, hipStream_t stream) {
+  const Fp8Plan c = fp8_plan(p.M, p.N, p.K);
+  p.tiles_m = c.tiles_m;
+  p.tiles_n = c.tiles_n;
+  p.splits = c.splits;
+  p.steps = c.steps;
+  if (out_type == 0) return launch_fp8_out<0>(p, c.kind, stream);
+  if (out_type == 1) return launch_fp8_out<1>(p, c.kind, stream);
+  return launch_fp8_out<2>(p, c.kind, stream);
+}
+
+}  // namespace pipe

@@ -1,0 +1,398 @@
+// RMS norm with the residual's addition and a 16-bit or e4m3 output, and its
+// gradient.
+//
+// Forward: h = x + residual (rounded to 16 bits), r = rsqrt(mean(h^2) + eps),
+// y = h r w. A row is read once: its h stays in registers, packed as the 16
+// bits that it is rounded to anyway, until the row's sum of squares is known.
+// The e4m3 output needs max|y| = r max|h w| before any value can be written;
+// that maximum does not depend on r, so it is taken in the same pass as the sum
+// and one exchange between the waves serves both. The maximum is taken over
+// the bit patterns of |h w| as integers, whose order is the floats' order with
+// NaN above everything: a NaN anywhere gives the row a NaN scale.
+//
+// Gradient: with g = dy w, dx = r g - h r^3 mean(g h) (+ dh) and
+// dweight = sum_rows dy h r. A row's two sums (h^2 and g h) come from one pass
+// over registers too. A workgroup walks rows in steps of the grid and keeps
+// the dweight sums of its columns in fp32 registers; the sums of the
+// workgroups meet in a second small kernel, in a fixed order.
+//
+// Both are bound by memory: a few fp32 operations for every byte moved.
+#include "pipe_linear.hpp"
+
+namespace pipe {
+
+namespace {
+
+constexpr float kE4m3Max = 448.f;
+constexpr float kAmaxMin = 0x1p-100f;  // keeps the scale and its reciprocal normal numbers
+
+// The sums of the waves of one row: TPR threads a row, in a workgroup of WG.
+template <int TPR, int WG, bool MAX>
+struct RowExchange {
+  static constexpr int kWaves = WG / 64, kRowWaves = TPR / 64;
+  float sum[2][kWaves];
+  uint32_t top[MAX ? kWaves : 1];
+};
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// Keeps the 16-bit pairs as what stays in registers across a reduction: without
+// it the compiler keeps their fp32 values, twice the registers.
+template <int CH>
+__device__ __forceinline__ void keep_packed(u32x4 (&v)[CH]) {
+#pragma unroll
+  for (int i = 0; i < CH; ++i) asm("" : "+v"(v[i]));
+}
+
+// One row per TPR threads, WG / TPR rows a workgroup; a thread holds CH chunks
+// of 8 elements, chunk index t + TPR * i.
+template <class T, int TPR, int WG, int CH, bool RES, bool Q8>
+__global__ void __launch_bounds__(WG) rmsnorm_kernel(NormParams p) {
+  constexpr int kRows = WG / TPR, kRowWaves = TPR / 64;
+  __shared__ RowExchange<TPR, WG, Q8> ex;
+  const int t = threadIdx.x % TPR;
+  const int64_t row = long_block() * kRows + threadIdx.x / TPR;
+  const bool live = row < p.M;
+  const int64_t at = live ? row : p.M - 1;
+  const u32x4* x = reinterpret_cast<const u32x4*>(p.x + at * p.ld_x);
+  const u32x4* res = reinterpret_cast<const u32x4*>(p.residual + at * p.ld_residual);
+  const u32x4* w = reinterpret_cast<const u32x4*>(p.weight);
+  u32x4 v[CH], a[RES ? CH : 1], wt[CH];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = t + TPR * i;
+    v[i] = u32x4{0, 0, 0, 0};
+    if (c < p.chunks) v[i] = __builtin_nontemporal_load(x + c);
+  }
+  if constexpr (RES) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = t + TPR * i;
+      a[i] = u32x4{0, 0, 0, 0};
+      if (c < p.chunks) a[i] = __builtin_nontemporal_load(res + c);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = t + TPR * i;
+    wt[i] = u32x4{0, 0, 0, 0};
+    if (c < p.chunks) wt[i] = w[c];
+  }
+  float sum = 0.f;
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (RES)
+        v[i][e] = Pair<T>::pack(Pair<T>::lo(v[i][e]) + Pair<T>::lo(a[i][e]),
+                                Pair<T>::hi(v[i][e]) + Pair<T>::hi(a[i][e]));
+      const float lo = Pair<T>::lo(v[i][e]), hi = Pair<T>::hi(v[i][e]);
+      sum += lo * lo;
+      sum += hi * hi;
+      if constexpr (Q8) {
+        const uint32_t tl = abs_bits(lo * Pair<T>::lo(wt[i][e]));
+        const uint32_t th = abs_bits(hi * Pair<T>::hi(wt[i][e]));
+        top = max(top, max(tl, th));
+      }
+    }
+  }
+  sum = wave_sum(sum);
+  if constexpr (Q8) top = wave_max(top);
+  if constexpr (kRowWaves > 1) {
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+      ex.sum[0][wave] = sum;
+      if constexpr (Q8) ex.top[wave] = top;
+    }
+    __syncthreads();
+    const int first = wave / kRowWaves * kRowWaves;
+    sum = 0.f;
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < kRowWaves; ++i) {
+      sum += ex.sum[0][first + i];
+      if constexpr (Q8) top = max(top, ex.top[first + i]);
+    }
+  }
+  if (!live) return;
+  keep_packed(v);
+  keep_packed(wt);
+  const float r = 1.0f / sqrtf(sum * p.inv_n + p.eps);
+  if constexpr (RES) {
+    u32x4* h = reinterpret_cast<u32x4*>(p.h + row * p.ld_h);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = t + TPR * i;
+      if (c < p.chunks) __builtin_nontemporal_store(v[i], h + c);
+    }
+  }
+  if constexpr (Q8) {
+    float m = __uint_as_float(top) * r;
+    m = m < kAmaxMin ? kAmaxMin : m;  // a NaN stays
+    const float s = m / kE4m3Max;
+    const float inv = kE4m3Max / m;
+    if (t == 0) p.scales[row] = s;
+    u32x2* y = reinterpret_cast<u32x2*>(p.y + row * p.ld_y);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = t + TPR * i;
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f[2 * e] = Pair<T>::lo(v[i][e]) * r * Pair<T>::lo(wt[i][e]) * inv;
+        f[2 * e + 1] = Pair<T>::hi(v[i][e]) * r * Pair<T>::hi(wt[i][e]) * inv;
+      }
+      u32x2 o;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        int b = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * e], f[4 * e + 1], 0, false);
+        o[e] = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * e + 2], f[4 * e + 3], b, true);
+      }
+      if (c < p.chunks) __builtin_nontemporal_store(o, y + c);
+    }
+  } else {
+    u32x4* y = reinterpret_cast<u32x4*>(p.y + row * p.ld_y);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = t + TPR * i;
+      u32x4 o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        o[e] = Pair<T>::pack(Pair<T>::lo(v[i][e]) * r * Pair<T>::lo(wt[i][e]),
+                             Pair<T>::hi(v[i][e]) * r * Pair<T>::hi(wt[i][e]));
+      if (c < p.chunks) __builtin_nontemporal_store(o, y + c);
+    }
+  }
+}
+
+template <class T, int TPR, int WG, int CH>
+hipError_t launch_norm_shape(const NormParams& p, bool q8, hipStream_t stream) {
+  const int64_t wgs = (p.M + WG / TPR - 1) / (WG / TPR);
+  const bool res = p.residual != nullptr;
+  void (*k)(NormParams) = res ? (q8 ? rmsnorm_kernel<T, TPR, WG, CH, true, true>
+                                    : rmsnorm_kernel<T, TPR, WG, CH, true, false>)
+                              : (q8 ? rmsnorm_kernel<T, TPR, WG, CH, false, true>
+                                    : rmsnorm_kernel<T, TPR, WG, CH, false, false>);
+  hipLaunchKernelGGL(k, long_grid(wgs), dim3(WG), 0, stream, p);
+  return hipGetLastError();
+}
+
+// Rows of up to 2048 elements: one wave each, no exchange between waves. Wider
+// rows: a workgroup each, of as many threads as leave each at most 4 chunks.
+template <class T>
+hipError_t launch_norm_type(const NormParams& p, bool q8, hipStream_t stream) {
+  if (p.chunks <= 64) return launch_norm_shape<T, 64, 256, 1>(p, q8, stream);
+  if (p.chunks <= 128) return launch_norm_shape<T, 64, 256, 2>(p, q8, stream);
+  if (p.chunks <= 256) return launch_norm_shape<T, 64, 256, 4>(p, q8, stream);
+  if (p.chunks <= 512) return launch_norm_shape<T, 256, 256, 2>(p, q8, stream);
+  if (p.chunks <= 1024) return launch_norm_shape<T, 256, 256, 4>(p, q8, stream);
+  if (p.chunks <= 2048) return launch_norm_shape<T, 512, 512, 4>(p, q8, stream);
+  return launch_norm_shape<T, 1024, 1024, 4>(p, q8, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Gradient.
+// ---------------------------------------------------------------------------
+template <class T, int TPR, int WG, int CH, bool RES>
+__global__ void __launch_bounds__(WG) rmsnorm_grad_kernel(NormGradParams p) {
+  constexpr int kRows = WG / TPR, kRowWaves = TPR / 64;
+  __shared__ RowExchange<TPR, WG, false> ex[2];
+  const int t = threadIdx.x % TPR;
+  const int sub = threadIdx.x / TPR;
+  const int wave = threadIdx.x >> 6;
+  const u32x4* w = reinterpret_cast<const u32x4*>(p.weight);
+  u32x4 wt[CH];
+  float dw[CH][8];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = t + TPR * i;
+    wt[i] = u32x4{0, 0, 0, 0};
+    if (c < p.chunks) wt[i] = w[c];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[i][e] = 0.f;
+  }
+  int turn = 0;
+  for (int64_t base = (int64_t)blockIdx.x * kRows; base < p.M;
+       base += (int64_t)gridDim.x * kRows, turn ^= 1) {
+    const int64_t row = base + sub;
+    const bool live = row < p.M;
+    const int64_t at = live ? row : p.M - 1;
+    const u32x4* dy = reinterpret_cast<const u32x4*>(p.dy + at * p.ld_dy);
+    const u32x4* x = reinterpret_cast<const u32x4*>(p.x + at * p.ld_x);
+    const u32x4* dh = reinterpret_cast<const u32x4*>(p.dh + at * p.ld_dh);
+    u32x4 d[CH], h[CH], s[RES ? CH : 1];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = t + TPR * i;
+      h[i] = d[i] = u32x4{0, 0, 0, 0};
+      if (c < p.chunks) {
+        h[i] = __builtin_nontemporal_load(x + c);
+        d[i] = __builtin_nontemporal_load(dy + c);
+      }
+    }
+    if constexpr (RES) {
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int c = t + TPR * i;
+        s[i] = u32x4{0, 0, 0, 0};
+        if (c < p.chunks) s[i] = __builtin_nontemporal_load(dh + c);
+      }
+    }
+    float hh = 0.f, gh = 0.f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float hl = Pair<T>::lo(h[i][e]), hu = Pair<T>::hi(h[i][e]);
+        hh += hl * hl;
+        hh += hu * hu;
+        gh += Pair<T>::lo(d[i][e]) * Pair<T>::lo(wt[i][e]) * hl;
+        gh += Pair<T>::hi(d[i][e]) * Pair<T>::hi(wt[i][e]) * hu;
+      }
+    }
+    hh = wave_sum(hh);
+    gh = wave_sum(gh);
+    if constexpr (kRowWaves > 1) {
+      // Two exchange buffers in turn: a wave writes one again only after the
+      // barrier of the other, which every wave reaches after its reads.
+      if ((threadIdx.x & 63) == 0) {
+        ex[turn].sum[0][wave] = hh;
+        ex[turn].sum[1][wave] = gh;
+      }
+      __syncthreads();
+      const int first = wave / kRowWaves * kRowWaves;
+      hh = gh = 0.f;
+#pragma unroll
+      for (int i = 0; i < kRowWaves; ++i) {
+        hh += ex[turn].sum[0][first + i];
+        gh += ex[turn].sum[1][first + i];
+      }
+    }
+    keep_packed(h);
+    keep_packed(d);
+    keep_packed(wt);
+    if (live) {
+      const float r = 1.0f / sqrtf(hh * p.inv_n + p.eps);
+      const float k = gh * p.inv_n * r * r * r;
+      u32x4* dx = reinterpret_cast<u32x4*>(p.dx + row * p.ld_dx);
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int c = t + TPR * i;
+        u32x4 o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float hl = Pair<T>::lo(h[i][e]), hu = Pair<T>::hi(h[i][e]);
+          const float dl = Pair<T>::lo(d[i][e]), du = Pair<T>::hi(d[i][e]);
+          float ol = dl * Pair<T>::lo(wt[i][e]) * r - hl * k;
+          float ou = du * Pair<T>::hi(wt[i][e]) * r - hu * k;
+          if constexpr (RES) {
+            ol += Pair<T>::lo(s[i][e]);
+            ou += Pair<T>::hi(s[i][e]);
+          }
+          o[e] = Pair<T>::pack(ol, ou);
+          dw[i][2 * e] += dl * (hl * r);
+          dw[i][2 * e + 1] += du * (hu * r);
+        }
+        if (c < p.chunks) __builtin_nontemporal_store(o, dx + c);
+      }
+    }
+  }
+  f32x4* out = reinterpret_cast<f32x4*>(p.partials + ((int64_t)blockIdx.x * kRows + sub) *
+                                                         ((int64_t)p.chunks * 8));
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = t + TPR * i;
+    if (c < p.chunks) {
+      out[2 * c] = f32x4{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
+      out[2 * c + 1] = f32x4{dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
+    }
+  }
+}
+
+// dweight: the partials' sum. A workgroup takes 32 columns (8 threads of four)
+// and 32 interleaved sets of partials, each summed in order, then the 32 sums
+// in order.
+__global__ void __launch_bounds__(256) rmsnorm_dweight_kernel(const float* __restrict__ partials,
+                                                              float* __restrict__ dweight,
+                                                              int count, int n) {
+  __shared__ f32x4 part[32][8];
+  const int lane = threadIdx.x & 7, set = threadIdx.x >> 3;
+  const int col = blockIdx.x * 32 + lane * 4;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  if (col < n) {
+    const float* src = partials + col;
+#pragma unroll 4
+    for (int i = set; i < count; i += 32)
+      acc += *reinterpret_cast<const f32x4*>(src + (int64_t)i * n);
+  }
+  part[set][lane] = acc;
+  __syncthreads();
+  if (set == 0 && col < n) {
+    acc = part[0][lane];
+    for (int i = 1; i < 32; ++i) acc += part[i][lane];
+    *reinterpret_cast<f32x4*>(dweight + col) = acc;
+  }
+}
+
+struct GradShape {
+  int rows;        // rows in flight a workgroup
+  int64_t grid;
+};
+
+// Workgroups of the gradient: enough to fill the card twice over, and no more
+// than there are rows to start on, since each writes a row of partials.
+GradShape grad_shape(int64_t M, int64_t chunks) {
+  GradShape g;
+  g.rows = chunks <= 256 ? 4 : 1;
+  const int64_t need = (M + g.rows - 1) / g.rows;
+  g.grid = need < 512 ? need : 512;
+  return g;
+}
+
+template <class T, int TPR, int WG, int CH>
+hipError_t launch_grad_shape(const NormGradParams& p, int64_t grid, hipStream_t stream) {
+  void (*k)(NormGradParams) = p.dh != nullptr ? rmsnorm_grad_kernel<T, TPR, WG, CH, true>
+                                              : rmsnorm_grad_kernel<T, TPR, WG, CH, false>;
+  hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(WG), 0, stream, p);
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t launch_grad_type(const NormGradParams& p, int64_t grid, hipStream_t stream) {
+  if (p.chunks <= 64) return launch_grad_shape<T, 64, 256, 1>(p, grid, stream);
+  if (p.chunks <= 128) return launch_grad_shape<T, 64, 256, 2>(p, grid, stream);
+  if (p.chunks <= 256) return launch_grad_shape<T, 64, 256, 4>(p, grid, stream);
+  if (p.chunks <= 512) return launch_grad_shape<T, 256, 256, 2>(p, grid, stream);
+  if (p.chunks <= 1024) return launch_grad_shape<T, 512, 512, 2>(p, grid, stream);
+  if (p.chunks <= 2048) return launch_grad_shape<T, 1024, 1024, 2>(p, grid, stream);
+  return launch_grad_shape<T, 1024, 1024, 4>(p, grid, stream);
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm(const NormParams& p, int type, bool q8, hipStream_t stream) {
+  return type == 0 ? launch_norm_type<__bf16>(p, q8, stream)
+                   : launch_norm_type<_Float16>(p, q8, stream);
+}
+
+int64_t rmsnorm_grad_partials(int64_t M, int64_t N) {
+  const GradShape g = grad_shape(M, N / 8);
+  return g.grid * g.rows;
+}
+
+hipError_t launch_rmsnorm_grad(const NormGradParams& p, float* dweight, int type,
+                               hipStream_t stream) {
+  const GradShape g = grad_shape(p.M, p.chunks);
+  if (g.grid > 0) {
+    const hipError_t e = type == 0 ? launch_grad_type<__bf16>(p, g.grid, stream)
+                                   : launch_grad_type<_Float16>(p, g.grid, stream);
+    if (e != hipSuccess) return e;
+  }
+  const int n = p.chunks * 8;
+  hipLaunchKernelGGL(rmsnorm_dweight_kernel, dim3((n + 31) / 32), dim3(256), 0, stream, p.partials,
+                     dweight, (int)(g.grid * g.rows), n);
+  return hipGetLastError();
+}
+
+}  // namespace pipe
