@@ -103,32 +103,52 @@ __global__ void __launch_bounds__(64 * WAVES) gemm_fp8_skinny_kernel(Fp8Params p
 
 // ---------------------------------------------------------------------------
 // Many rows. Workgroups of WM x WN waves compute tiles of 32 WM FM x 32 WN FN,
-// each wave FM x FN MFMA blocks of 32 x 32. A stage of the LDS ring holds 64 k
-// (64 bytes) of the tile's A rows and B rows; S stages. 16 rows of 64 bytes are
-// one direct-to-LDS block; 16-byte chunk c of row r lies at place
-// c ^ ((r >> 2) & 3), which spreads the reads of one chunk of 16 consecutive
-// rows over all 64 banks. Half h (32 lanes) of a fragment takes chunks h and
-// 2 + h.
+// each wave FM x FN MFMA blocks of 32 x 32. A stage of the LDS ring holds 128 k
+// (128 bytes: whole cache lines) of the tile's A rows and B rows; S stages.
+// 8 rows are one direct-to-LDS block; 16-byte chunk c of row r lies at place
+// c ^ ((r >> 1) & 7), which spreads the reads of one chunk of 16 consecutive
+// rows over all 64 banks. A stage is two MFMA steps of 64 k; half h (32 lanes)
+// of a fragment of step t takes chunks 4 t + h and 4 t + 2 + h.
 //
-// One barrier a stage: at its top a wave's own loads of the next stage have
-// landed and its fragments of this stage are in registers. After the barrier
-// that holds for every wave, so this stage's slot is free and takes the stage S
-// ahead, and the next stage's fragments may be read; both go out between the
-// stage's MFMAs.
+// Fragments are read one step ahead. The first step's MFMAs of a stage go with
+// the reads of its second step. Then one barrier: every wave has read all of
+// this stage's slot, and its own loads of the next stage have landed. The
+// second step's MFMAs go with the loads of the stage S ahead, into this stage's
+// slot, and the reads of the next stage's first step. The loads near the end
+// fetch the last stage again, so that the loop has no branch and its wait one
+// count.
 //
-// Rows past M and N are read from the last row and dropped. Chunks past K come
-// from a buffer of zeros.
+// A load's address is a scalar base, which moves 128 bytes a stage, and a
+// 32-bit offset a lane that stays: rows of up to 2^24 bytes. Rows past M and N
+// are read from the last row and dropped. Lanes whose chunk lies past K (in the
+// last stage) load the row's chunk 0 of that stage instead, and A's fragments
+// are zeroed there, so that chunk's finite values add nothing, and a NaN in it
+// is in the row's product anyway.
 // ---------------------------------------------------------------------------
-__device__ uint8_t g_fp8_zeros[16];
+__device__ __forceinline__ void dma_block_at(const uint8_t* base, uint32_t offset,
+                                             uint32_t lds_base) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :
+               : "v"(offset), "s"(base), "{m0}"(lds_base)
+               : "memory");
+}
+
+constexpr int kFp8StageK = 128;
+
+template <int T>
+struct Step {
+  static constexpr int value = T;
+};
 
 template <int FM, int FN, int WM, int WN, int S>
 struct Fp8Tile {
   static constexpr int kWaves = WM * WN;
   static constexpr int kRowsA = 32 * FM * WM, kRowsB = 32 * FN * WN;
-  static constexpr int kBlocksA = kRowsA / 16, kBlocksB = kRowsB / 16;
+  static constexpr int kBlocksA = kRowsA / 8, kBlocksB = kRowsB / 8;
   static constexpr int kLoads = (kBlocksA + kBlocksB) / kWaves;
-  static constexpr int kStage = (kRowsA + kRowsB) * 64;
-  static_assert((kBlocksA + kBlocksB) % kWaves == 0, "whole blocks a wave");
+  static constexpr int kStage = (kRowsA + kRowsB) * kFp8StageK;
+  static_assert((kBlocksA + kBlocksB) % kWaves == 0 && kBlocksA % kLoads == 0 && kLoads % 2 == 0,
+                "a wave loads whole blocks of one operand, an even number");
   static_assert(S * kStage <= 163840, "the ring fits");
 };
 
@@ -161,9 +181,6 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_fp8_tile_kernel(Fp8
   const int wm = wave / WN, wn = wave % WN;
   const uint32_t base = uniform(lds_addr(&ring[0][0]));
   const int items = p.tiles_m * p.tiles_n * p.splits;  // < 2^31, checked by the host
-  // In a block, lane l loads the chunk that lies at place l % 4 of row l / 4.
-  const int chunk = (lane & 3) ^ ((lane >> 4) & 3);
-
   const int64_t wg = long_block();
   if (wg >= items) return;
   int tm, tn, split;
@@ -172,29 +189,55 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_fp8_tile_kernel(Fp8
   const int first = split * per;
   const int count = min(per, p.steps - first);   // >= 1: the host leaves no split empty
 
-  const uint8_t* src[Tile::kLoads];
+  // This wave's blocks of a stage: kLoads of A's, or of B's.
+  const bool load_a = wave * Tile::kLoads < Tile::kBlocksA;
+  const int block0 = wave * Tile::kLoads - (load_a ? 0 : Tile::kBlocksA);
+  const int row0 = load_a ? tm * Tile::kRowsA : tn * Tile::kRowsB;
+  const int64_t ld = load_a ? p.lda : p.ldb;
+  const int rows = (load_a ? p.M : p.N) - row0;   // rows of the tile, and more
+  // In block j, lane l loads the chunk that lies at place l % 8 of row l / 8.
+  const int chunk0 = (lane & 7) ^ (lane >> 4) ^ ((block0 & 1) << 2);
+  uint32_t off[Tile::kLoads];
 #pragma unroll
-  for (int j = 0; j < Tile::kLoads; ++j) {
-    const int q = wave * Tile::kLoads + j;       // blocks of A, then of B
-    if (q < Tile::kBlocksA) {
-      const int r = min(tm * Tile::kRowsA + q * 16 + (lane >> 2), p.M - 1);
-      src[j] = p.A + (int64_t)r * p.lda + chunk * 16;
-    } else {
-      const int r = min(tn * Tile::kRowsB + (q - Tile::kBlocksA) * 16 + (lane >> 2), p.N - 1);
-      src[j] = p.B + (int64_t)r * p.ldb + chunk * 16;
-    }
-  }
-  auto load = [&](int ks, int slot, int j) {
-    const int64_t k = (int64_t)(first + ks) * 64;
-    const uint8_t* g = src[j] + k;
-    if (k + chunk * 16 >= p.K) g = g_fp8_zeros;
-    dma_block(g, base + slot * Tile::kStage + (wave * Tile::kLoads + j) * kBlockBytes);
+  for (int j = 0; j < Tile::kLoads; ++j)
+    off[j] = (uint32_t)min((block0 + j) * 8 + (lane >> 3), rows - 1) * (uint32_t)ld +
+             (uint32_t)(chunk0 ^ ((j & 1) << 2)) * 16;
+  const uint8_t* g = (load_a ? p.A : p.B) + row0 * ld + (int64_t)first * kFp8StageK;
+  // Bytes of K in the tile's last stage, and what a lane past them subtracts
+  // in even and odd blocks.
+  const int tail = min(kFp8StageK, p.K - (first + count - 1) * kFp8StageK);
+  uint32_t shift[2] = {0, 0};
+  const uint32_t mine = base + wave * Tile::kLoads * kBlockBytes;
+  auto load = [&](int slot, int j) {
+    dma_block_at(g, off[j] - shift[j & 1], mine + slot * Tile::kStage + j * kBlockBytes);
   };
-  const uint8_t* frag_a = &ring[0][0] + (wm * FM * 32 + li) * 64;
-  const uint8_t* frag_b = &ring[0][0] + (Tile::kRowsA + wn * FN * 32 + li) * 64;
-  const int x0 = (lh ^ ((li >> 2) & 3)) * 16, x1 = ((2 + lh) ^ ((li >> 2) & 3)) * 16;
-  auto read = [&](const uint8_t* row) {
-    return join(*reinterpret_cast<const u32x4*>(row + x0), *reinterpret_cast<const u32x4*>(row + x1));
+  int fetched = 0;  // stage that the next loads fetch
+  auto at_last = [&]() {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int at = (chunk0 ^ (e << 2)) * 16;
+      shift[e] = at >= tail ? at : 0;
+    }
+  };
+  if (count == 1) at_last();
+  auto advance = [&]() {
+    if (fetched < count - 1) {
+      ++fetched;
+      g += kFp8StageK;
+      if (fetched == count - 1) at_last();
+    }
+  };
+  // Row 32 i + li of a wave's rows: (r >> 1) & 7 is (li >> 1) & 7 for every i.
+  const uint8_t* frag_a = &ring[0][0] + (wm * FM * 32 + li) * kFp8StageK;
+  const uint8_t* frag_b = &ring[0][0] + (Tile::kRowsA + wn * FN * 32 + li) * kFp8StageK;
+  int place[2][2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) place[t][e] = ((4 * t + 2 * e + lh) ^ ((li >> 1) & 7)) * 16;
+  auto read = [&](const uint8_t* row, int t) {
+    return join(*reinterpret_cast<const u32x4*>(row + place[t][0]),
+                *reinterpret_cast<const u32x4*>(row + place[t][1]));
   };
 
   f32x16 acc[FM][FN];
@@ -205,58 +248,71 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_fp8_tile_kernel(Fp8
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
 
-  const int ahead = min(count, S);
-  for (int g = 0; g < ahead; ++g)
+  for (int i = 0; i < S; ++i) {
 #pragma unroll
-    for (int j = 0; j < Tile::kLoads; ++j) load(g, g, j);
-  if (ahead == S) wait_vmcnt<(S - 1) * Tile::kLoads>();
-  else wait_vmcnt<0>();
+    for (int j = 0; j < Tile::kLoads; ++j) load(i, j);
+    advance();
+  }
+  wait_vmcnt<(S - 1) * Tile::kLoads>();
   __syncthreads();
   i32x8 fa[2][FM], fb[2][FN];
 #pragma unroll
-  for (int i = 0; i < FM; ++i) fa[0][i] = read(frag_a + i * 2048);
+  for (int i = 0; i < FM; ++i) fa[0][i] = read(frag_a + i * 32 * kFp8StageK, 0);
 #pragma unroll
-  for (int j = 0; j < FN; ++j) fb[0][j] = read(frag_b + j * 2048);
+  for (int j = 0; j < FN; ++j) fb[0][j] = read(frag_b + j * 32 * kFp8StageK, 0);
 
-  int slot = 0;
-  auto stage = [&](int ks, i32x8 (&a)[FM], i32x8 (&b)[FN], i32x8 (&na)[FM], i32x8 (&nb)[FN]) {
-    // This wave's loads of stage ks + 1 have landed: at most those of the
-    // stages ks + 2 .. ks + S - 1 are younger. Near the end fewer were issued.
-    if (ks + S <= count) wait_vmcnt<(S - 2) * Tile::kLoads>();
-    else wait_vmcnt<0>();
-    wait_lgkmcnt0();
-    __syncthreads();
-    const int next = slot + 1 == S ? 0 : slot + 1;
-    const bool fill = ks + S < count;
-    const uint8_t* sa = frag_a + next * Tile::kStage;
-    const uint8_t* sb = frag_b + next * Tile::kStage;
+  // The MFMAs of step T on its fragments, with the reads of the next step's
+  // (`ahead` picks its slot) and, in the second step, the loads into `slot`.
+  auto step = [&](auto T, int slot, int ahead) {
+    constexpr int t = decltype(T)::value;
+    i32x8(&a)[FM] = fa[t];
+    i32x8(&b)[FN] = fb[t];
+    i32x8(&na)[FM] = fa[t ^ 1];
+    i32x8(&nb)[FN] = fb[t ^ 1];
+    const uint8_t* sa = frag_a + ahead * Tile::kStage;
+    const uint8_t* sb = frag_b + ahead * Tile::kStage;
+    constexpr int kBlocks = FM * FN, kReads = FM + FN;
+#pragma unroll
+    for (int at = 0; at < kBlocks; ++at) {
+      const int i = at / FN, j = at % FN;
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[i], b[j], acc[i][j], 0, 0, 0, 0,
+                                                                  0, 0);
+#pragma unroll
+      for (int f = at * kReads / kBlocks; f < (at + 1) * kReads / kBlocks; ++f) {
+        if (f < FM) na[f] = read(sa + f * 32 * kFp8StageK, t ^ 1);
+        else nb[f - FM] = read(sb + (f - FM) * 32 * kFp8StageK, t ^ 1);
+      }
+      if constexpr (t == 1) {
+#pragma unroll
+        for (int l = at * Tile::kLoads / kBlocks; l < (at + 1) * Tile::kLoads / kBlocks; ++l)
+          load(slot, l);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  auto zero_past = [&](i32x8(&a)[FM], int t) {
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        constexpr int kBlocks = FM * FN;
-        const int at = i * FN + j;
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[i], b[j], acc[i][j], 0, 0, 0,
-                                                                    0, 0, 0);
-        // After the last stage these reads take a slot nobody uses.
-#pragma unroll
-        for (int f = at * (FM + FN) / kBlocks; f < (at + 1) * (FM + FN) / kBlocks; ++f) {
-          if (f < FM) na[f] = read(sa + f * 2048);
-          else nb[f - FM] = read(sb + (f - FM) * 2048);
-        }
-#pragma unroll
-        for (int l = at * Tile::kLoads / kBlocks; l < (at + 1) * Tile::kLoads / kBlocks; ++l)
-          if (fill) load(ks + S, slot, l);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    slot = next;
+      for (int e = 0; e < 8; ++e)
+        if ((4 * t + 2 * (e >> 2) + lh) * 16 >= tail) a[i][e] = 0;
   };
-  int ks = 0;
-  for (; ks + 1 < count; ks += 2) {
-    stage(ks, fa[0], fb[0], fa[1], fb[1]);
-    stage(ks + 1, fa[1], fb[1], fa[0], fb[0]);
+  int slot = 0;
+  for (int ks = 0; ks < count; ++ks) {
+    const bool cut = ks == count - 1 && tail < kFp8StageK;
+    const int next = slot + 1 == S ? 0 : slot + 1;
+    if (cut) zero_past(fa[0], 0);
+    step(Step<0>{}, slot, slot);
+    // At most the loads of the stages ks + 2 .. ks + S - 1 are younger than
+    // those of stage ks + 1.
+    wait_vmcnt<(S - 2) * Tile::kLoads>();
+    wait_lgkmcnt0();
+    __syncthreads();
+    if (cut) zero_past(fa[1], 1);
+    step(Step<1>{}, slot, next);   // after the last stage it reads a slot nobody uses
+    advance();
+    slot = next;
   }
-  if (ks < count) stage(ks, fa[0], fb[0], fa[1], fb[1]);
   wait_vmcnt<0>();
 
   // As in the 16-bit GEMM's epilogue: the wave sleeps once before the first
@@ -327,7 +383,7 @@ struct Fp8Plan {
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K) {
-  Fp8Plan c{kSkinny, 0, 0, 1, ceil_div(K, 64)};
+  Fp8Plan c{kSkinny, 0, 0, 1, ceil_div(K, kFp8StageK)};
   if (M <= 64) return c;
   const int64_t big = (int64_t)ceil_div(M, 256) * ceil_div(N, 256);
   const int tile = big >= 256 ? 256 : 128;
@@ -335,11 +391,11 @@ Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K) {
   c.tiles_m = ceil_div(M, tile);
   c.tiles_n = ceil_div(N, tile);
   if (tile == 128) {
-    // Fill the 512 places for workgroups (two a CU) by splitting K, 8 stages a
+    // Fill the 512 places for workgroups (two a CU) by splitting K, 4 stages a
     // split at least.
     const int64_t tiles = (int64_t)c.tiles_m * c.tiles_n;
     int splits = (int)(512 / tiles);
-    splits = splits < c.steps / 8 ? splits : c.steps / 8;
+    splits = splits < c.steps / 4 ? splits : c.steps / 4;
     splits = splits > 16 ? 16 : splits;
     if (splits > 1) {
       const int per = ceil_div(c.steps, splits);
@@ -365,10 +421,10 @@ hipError_t launch_fp8_out(const Fp8Params& p, Fp8Kind kind, hipStream_t stream) 
   }
   const int64_t items = (int64_t)p.tiles_m * p.tiles_n * p.splits;
   if (kind == kTile256)
-    hipLaunchKernelGGL((gemm_fp8_tile_kernel<4, 4, 2, 2, 4, 1, OUT>), long_grid(items), dim3(256), 0,
+    hipLaunchKernelGGL((gemm_fp8_tile_kernel<4, 2, 2, 4, 2, 1, OUT>), long_grid(items), dim3(512), 0,
                        stream, p);
   else
-    hipLaunchKernelGGL((gemm_fp8_tile_kernel<2, 2, 2, 2, 4, 2, OUT>), long_grid(items), dim3(256), 0,
+    hipLaunchKernelGGL((gemm_fp8_tile_kernel<2, 2, 2, 2, 2, 2, OUT>), long_grid(items), dim3(256), 0,
                        stream, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;

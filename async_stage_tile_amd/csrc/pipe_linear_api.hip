@@ -16,6 +16,9 @@ bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(
 // bytes (row counts are at most 2^31 - 1).
 bool pitch_fits(int64_t ld) { return ld <= int64_t(1) << 28; }
 
+// The e4m3 product's kernels reach the 256 rows of a tile by 32-bit offsets.
+constexpr int64_t kFp8PitchEnd = int64_t(1) << 24;
+
 pipe_status_t hip_status(hipError_t e) { return e == hipSuccess ? PIPE_OK : PIPE_ERR_HIP; }
 
 bool is16(pipe_dtype_t t) { return t == PIPE_BF16 || t == PIPE_FP16; }
@@ -159,7 +162,7 @@ pipe_status_t pipe_gemm_fp8(const void* A, const float* a_scales, const void* B,
   size_t need = 0;
   const pipe_status_t s = pipe_gemm_fp8_workspace_bytes(M, N, K, &need);
   if (s != PIPE_OK) return s;
-  if (lda < K || ldb < K || ldc < N || !pitch_fits(lda) || !pitch_fits(ldb) || !pitch_fits(ldc))
+  if (lda < K || ldb < K || ldc < N || lda >= kFp8PitchEnd || ldb >= kFp8PitchEnd || !pitch_fits(ldc))
     return PIPE_ERR_SHAPE;
   if (M == 0 || N == 0) return PIPE_OK;
   if (C == nullptr) return PIPE_ERR_NULL;

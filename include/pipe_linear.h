@@ -83,8 +83,8 @@ pipe_status_t pipe_gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K, siz
  * e4m3, the sum in fp32, C in PIPE_BF16, PIPE_FP16 or PIPE_FP32.
  *   N % 8 == 0, K % 16 == 0, M arbitrary (else PIPE_ERR_SHAPE); M == 0 or
  *   N == 0 is a no-op, K == 0 gives C = 0 (scales unread). A, B, C bases
- *   16-byte aligned, lda and ldb multiples of 16, ldc a multiple of 8, scales
- *   4-byte and the workspace 16-byte aligned (else PIPE_ERR_ALIGN). */
+ *   16-byte aligned, lda and ldb multiples of 16 and below 2^24 (else
+ *   PIPE_ERR_SHAPE), ldc a multiple of 8, scales 4-byte and the workspace 16-byte aligned (else PIPE_ERR_ALIGN). */
 pipe_status_t pipe_gemm_fp8(const void* A, const float* a_scales, const void* B,
                             const float* b_scales, void* C, int64_t M, int64_t N, int64_t K,
                             int64_t lda, int64_t ldb, int64_t ldc, pipe_dtype_t out_type,
