@@ -134,6 +134,20 @@ __device__ __forceinline__ void dma_block_at(const uint8_t* base, uint32_t offse
 }
 
 constexpr int kFp8StageK = 128;
+constexpr int kFp8Staging = 4096;   // bytes of a wave's part of the epilogue
+
+template <int OUT>
+struct Out16;
+template <>
+struct Out16<0> {
+  using type = __bf16;
+};
+template <>
+struct Out16<1> {
+  using type = _Float16;
+};
+// Four floats at any 4-byte boundary.
+typedef float f32x4_by4 __attribute__((ext_vector_type(4), aligned(4)));
 
 template <int T>
 struct Step {
@@ -149,7 +163,7 @@ struct Fp8Tile {
   static constexpr int kStage = (kRowsA + kRowsB) * kFp8StageK;
   static_assert((kBlocksA + kBlocksB) % kWaves == 0 && kBlocksA % kLoads == 0 && kLoads % 2 == 0,
                 "a wave loads whole blocks of one operand, an even number");
-  static_assert(S * kStage <= 163840, "the ring fits");
+  static_assert(S * kStage + kWaves * kFp8Staging <= 163840, "the ring and the staging fit");
 };
 
 // Output tile and K range of a work item. Workgroups go to the 8 XCDs in turn:
@@ -175,57 +189,62 @@ template <int FM, int FN, int WM, int WN, int S, int PER_CU, int OUT>
 __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_fp8_tile_kernel(Fp8Params p) {
   using Tile = Fp8Tile<FM, FN, WM, WN, S>;
   __shared__ __align__(1024) uint8_t ring[S][Tile::kStage];
+  __shared__ __align__(1024) uint8_t staging[Tile::kWaves][kFp8Staging];
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int lane = lane_id();
   const int li = lane & 31, lh = lane >> 5;
   const int wm = wave / WN, wn = wave % WN;
   const uint32_t base = uniform(lds_addr(&ring[0][0]));
   const int items = p.tiles_m * p.tiles_n * p.splits;  // < 2^31, checked by the host
-  const int64_t wg = long_block();
-  if (wg >= items) return;
-  int tm, tn, split;
-  fp8_item(p, (int)wg, items, tm, tn, split);
   const int per = (p.steps + p.splits - 1) / p.splits;
-  const int first = split * per;
-  const int count = min(per, p.steps - first);   // >= 1: the host leaves no split empty
 
-  // This wave's blocks of a stage: kLoads of A's, or of B's.
+  // The stream of stages that this wave fetches, over all the workgroup's
+  // items: kLoads blocks of A's, or of B's, a stage.
   const bool load_a = wave * Tile::kLoads < Tile::kBlocksA;
   const int block0 = wave * Tile::kLoads - (load_a ? 0 : Tile::kBlocksA);
-  const int row0 = load_a ? tm * Tile::kRowsA : tn * Tile::kRowsB;
   const int64_t ld = load_a ? p.lda : p.ldb;
-  const int rows = (load_a ? p.M : p.N) - row0;   // rows of the tile, and more
+  const uint32_t mine = base + wave * Tile::kLoads * kBlockBytes;
   // In block j, lane l loads the chunk that lies at place l % 8 of row l / 8.
   const int chunk0 = (lane & 7) ^ (lane >> 4) ^ ((block0 & 1) << 2);
-  uint32_t off[Tile::kLoads];
-#pragma unroll
-  for (int j = 0; j < Tile::kLoads; ++j)
-    off[j] = (uint32_t)min((block0 + j) * 8 + (lane >> 3), rows - 1) * (uint32_t)ld +
-             (uint32_t)(chunk0 ^ ((j & 1) << 2)) * 16;
-  const uint8_t* g = (load_a ? p.A : p.B) + row0 * ld + (int64_t)first * kFp8StageK;
-  // Bytes of K in the tile's last stage, and what a lane past them subtracts
-  // in even and odd blocks.
-  const int tail = min(kFp8StageK, p.K - (first + count - 1) * kFp8StageK);
-  uint32_t shift[2] = {0, 0};
-  const uint32_t mine = base + wave * Tile::kLoads * kBlockBytes;
-  auto load = [&](int slot, int j) {
-    dma_block_at(g, off[j] - shift[j & 1], mine + slot * Tile::kStage + j * kBlockBytes);
-  };
-  int fetched = 0;  // stage that the next loads fetch
-  auto at_last = [&]() {
+  int f_item = (int)blockIdx.x, f_stage, f_last;   // the item and stage that the next loads fetch
+  const uint8_t* g;
+  uint32_t off[Tile::kLoads], shift[2];
+  auto set_shift = [&](int tail) {   // tail: bytes of K in the stage
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int at = (chunk0 ^ (e << 2)) * 16;
       shift[e] = at >= tail ? at : 0;
     }
   };
-  if (count == 1) at_last();
+  int f_k = 0;
+  auto open = [&]() {
+    int tm, tn, split;
+    fp8_item(p, f_item, items, tm, tn, split);
+    const int row0 = load_a ? tm * Tile::kRowsA : tn * Tile::kRowsB;
+    const int rows = (load_a ? p.M : p.N) - row0;   // rows of the tile, and more
+#pragma unroll
+    for (int j = 0; j < Tile::kLoads; ++j)
+      off[j] = (uint32_t)min((block0 + j) * 8 + (lane >> 3), rows - 1) * (uint32_t)ld +
+               (uint32_t)(chunk0 ^ ((j & 1) << 2)) * 16;
+    f_k = split * per * kFp8StageK;
+    f_stage = 0;
+    f_last = min(per, p.steps - split * per) - 1;   // >= 0: the host leaves no split empty
+    g = (load_a ? p.A : p.B) + row0 * ld + f_k;
+    set_shift(p.K - f_k);
+  };
   auto advance = [&]() {
-    if (fetched < count - 1) {
-      ++fetched;
+    if (f_stage < f_last) {
+      ++f_stage;
+      f_k += kFp8StageK;
       g += kFp8StageK;
-      if (fetched == count - 1) at_last();
+      if (f_stage == f_last) set_shift(p.K - f_k);
+    } else if (f_item + (int)gridDim.x < items) {
+      f_item += (int)gridDim.x;
+      open();
     }
+  };
+  auto load = [&](int slot, int j) {
+    dma_block_at(g, off[j] - shift[j & 1], mine + slot * Tile::kStage + j * kBlockBytes);
   };
   // Row 32 i + li of a wave's rows: (r >> 1) & 7 is (li >> 1) & 7 for every i.
   const uint8_t* frag_a = &ring[0][0] + (wm * FM * 32 + li) * kFp8StageK;
@@ -240,14 +259,7 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_fp8_tile_kernel(Fp8
                 *reinterpret_cast<const u32x4*>(row + place[t][1]));
   };
 
-  f32x16 acc[FM][FN];
-#pragma unroll
-  for (int i = 0; i < FM; ++i)
-#pragma unroll
-    for (int j = 0; j < FN; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
-
+  open();
   for (int i = 0; i < S; ++i) {
 #pragma unroll
     for (int j = 0; j < Tile::kLoads; ++j) load(i, j);
@@ -256,13 +268,11 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_fp8_tile_kernel(Fp8
   wait_vmcnt<(S - 1) * Tile::kLoads>();
   __syncthreads();
   i32x8 fa[2][FM], fb[2][FN];
-#pragma unroll
-  for (int i = 0; i < FM; ++i) fa[0][i] = read(frag_a + i * 32 * kFp8StageK, 0);
-#pragma unroll
-  for (int j = 0; j < FN; ++j) fb[0][j] = read(frag_b + j * 32 * kFp8StageK, 0);
 
+  f32x16 acc[FM][FN];
   // The MFMAs of step T on its fragments, with the reads of the next step's
-  // (`ahead` picks its slot) and, in the second step, the loads into `slot`.
+  // (`ahead` is its slot) and, in the second step, the loads into `slot`. B is
+  // the first operand: a lane then holds four neighbouring columns of C's row.
   auto step = [&](auto T, int slot, int ahead) {
     constexpr int t = decltype(T)::value;
     i32x8(&a)[FM] = fa[t];
@@ -275,7 +285,7 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_fp8_tile_kernel(Fp8
 #pragma unroll
     for (int at = 0; at < kBlocks; ++at) {
       const int i = at / FN, j = at % FN;
-      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[i], b[j], acc[i][j], 0, 0, 0, 0,
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b[j], a[i], acc[i][j], 0, 0, 0, 0,
                                                                   0, 0);
 #pragma unroll
       for (int f = at * kReads / kBlocks; f < (at + 1) * kReads / kBlocks; ++f) {
@@ -290,66 +300,129 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_fp8_tile_kernel(Fp8
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  auto zero_past = [&](i32x8(&a)[FM], int t) {
+  auto zero_past = [&](i32x8(&a)[FM], int t, int tail) {
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         if ((4 * t + 2 * (e >> 2) + lh) * 16 >= tail) a[i][e] = 0;
   };
-  int slot = 0;
-  for (int ks = 0; ks < count; ++ks) {
-    const bool cut = ks == count - 1 && tail < kFp8StageK;
-    const int next = slot + 1 == S ? 0 : slot + 1;
-    if (cut) zero_past(fa[0], 0);
-    step(Step<0>{}, slot, slot);
-    // At most the loads of the stages ks + 2 .. ks + S - 1 are younger than
-    // those of stage ks + 1.
-    wait_vmcnt<(S - 2) * Tile::kLoads>();
-    wait_lgkmcnt0();
-    __syncthreads();
-    if (cut) zero_past(fa[1], 1);
-    step(Step<1>{}, slot, next);   // after the last stage it reads a slot nobody uses
-    advance();
-    slot = next;
-  }
-  wait_vmcnt<0>();
 
-  // As in the 16-bit GEMM's epilogue: the wave sleeps once before the first
-  // accumulator is read, which was seen to come too early there.
-  __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_sleep(1);
-  __builtin_amdgcn_sched_barrier(0);
-  // Lane l holds column l % 32 and rows 8 (e / 4) + 4 (l / 32) + e % 4 of a block.
+  int slot = 0;
+  for (int item = (int)blockIdx.x; item < items; item += (int)gridDim.x) {
+    int tm, tn, split;
+    fp8_item(p, item, items, tm, tn, split);
+    const int first = split * per, count = min(per, p.steps - first);
+    const int tail = p.K - (first + count - 1) * kFp8StageK;   // bytes of K in the last stage, and more
 #pragma unroll
-  for (int i = 0; i < FM; ++i)
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const int col = tn * Tile::kRowsB + (wn * FN + j) * 32 + li;
-      const int row0 = tm * Tile::kRowsA + (wm * FM + i) * 32 + 4 * lh;
-      if (col >= p.N) continue;
-      if (p.splits > 1) {
-        float* out = p.partials + (int64_t)split * p.M * p.N + col;
+      for (int j = 0; j < FN; ++j)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int row = row0 + 8 * (e >> 2) + (e & 3);
-          if (row < p.M) out[(int64_t)row * p.N] = acc[i][j][e];
-        }
-        continue;
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+    // Read here and not with the previous item's last step: the registers are
+    // its epilogue's until now.
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+      fa[0][i] = read(frag_a + slot * Tile::kStage + i * 32 * kFp8StageK, 0);
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      fb[0][j] = read(frag_b + slot * Tile::kStage + j * 32 * kFp8StageK, 0);
+    for (int ks = 0; ks < count; ++ks) {
+      const bool cut = ks == count - 1 && tail < kFp8StageK;
+      const int next = slot + 1 == S ? 0 : slot + 1;
+      if (cut) zero_past(fa[0], 0, tail);
+      step(Step<0>{}, slot, slot);
+      // At most the loads of the stages ks + 2 .. ks + S - 1 are younger than
+      // those of stage ks + 1 (and the last item's stores: not counted, which
+      // only makes the wait longer).
+      wait_vmcnt<(S - 2) * Tile::kLoads>();
+      wait_lgkmcnt0();
+      __syncthreads();
+      if (cut) zero_past(fa[1], 1, tail);
+      step(Step<1>{}, slot, next);   // after the last stage its reads are not used
+      advance();
+      slot = next;
+    }
+
+    // As in the 16-bit GEMM's epilogue: the wave sleeps once before the first
+    // accumulator is read, which was seen to come too early there.
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_sleep(1);
+    __builtin_amdgcn_sched_barrier(0);
+    // Lane l holds row l % 32 and columns 8 (e / 4) + 4 (l / 32) + e % 4 of a
+    // block. Rows of 128 bytes go through the wave's own staging buffer, its
+    // 16-byte chunks placed as the ring's, and leave as whole cache lines,
+    // while the next item's first stages arrive.
+    // The lane is made anew for the compiler, which would else compute the
+    // epilogue's addresses before the loop and spill them.
+    int el = lane;
+    asm volatile("" : "+v"(el));
+    const int eli = el & 31, elh = el >> 5;
+    uint8_t* mid = &staging[wave][0];
+    const int row0 = tm * Tile::kRowsA + wm * FM * 32, col0 = tn * Tile::kRowsB + wn * FN * 32;
+    const int wrow = eli * 128, wswz = (eli >> 1) & 7;
+    auto flush = [&](uint8_t* out, int64_t pitch, int row, int col, int per_chunk) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = 8 * k + (el >> 3), c = (el & 7) ^ ((r >> 1) & 7);
+        const u32x4 v = *reinterpret_cast<const u32x4*>(mid + r * 128 + (el & 7) * 16);
+        if (row + r < p.M && col + c * per_chunk < p.N)
+          *reinterpret_cast<u32x4*>(out + (row + r) * pitch + (int64_t)col * (16 / per_chunk) + c * 16) = v;
       }
-      const float sb = p.b_scales[col];
+    };
+    auto block32 = [&](int i, int j, float sa, const f32x4(&sb)[4], uint8_t* out, int64_t pitch) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int row = row0 + 8 * (e >> 2) + (e & 3);
-        if (row < p.M) {
-          const float v = acc[i][j][e] * p.a_scales[row] * sb;
-          const int64_t at = (int64_t)row * p.ldc + col;
-          if constexpr (OUT == 0) static_cast<__bf16*>(p.C)[at] = (__bf16)v;
-          else if constexpr (OUT == 1) static_cast<_Float16*>(p.C)[at] = (_Float16)v;
-          else static_cast<float*>(p.C)[at] = v;
-        }
+      for (int q = 0; q < 4; ++q) {
+        f32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e] * sa * sb[q][e];
+        *reinterpret_cast<f32x4*>(mid + wrow + ((2 * q + elh) ^ wswz) * 16) = v;
+      }
+      flush(out, pitch, row0 + 32 * i, col0 + 32 * j, 4);
+    };
+    if (p.splits > 1) {
+      const f32x4 one = {1.f, 1.f, 1.f, 1.f};
+      const f32x4 ones[4] = {one, one, one, one};
+      uint8_t* out = reinterpret_cast<uint8_t*>(p.partials + (int64_t)split * p.M * p.N);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) block32(i, j, 1.f, ones, out, (int64_t)p.N * 4);
+      continue;
+    }
+    f32x4 sb[FN][4];
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        sb[j][q] = *reinterpret_cast<const f32x4_by4*>(
+            p.b_scales + min(col0 + 32 * j + 8 * q + 4 * elh, p.N - 4));
+    uint8_t* out = static_cast<uint8_t*>(p.C);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const float sa = p.a_scales[min(row0 + 32 * i + eli, p.M - 1)];
+      if constexpr (OUT == 2) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) block32(i, j, sa, sb[j], out, p.ldc * 4);
+      } else {
+        static_assert(FN == 2, "a wave's row of 16-bit values is 128 bytes");
+        using T = typename Out16<OUT>::type;
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            f32x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e] * sa * sb[j][q][e];
+            *reinterpret_cast<u32x2*>(mid + wrow + ((4 * j + q) ^ wswz) * 16 + elh * 8) =
+                u32x2{Pair<T>::pack(v[0], v[1]), Pair<T>::pack(v[2], v[3])};
+          }
+        flush(out, p.ldc * 2, row0 + 32 * i, col0, 8);
       }
     }
+  }
+  wait_vmcnt<0>();
 }
 
 // Sum of the splits' partial products in split order, scaled and rounded: four
@@ -419,13 +492,13 @@ hipError_t launch_fp8_out(const Fp8Params& p, Fp8Kind kind, hipStream_t stream) 
       hipLaunchKernelGGL((gemm_fp8_skinny_kernel<4, 2, 8, OUT>), grid(4, 2), dim3(512), 0, stream, p);
     return hipGetLastError();
   }
-  const int64_t items = (int64_t)p.tiles_m * p.tiles_n * p.splits;
+  const int items = p.tiles_m * p.tiles_n * p.splits;
   if (kind == kTile256)
-    hipLaunchKernelGGL((gemm_fp8_tile_kernel<4, 2, 2, 4, 2, 1, OUT>), long_grid(items), dim3(512), 0,
-                       stream, p);
+    hipLaunchKernelGGL((gemm_fp8_tile_kernel<4, 2, 2, 4, 2, 1, OUT>), dim3(items < 256 ? items : 256),
+                       dim3(512), 0, stream, p);
   else
-    hipLaunchKernelGGL((gemm_fp8_tile_kernel<2, 2, 2, 2, 2, 2, OUT>), long_grid(items), dim3(256), 0,
-                       stream, p);
+    hipLaunchKernelGGL((gemm_fp8_tile_kernel<2, 2, 2, 2, 2, 2, OUT>), dim3(items < 512 ? items : 512),
+                       dim3(256), 0, stream, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   const int64_t quads = (int64_t)p.M * (p.N / 4);
