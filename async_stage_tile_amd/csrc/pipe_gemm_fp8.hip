@@ -52,32 +52,46 @@ __global__ void __launch_bounds__(64 * WAVES) gemm_fp8_skinny_kernel(Fp8Params p
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  const int steps = (p.K + 127) >> 7;
-#pragma unroll 4
-  for (int st = wave; st < steps; st += WAVES) {
-    const int k0 = st << 7;
-    const bool in0 = k0 + 16 * lq < p.K, in1 = k0 + 64 + 16 * lq < p.K;
-    i32x8 b[NT], a[MT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      u32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
-      if (in0) lo = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(b_row[j] + k0));
-      if (in1) hi = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(b_row[j] + k0 + 64));
-      b[j] = join(lo, hi);
-    }
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      u32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
-      if (in0) lo = *reinterpret_cast<const u32x4*>(a_row[i] + k0);
-      if (in1) hi = *reinterpret_cast<const u32x4*>(a_row[i] + k0 + 64);
-      a[i] = join(lo, hi);
-    }
+  const auto use = [&](i32x8(&b)[NT], i32x8(&a)[MT]) {
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int i = 0; i < MT; ++i)
         acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j], a[i], acc[j][i], 0, 0, 0,
                                                                      0, 0, 0);
+  };
+  const int full = p.K >> 7;
+#pragma unroll 4
+  for (int st = wave; st < full; st += WAVES) {
+    const int k0 = st << 7;
+    i32x8 b[NT], a[MT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      b[j] = join(__builtin_nontemporal_load(reinterpret_cast<const u32x4*>(b_row[j] + k0)),
+                  __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(b_row[j] + k0 + 64)));
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+      a[i] = join(*reinterpret_cast<const u32x4*>(a_row[i] + k0),
+                  *reinterpret_cast<const u32x4*>(a_row[i] + k0 + 64));
+    use(b, a);
+  }
+  if ((p.K & 127) != 0 && wave == full % WAVES) {
+    // Lanes past K read the row's chunk 0 of the step; A's is zeroed.
+    const int k0 = full << 7, left = p.K - k0;
+    const int at0 = 16 * lq < left ? 0 : -16 * lq, at1 = 64 + 16 * lq < left ? 64 : -16 * lq;
+    const u32x4 zero4 = {0, 0, 0, 0};
+    i32x8 b[NT], a[MT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      b[j] = join(*reinterpret_cast<const u32x4*>(b_row[j] + k0 + at0),
+                  *reinterpret_cast<const u32x4*>(b_row[j] + k0 + at1));
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const u32x4 lo = *reinterpret_cast<const u32x4*>(a_row[i] + k0 + at0);
+      const u32x4 hi = *reinterpret_cast<const u32x4*>(a_row[i] + k0 + at1);
+      a[i] = join(16 * lq < left ? lo : zero4, 64 + 16 * lq < left ? hi : zero4);
+    }
+    use(b, a);
   }
 #pragma unroll
   for (int j = 0; j < NT; ++j)

@@ -96,12 +96,42 @@ __device__ __forceinline__ u32x4 transpose_quarters(u32x4 w) {
   return u32x4{c[0], d[0], c[1], d[1]};
 }
 
+// Scales and zero points of the groups of one block, at any alignment.
+template <int N>
+struct Packed;
+template <>
+struct Packed<1> {
+  typedef uint16_t scales;
+  typedef uint8_t zeros;
+};
+template <>
+struct Packed<2> {
+  typedef uint16_t scales __attribute__((ext_vector_type(2), aligned(2)));
+  typedef uint8_t zeros __attribute__((ext_vector_type(2), aligned(1)));
+};
+template <>
+struct Packed<4> {
+  typedef uint16_t scales __attribute__((ext_vector_type(4), aligned(2)));
+  typedef uint8_t zeros __attribute__((ext_vector_type(4), aligned(1)));
+};
+
+// What a wave holds of one block of 128 k's.
+template <int MT, int NT, int FLUSHES>
+struct Block {
+  u32x4 w[NT];
+  u32x4 a[MT][4];
+  uint16_t s[NT][FLUSHES];
+  uint8_t z[NT][FLUSHES];
+};
+
 // MT, NT: 16-row tiles of A and of the weights that a wave holds. WAVES split
 // K. F: k's between two scalings, the group size or 128 if that is larger.
+// Rows past M and N are read from the last row and dropped.
 template <class T, int MT, int NT, int WAVES, int F, bool ZEROS>
 __global__ void __launch_bounds__(64 * WAVES) gemm_w4_kernel(W4Params p) {
   constexpr int kFlushes = 128 / F;   // scalings in a block
   constexpr int kTiles = MT * NT;
+  using Blk = Block<MT, NT, kFlushes>;
   __shared__ f32x4 red[WAVES][kTiles][64];
   const int lane = (int)(threadIdx.x & 63);
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -117,66 +147,75 @@ __global__ void __launch_bounds__(64 * WAVES) gemm_w4_kernel(W4Params p) {
   const uint8_t* zero_row[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    const int n = min(n0 + 16 * j + li, p.N - 1);   // columns past N are computed and dropped
-    code_row[j] = p.codes + (int64_t)n * p.ld_codes;
+    const int n = min(n0 + 16 * j + li, p.N - 1);
+    code_row[j] = p.codes + (int64_t)n * p.ld_codes + 16 * lq;
     scale_row[j] = p.scales + (int64_t)n * p.ld_scales;
     zero_row[j] = ZEROS ? p.zeros + (int64_t)n * p.ld_zeros : nullptr;
   }
   const uint8_t* a_row[MT];
-  bool a_live[MT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int m = m0 + 16 * i + li;
-    a_live[i] = m < p.M;
-    a_row[i] = p.A + (int64_t)(a_live[i] ? m : 0) * p.lda;
-  }
+  for (int i = 0; i < MT; ++i) a_row[i] = p.A + (int64_t)min(m0 + 16 * i + li, p.M - 1) * p.lda;
   f32x4 acc[MT][NT];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   const u32x4 ones = {Mma<T>::kOnes, Mma<T>::kOnes, Mma<T>::kOnes, Mma<T>::kOnes};
-  const u32x4 zero4 = {0, 0, 0, 0};
 
-  const int blocks = (p.K + 127) >> 7;
-#pragma unroll 2
-  for (int b = wave; b < blocks; b += WAVES) {
-    const int k0 = b << 7;
-    u32x4 w[NT];
-    float s[NT][kFlushes], z[NT][kFlushes];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      w[j] = zero4;
-      if (k0 + 32 * lq < p.K)
-        w[j] = __builtin_nontemporal_load(
-            reinterpret_cast<const u32x4*>(code_row[j] + (k0 >> 1) + 16 * lq));
-    }
+  // A's k's of MFMA step t in this lane.
+  const auto a_k = [&](int t) { return F < 128 ? 32 * t + 8 * lq : 32 * lq + 8 * t; };
+  const auto load = [&](Blk& blk, int k0) {
 #pragma unroll
     for (int j = 0; j < NT; ++j)
+      blk.w[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(code_row[j] + (k0 >> 1)));
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int g = k0 >> p.group_shift;
+      using P = Packed<kFlushes>;
+      *reinterpret_cast<typename P::scales*>(&blk.s[j]) =
+          *reinterpret_cast<const typename P::scales*>(scale_row[j] + g);
+      if constexpr (ZEROS)
+        *reinterpret_cast<typename P::zeros*>(&blk.z[j]) =
+            *reinterpret_cast<const typename P::zeros*>(zero_row[j] + g);
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        blk.a[i][t] = *reinterpret_cast<const u32x4*>(a_row[i] + 2 * (int64_t)(k0 + a_k(t)));
+  };
+  // The last block of a K that is no multiple of 128: addresses stay in the
+  // row, and A and the scales are zeros past K.
+  const auto load_tail = [&](Blk& blk, int k0) {
+    const u32x4 zero4 = {0, 0, 0, 0};
+    const int back = k0 + 32 * lq < p.K ? 0 : 16 * lq;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      blk.w[j] = *reinterpret_cast<const u32x4*>(code_row[j] + (k0 >> 1) - back);
 #pragma unroll
       for (int f = 0; f < kFlushes; ++f) {
-        const int k = k0 + f * F;
-        const int g = k >> p.group_shift;
-        s[j][f] = 0.f;
-        z[j][f] = 8.f;
-        if (k < p.K) {
-          s[j][f] = Mma<T>::to_float(scale_row[j][g]);
-          if constexpr (ZEROS) z[j][f] = (float)zero_row[j][g];
-        }
+        const int k = k0 + f * F, g = min(k, p.K - 1) >> p.group_shift;
+        blk.s[j][f] = k < p.K ? scale_row[j][g] : 0;
+        if constexpr (ZEROS) blk.z[j][f] = zero_row[j][g];
       }
-    u32x4 a[MT][4];
+    }
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const int k = k0 + (F < 128 ? 32 * t + 8 * lq : 32 * lq + 8 * t);
-        a[i][t] = zero4;
-        if (a_live[i] && k < p.K)
-          a[i][t] = even_odd(*reinterpret_cast<const u32x4*>(a_row[i] + 2 * (int64_t)k));
+        const int k = k0 + a_k(t);
+        const u32x4 v = *reinterpret_cast<const u32x4*>(a_row[i] + 2 * (int64_t)min(k, p.K - 8));
+        blk.a[i][t] = k < p.K ? v : zero4;
       }
+  };
+  const auto compute = [&](Blk& blk) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) blk.a[i][t] = even_odd(blk.a[i][t]);
     if constexpr (F < 128) {
 #pragma unroll
-      for (int j = 0; j < NT; ++j) w[j] = transpose_quarters(w[j]);
+      for (int j = 0; j < NT; ++j) blk.w[j] = transpose_quarters(blk.w[j]);
     }
 #pragma unroll
     for (int f = 0; f < kFlushes; ++f) {
@@ -190,22 +229,46 @@ __global__ void __launch_bounds__(64 * WAVES) gemm_w4_kernel(W4Params p) {
 #pragma unroll
       for (int t = f * (F / 32); t < (f + 1) * (F / 32); ++t) {
 #pragma unroll
-        for (int i = 0; i < MT; ++i) sum[i] = Mma<T>::mfma(a[i][t], ones, sum[i]);
+        for (int i = 0; i < MT; ++i) sum[i] = Mma<T>::mfma(blk.a[i][t], ones, sum[i]);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          const u32x4 q = expand<T>(w[j][t]);
+          const u32x4 q = expand<T>(blk.w[j][t]);
 #pragma unroll
-          for (int i = 0; i < MT; ++i) part[i][j] = Mma<T>::mfma(a[i][t], q, part[i][j]);
+          for (int i = 0; i < MT; ++i) part[i][j] = Mma<T>::mfma(blk.a[i][t], q, part[i][j]);
         }
       }
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+      for (int j = 0; j < NT; ++j) {
+        const float s = Mma<T>::to_float(blk.s[j][f]);
+        const float z = ZEROS ? (float)blk.z[j][f] : 8.f;
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            acc[i][j][e] += s[j][f] * (part[i][j][e] - z[j][f] * sum[i][e]);
+          for (int e = 0; e < 4; ++e) acc[i][j][e] += s * (part[i][j][e] - z * sum[i][e]);
+      }
     }
+  };
+  // A block's loads go out before the block ahead of it is used.
+  const int full = p.K >> 7;
+  int b = wave;
+  if (b < full) {
+    Blk x, y;
+    load(x, b << 7);
+    for (;;) {
+      b += WAVES;
+      if (b < full) load(y, b << 7);
+      compute(x);
+      if (b >= full) break;
+      b += WAVES;
+      if (b < full) load(x, b << 7);
+      compute(y);
+      if (b >= full) break;
+    }
+  }
+  if ((p.K & 127) != 0 && wave == full % WAVES) {
+    Blk x;
+    load_tail(x, full << 7);
+    compute(x);
   }
 #pragma unroll
   for (int i = 0; i < MT; ++i)
