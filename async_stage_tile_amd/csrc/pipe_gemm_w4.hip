@@ -1,14 +1,9 @@
 // Products of 16-bit rows with 4-bit weights: C = A ((q - z) s)^T, a scale and
 // a zero point for each group of K.
 //
-// For up to 64 rows the call is bound by reading the weights once: N K / 2
-// bytes of codes, for a few operations each. So the codes go from memory
-// straight into registers, 16 bytes (32 codes) a lane, become 16-bit integers
-// there, and enter v_mfma_f32_16x16x32 with the rows of A as the other
-// operand. The waves of a workgroup share 16 NT weight rows and split K
-// between them in blocks of 128, each next block going to the next wave, so
-// that the workgroup as a whole reads long runs of each row; their sums meet
-// in LDS at the end, in wave order.
+// For a few rows the call is bound by reading the weights once: N K / 2 bytes
+// of codes, for a few operations each. One to four rows of A meet them on the
+// vector units (gemv_w4_kernel); more rows on the MFMAs (gemm_w4_tile_kernel).
 //
 // Integers: a byte 0..15 is, read as e4m3, q * 2^-9 (the subnormals and the
 // first binade are evenly spaced), so one v_cvt_scalef32_pk with scale 2^9
@@ -16,18 +11,10 @@
 // shift and masks included.
 //
 // Scales and zero points: over one group (q - z) s = s q - s z, so with
-// P = sum_k a q and S = sum_k a of the group, acc += s P - (s z) S. P is the
-// MFMA's sum over the group and S that of one more MFMA, against ones, that
-// the wave's NT column tiles share. Everything is exact or fp32; no weight is
+// P = sum_k a q and S = sum_k a of the group, acc += s (P - z S). On the MFMAs S
+// is one more product, against ones. Everything is exact or fp32; no weight is
 // rounded to 16 bits.
-//
-// K order: within a lane's 8 codes of an MFMA the order is even k's, then odd
-// (as the masks leave them), and A's pairs are permuted alike. Over the lanes,
-// groups of 128 and more take a lane's four words as they come: word t of
-// quarter q (16 lanes) holds k = 32 q + 8 t .. + 7, and A's lanes load that.
-// Smaller groups need every MFMA inside 32 consecutive k's: the words of the
-// four quarters are transposed first (two 16-lane and two 32-lane swaps), after
-// which word t of quarter q holds k = 32 t + 8 q .. + 7.
+#include "pipe_device.hpp"
 #include "pipe_linear.hpp"
 
 namespace pipe {
@@ -95,237 +82,260 @@ __device__ __forceinline__ u32x4 even_odd(u32x4 a) {
                __builtin_amdgcn_perm(a[3], a[2], 0x07060302u)};
 }
 
-// Word t of quarter q <- word q of quarter t.
-__device__ __forceinline__ u32x4 transpose_quarters(u32x4 w) {
-  const u32x2 a = __builtin_amdgcn_permlane16_swap(w[0], w[1], false, false);
-  const u32x2 b = __builtin_amdgcn_permlane16_swap(w[2], w[3], false, false);
-  const u32x2 c = __builtin_amdgcn_permlane32_swap(a[0], b[0], false, false);
-  const u32x2 d = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
-  return u32x4{c[0], d[0], c[1], d[1]};
+// 8 codes as 16-bit floats in their own order.
+template <class T>
+__device__ __forceinline__ u32x4 expand_in_order(uint32_t codes) {
+  const uint32_t even = codes & 0x0F0F0F0Fu, odd = (codes >> 4) & 0x0F0F0F0Fu;
+  const uint32_t lo = __builtin_amdgcn_perm(odd, even, 0x05010400u);   // k0 k1 k2 k3
+  const uint32_t hi = __builtin_amdgcn_perm(odd, even, 0x07030602u);   // k4 k5 k6 k7
+  return u32x4{Mma<T>::codes_lo(lo), Mma<T>::codes_hi(lo), Mma<T>::codes_lo(hi),
+               Mma<T>::codes_hi(hi)};
 }
 
-// MT, NT: 16-row tiles of A and of the weights that a wave holds. WAVES split
-// K into runs of blocks of 128. F: k's between two scalings, the group size or
-// 128 if that is larger. Rows of A and of the weights past the end are read
-// from the last row and dropped.
+// ---------------------------------------------------------------------------
+// Five rows of A and more. A workgroup of 8 waves computes 16 MT rows of A
+// times 128 weight rows; stages of 256 k pass through an LDS ring, filled by direct-to-LDS loads alone, so that one wait count covers a
+// stage: codes (128 rows of 128 bytes, 16-byte chunk c of row r at place
+// c ^ ((r >> 1) & 7)), A (rows of 512 bytes, chunk c of row r at
+// c ^ (r & 15)), and the scales and zero points of the stage's groups, widened
+// to 32 bits by the load. Wave (wn, kh) takes weight rows 32 wn .. + 31 and the
+// stage's half kh; with the codes of 8 k's in one LDS word, an MFMA step of 32
+// k's reads its operand as it lies: quarter q of the lanes holds
+// k = 8 q .. 8 q + 7. The halves' sums meet in LDS at the end.
 //
-// K is taken in chunks of at most kChunkGroups groups, whose scales and zero
-// points the workgroup first turns into pairs of floats in LDS: a 2-byte and a
-// 1-byte load in every block cost more than the block's codes.
+// One barrier a stage: at its top a wave's own loads of the stage have landed
+// and its reads of the stage before have returned. After the barrier that
+// holds for every wave, and the slot of the stage before takes the next one
+// that is not under way.
 //
-// Loads run ahead of their use without a second set of registers: the codes of
-// a block are followed at once by those of the block four further on. Loads
-// return in order, so a fragment of A has to be asked for as far ahead or it
-// would wait for younger codes: also four blocks with one row tile, where
-// registers allow it; with more tiles A's loads are the longer part, and each
-// fragment is followed by the next block's.
-constexpr int kChunkGroups = 128;
+// Where the tiles leave compute units idle K is split over workgroups, which
+// then write fp32 partial products for gemm_w4_join_kernel to add up in order.
+// Rows past M and N are read from the last row and dropped; of the last stage
+// only the MFMA steps and groups inside K are used, and loads past K take the
+// stage's first chunk or the last group instead.
+// ---------------------------------------------------------------------------
+template <bool B>
+struct W4Flag {
+  static constexpr bool value = B;
+};
 
-template <class T, int MT, int NT, int WAVES, int F, bool ZEROS>
-__global__ void __launch_bounds__(64 * WAVES) gemm_w4_kernel(W4Params p) {
-  constexpr int kFlushes = 128 / F;   // scalings in a block
-  constexpr int kTiles = MT * NT, kRows = 16 * NT;
-  constexpr int kAhead = MT == 1 ? 4 : 1;
-  constexpr int kPitch = kChunkGroups + 1;
-  __shared__ union {
-    f32x4 red[WAVES][kTiles][64];
-    f32x2 groups[kRows][kPitch];      // scale, zero point
-  } lds;
-  const int lane = (int)(threadIdx.x & 63);
+constexpr int kW4TileN = 128, kW4StageK = 256;
+
+template <int MT, int F>
+struct W4Tile {
+  static constexpr int kGroups = kW4StageK / F;            // groups of a stage
+  static constexpr int kCodes = kW4TileN * kW4StageK / 2;  // bytes of a slot's parts
+  static constexpr int kA = 16 * MT * kW4StageK * 2;
+  static constexpr int kScales = kGroups * kW4TileN * 4;
+  static constexpr int kSlot = kCodes + kA + 2 * kScales;
+  static constexpr int kPitch = kW4TileN + 4;              // floats of a row of sums
+  static constexpr int kSums = 16 * MT * kPitch * 4;
+  // One row tile: three slots, so that two workgroups fit a CU. More: what fits.
+  static constexpr int kSlots = MT == 1 ? 3 : 163840 / kSlot;
+  static constexpr int kLds = kSlots * kSlot > kSums ? kSlots * kSlot : kSums;
+  static constexpr int kLoads = 2 + MT + kGroups / 2;      // a wave and stage
+};
+
+template <int BYTES>
+__device__ __forceinline__ void dma_words(const void* g, uint32_t lds_base) {
+  if constexpr (BYTES == 2)
+    asm volatile("s_nop 0\n\tglobal_load_lds_ushort %0, off" : : "v"(g), "{m0}"(lds_base) : "memory");
+  else
+    asm volatile("s_nop 0\n\tglobal_load_lds_ubyte %0, off" : : "v"(g), "{m0}"(lds_base) : "memory");
+}
+
+template <class T, int MT, int F, bool ZEROS>
+__global__ void __launch_bounds__(512) gemm_w4_tile_kernel(W4Params p) {
+  using Tile = W4Tile<MT, F>;
+  __shared__ __align__(1024) uint8_t lds[Tile::kLds];
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int lane = lane_id();
   const int li = lane & 15, lq = lane >> 4;
-  // Workgroups that share weight rows are neighbours.
-  const int m_tiles = (p.M + 16 * MT - 1) / (16 * MT);
+  const int wn = wave & 3, kh = wave >> 2;
+  const uint32_t base = uniform(lds_addr(&lds[0]));
   const int64_t wg = long_block();
-  if (wg >= (int64_t)m_tiles * ((p.N + kRows - 1) / kRows)) return;
-  const int n0 = (int)(wg / m_tiles) * kRows, m0 = (int)(wg % m_tiles) * (16 * MT);
+  // Neighbours share weight rows, then lie along N.
+  const int m_tiles = (p.M + 16 * MT - 1) / (16 * MT), n_tiles = (p.N + kW4TileN - 1) / kW4TileN;
+  if (wg >= (int64_t)m_tiles * n_tiles * p.splits) return;
+  const int split = (int)(wg / ((int64_t)m_tiles * n_tiles));
+  const int tile = (int)(wg % ((int64_t)m_tiles * n_tiles));
+  const int m0 = tile % m_tiles * (16 * MT), n0 = tile / m_tiles * kW4TileN;
+  const int stages = (p.K + kW4StageK - 1) / kW4StageK;
+  const int per = (stages + p.splits - 1) / p.splits;
+  const int first = split * per, count = min(per, stages - first);   // >= 1
 
-  const uint8_t* code_row[NT];
+  // This wave's loads of a stage.
+  const uint8_t* code_src[2];
+  int code_k[2];
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
-    code_row[j] = p.codes + (int64_t)min(n0 + 16 * j + li, p.N - 1) * p.ld_codes + 16 * lq;
-  const uint8_t* a_row[MT];
+  for (int j = 0; j < 2; ++j) {
+    const int r = (wave * 2 + j) * 8 + (lane >> 3);
+    const int c = (lane & 7) ^ ((r >> 1) & 7);
+    code_src[j] = p.codes + (int64_t)min(n0 + r, p.N - 1) * p.ld_codes;
+    code_k[j] = 32 * c;
+  }
+  const uint8_t* a_src[MT];
+  int a_k[MT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) a_row[i] = p.A + (int64_t)min(m0 + 16 * i + li, p.M - 1) * p.lda;
-  f32x4 acc[MT][NT];
+  for (int j = 0; j < MT; ++j) {
+    const int r = (wave * MT + j) * 2 + (lane >> 5);
+    a_src[j] = p.A + (int64_t)min(m0 + r, p.M - 1) * p.lda;
+    a_k[j] = 8 * ((lane & 31) ^ (r & 15));
+  }
+  // Groups: waves 0-3 load scales, 4-7 zero points (or the scales again), half
+  // of the 128 rows an instruction.
+  const int64_t group_row = min(n0 + 64 * (wave & 1) + lane, p.N - 1);
+  auto load = [&](int ks, int slot) {
+    const int k0 = (first + min(ks, count - 1)) * kW4StageK;
+    const uint32_t to = base + slot * Tile::kSlot;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int k = k0 + (k0 + code_k[j] < p.K ? code_k[j] : 0);
+      dma_block_nt(code_src[j] + (k >> 1), to + (wave * 2 + j) * kBlockBytes);
+    }
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      const int k = k0 + (k0 + a_k[j] < p.K ? a_k[j] : 0);
+      dma_block(a_src[j] + 2 * (int64_t)k, to + Tile::kCodes + (wave * MT + j) * kBlockBytes);
+    }
+#pragma unroll
+    for (int j = 0; j < Tile::kGroups / 2; ++j) {
+      const int g = 2 * j + ((wave >> 1) & 1);   // this wave's groups of the stage
+      const int at = min(k0 + g * F, p.K - 1) >> p.group_shift;
+      const uint32_t word = Tile::kCodes + Tile::kA + (g * kW4TileN + 64 * (wave & 1)) * 4;
+      if (ZEROS && kh == 1)
+        dma_words<1>(p.zeros + group_row * p.ld_zeros + at, to + word + Tile::kScales);
+      else
+        dma_words<2>(p.scales + group_row * p.ld_scales + at,
+                     to + word + (kh == 1 ? Tile::kScales : 0));
+    }
+  };
+
+  f32x4 acc[MT][2];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   const u32x4 ones = {Mma<T>::kOnes, Mma<T>::kOnes, Mma<T>::kOnes, Mma<T>::kOnes};
 
-  u32x4 w[4][NT], a[kAhead][4][MT];
-  const auto load_codes = [&](int i, int b) {
+  // The 128 k's of this wave's half of a slot, of which `left` are inside K.
+  auto compute = [&](int slot, auto CUT, int left) {
+    constexpr bool cut = decltype(CUT)::value;
+    const uint8_t* codes = &lds[slot * Tile::kSlot] + (32 * wn + li) * 128 + 4 * lq;
+    const uint8_t* rows = &lds[slot * Tile::kSlot + Tile::kCodes] + li * 512;
+    const uint32_t* groups = reinterpret_cast<const uint32_t*>(
+        &lds[slot * Tile::kSlot + Tile::kCodes + Tile::kA]) + 32 * wn + li;
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-      w[i][j] = __builtin_nontemporal_load(
-          reinterpret_cast<const u32x4*>(code_row[j] + ((int64_t)b << 6)));
-  };
-  // A's k's of MFMA step t in this lane.
-  const auto a_k = [&](int t) { return F < 128 ? 32 * t + 8 * lq : 32 * lq + 8 * t; };
-  const auto load_a = [&](int i, int t, int b) {
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-      a[i][t][m] = *reinterpret_cast<const u32x4*>(a_row[m] + 2 * (((int64_t)b << 7) + a_k(t)));
-  };
-  // One block: its codes, its A fragments (`next` follows the use of step t),
-  // its groups from `at` on in the chunk.
-  const auto compute = [&](u32x4(&wb)[NT], u32x4(&ab)[4][MT], int at, auto next) {
-    if constexpr (F < 128) {
-#pragma unroll
-      for (int j = 0; j < NT; ++j) wb[j] = transpose_quarters(wb[j]);
-    }
-#pragma unroll
-    for (int f = 0; f < kFlushes; ++f) {
-      f32x4 sum[MT], part[MT][NT];
+    for (int f = 0; f < 128 / F; ++f) {
+      if (cut && f * F >= left) break;
+      f32x4 sum[MT], part[MT][2];
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         sum[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < NT; ++j) part[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < 2; ++j) part[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
 #pragma unroll
       for (int t = f * (F / 32); t < (f + 1) * (F / 32); ++t) {
-        u32x4 av[MT];
+        if (cut && 32 * t >= left) break;
+        u32x4 a[MT];
 #pragma unroll
-        for (int i = 0; i < MT; ++i) av[i] = even_odd(ab[t][i]);
-        next(t);
+        for (int i = 0; i < MT; ++i) {
+          a[i] = *reinterpret_cast<const u32x4*>(rows + i * 16 * 512 +
+                                                 ((16 * kh + 4 * t + lq) ^ li) * 16);
+          sum[i] = Mma<T>::mfma(a[i], ones, sum[i]);
+        }
 #pragma unroll
-        for (int i = 0; i < MT; ++i) sum[i] = Mma<T>::mfma(av[i], ones, sum[i]);
+        for (int j = 0; j < 2; ++j) {
+          // Row 16 j + li of the wave's: (r >> 1) & 7 is (li >> 1) & 7.
+          const uint32_t word = *reinterpret_cast<const uint32_t*>(
+              codes + j * 16 * 128 + ((4 * kh + t) ^ ((li >> 1) & 7)) * 16);
+          const u32x4 q = expand_in_order<T>(word);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const u32x4 q = expand<T>(wb[j][t]);
-#pragma unroll
-          for (int i = 0; i < MT; ++i) part[i][j] = Mma<T>::mfma(av[i], q, part[i][j]);
+          for (int i = 0; i < MT; ++i) part[i][j] = Mma<T>::mfma(a[i], q, part[i][j]);
         }
       }
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const f32x2 g = lds.groups[16 * j + li][at + f];
+      for (int j = 0; j < 2; ++j) {
+        const int at = (kh * (128 / F) + f) * kW4TileN + 16 * j;
+        const float s = Mma<T>::to_float((uint16_t)groups[at]);
+        const float z = ZEROS ? (float)(groups[Tile::kScales / 4 + at] & 0xFFu) : 8.f;
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] += g[0] * (part[i][j][e] - g[1] * sum[i][e]);
+          for (int e = 0; e < 4; ++e) acc[i][j][e] += s * (part[i][j][e] - z * sum[i][e]);
       }
     }
   };
 
-  // Chunks: equal numbers of blocks (groups of more than 128 are counted as
-  // blocks here: each block finds its own copy of the group's pair).
-  const int full = p.K >> 7, blocks = (p.K + 127) >> 7;   // whole blocks; all
-  constexpr int kMost = kChunkGroups / kFlushes;
-  const int chunks = (blocks + kMost - 1) / kMost, chunk = (blocks + chunks - 1) / chunks;
-  for (int c0 = 0; c0 < blocks; c0 += chunk) {
-    const int c1 = min(c0 + chunk, blocks);
-    const int each = (min(c1, full) - c0 + WAVES - 1) / WAVES;
-    int b = c0 + wave * each;
-    const int end = min(b + each, min(c1, full));
-    const bool work = b < end;
-
-    // This thread's part of the scales: wave r takes rows r, r + WAVES, ...,
-    // its lanes the pairs of a row.
-    const int pairs = (c1 - c0) * kFlushes;
-    uint16_t sv[2][kRows / WAVES];
-    uint8_t zv[2][kRows / WAVES];
-    static_assert(kRows % WAVES == 0 && kChunkGroups == 128, "two pairs a lane and row");
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int g = min(((c0 << 7) + (lane + 64 * h) * F), p.K - 1) >> p.group_shift;
-#pragma unroll
-      for (int r = 0; r < kRows / WAVES; ++r) {
-        const int64_t n = min(n0 + wave + r * WAVES, p.N - 1);
-        sv[h][r] = p.scales[n * p.ld_scales + g];
-        if constexpr (ZEROS) zv[h][r] = p.zeros[n * p.ld_zeros + g];
-      }
-    }
-    if (work) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        load_codes(i, min(b + i, end - 1));
-        if (i < kAhead)
-#pragma unroll
-          for (int t = 0; t < 4; ++t) load_a(i, t, min(b + i, end - 1));
-      }
-    }
-    if (c0 > 0) __syncthreads();   // the last chunk's pairs are no longer read
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int r = 0; r < kRows / WAVES; ++r)
-        if (lane + 64 * h < pairs) {
-          // Past K: zeros, which the tail's products are multiplied by.
-          const bool in = (c0 << 7) + (lane + 64 * h) * F < p.K;
-          const float s = in ? Mma<T>::to_float(sv[h][r]) : 0.f;
-          lds.groups[wave + r * WAVES][lane + 64 * h] = f32x2{s, ZEROS ? (float)zv[h][r] : 8.f};
-        }
+  for (int i = 0; i < Tile::kSlots - 1; ++i) load(i, i);
+  int slot = 0;
+  for (int ks = 0; ks < count; ++ks) {
+    wait_vmcnt<(Tile::kSlots - 2) * Tile::kLoads>();   // those of younger stages
+    wait_lgkmcnt0();
     __syncthreads();
-
-    if (work) {
-      for (; b + 4 < end; b += 4) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int far = min(b + i + 4, end - 1);
-          if constexpr (kAhead == 4)
-            compute(w[i], a[i], (b + i - c0) * kFlushes, [&](int t) { load_a(i, t, far); });
-          else
-            compute(w[i], a[0], (b + i - c0) * kFlushes, [&](int t) { load_a(0, t, b + i + 1); });
-          load_codes(i, far);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (b + i < end) {
-          if constexpr (kAhead == 4)
-            compute(w[i], a[i], (b + i - c0) * kFlushes, [](int) {});
-          else
-            compute(w[i], a[0], (b + i - c0) * kFlushes,
-                    [&](int t) { load_a(0, t, min(b + i + 1, end - 1)); });
-        }
-      }
-    }
-    if (c1 > full && wave == WAVES - 1) {
-      // The last block of a K that is no multiple of 128: addresses stay in the
-      // row, and A and the scales are zeros past K.
-      const int k0 = full << 7;
-      const u32x4 zero4 = {0, 0, 0, 0};
-      const int back = k0 + 32 * lq < p.K ? 0 : 16 * lq;
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        w[0][j] = *reinterpret_cast<const u32x4*>(code_row[j] + (k0 >> 1) - back);
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          const int k = k0 + a_k(t);
-          const u32x4 v = *reinterpret_cast<const u32x4*>(a_row[i] + 2 * (int64_t)min(k, p.K - 8));
-          a[0][t][i] = k < p.K ? v : zero4;
-        }
-      compute(w[0], a[0], (full - c0) * kFlushes, [](int) {});
-    }
+    load(ks + Tile::kSlots - 1, slot == 0 ? Tile::kSlots - 1 : slot - 1);
+    const int left = p.K - (first + ks) * kW4StageK - 128 * kh;
+    if (left >= 128) compute(slot, W4Flag<false>{}, 128);
+    else if (left > 0) compute(slot, W4Flag<true>{}, left);
+    slot = slot + 1 == Tile::kSlots ? 0 : slot + 1;
   }
-  __syncthreads();   // the pairs' place is the sums' now
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) lds.red[wave][i * NT + j][lane] = acc[i][j];
+  // The ring's last loads have landed and its last reads returned: its place
+  // holds the sums now, a row of A each.
+  wait_vmcnt<0>();
+  wait_lgkmcnt0();
   __syncthreads();
-  // An output value is element e of lane (16 (m / 4 % 4) + n % 16) of its tile,
-  // e = m % 4. A thread adds up one pair of neighbouring columns of one row.
-  constexpr int kPairs = kTiles * 128;
-  uint32_t* C = reinterpret_cast<uint32_t*>(p.C);
-  for (int u = (int)threadIdx.x; u < kPairs; u += 64 * WAVES) {
-    const int pair = u & 7, tile = (u >> 3) % NT, r = (u >> 3) / NT;   // row of the workgroup's rows
-    const int m = m0 + r, n = n0 + 16 * tile + 2 * pair;
-    if (m >= p.M || n >= p.N) continue;
-    const int src = ((r >> 2) & 3) * 16 + 2 * pair, e = r & 3, at = (r >> 4) * NT + tile;
-    float lo = 0.f, hi = 0.f;
+  float* sums = reinterpret_cast<float*>(&lds[0]);
+  auto at = [&](int i, int j, int e) {
+    return (16 * i + 4 * lq + e) * Tile::kPitch + 32 * wn + 16 * j + li;
+  };
 #pragma unroll
-    for (int v = 0; v < WAVES; ++v) {
-      lo += reinterpret_cast<const float*>(&lds.red[v][at][src])[e];
-      hi += reinterpret_cast<const float*>(&lds.red[v][at][src + 1])[e];
+  for (int half = 1; half >= 0; --half) {
+    if (kh == half) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            sums[at(i, j, e)] = half == 1 ? acc[i][j][e] : acc[i][j][e] + sums[at(i, j, e)];
     }
-    C[((int64_t)m * p.ldc + n) >> 1] = Mma<T>::pack(lo, hi);
+    __syncthreads();
   }
+  for (int u = (int)threadIdx.x; u < 16 * MT * (kW4TileN / 8); u += 512) {
+    const int r = u / (kW4TileN / 8), c = u % (kW4TileN / 8) * 8;
+    const int m = m0 + r, n = n0 + c;
+    if (m >= p.M || n >= p.N) continue;
+    const f32x4 lo = *reinterpret_cast<const f32x4*>(&sums[r * Tile::kPitch + c]);
+    const f32x4 hi = *reinterpret_cast<const f32x4*>(&sums[r * Tile::kPitch + c + 4]);
+    if (p.splits > 1) {
+      f32x4* to = reinterpret_cast<f32x4*>(p.partials + ((int64_t)split * p.M + m) * p.N + n);
+      to[0] = lo;
+      to[1] = hi;
+    } else {
+      *reinterpret_cast<u32x4*>(p.C + ((int64_t)m * p.ldc + n) * 2) =
+          u32x4{Mma<T>::pack(lo[0], lo[1]), Mma<T>::pack(lo[2], lo[3]),
+                Mma<T>::pack(hi[0], hi[1]), Mma<T>::pack(hi[2], hi[3])};
+    }
+  }
+}
+
+// The splits' partial products added up in order: eight columns a thread.
+template <class T>
+__global__ void __launch_bounds__(256) gemm_w4_join_kernel(W4Params p) {
+  const int octets = p.N >> 3;
+  const int64_t i = long_block() * 256 + threadIdx.x;
+  if (i >= (int64_t)p.M * octets) return;
+  const int64_t m = i / octets, n = i % octets * 8;
+  const float* src = p.partials + m * p.N + n;
+  f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
+  for (int s = 0; s < p.splits; ++s, src += (int64_t)p.M * p.N) {
+    lo += *reinterpret_cast<const f32x4*>(src);
+    hi += *reinterpret_cast<const f32x4*>(src + 4);
+  }
+  *reinterpret_cast<u32x4*>(p.C + (m * p.ldc + n) * 2) =
+      u32x4{Mma<T>::pack(lo[0], lo[1]), Mma<T>::pack(lo[2], lo[3]), Mma<T>::pack(hi[0], hi[1]),
+            Mma<T>::pack(hi[2], hi[3])};
 }
 
 // ---------------------------------------------------------------------------
@@ -493,21 +503,42 @@ hipError_t launch_w4_vec_k(const W4Params& p, hipStream_t stream) {
   return launch_w4_vec<T, MM, 64>(p, stream);
 }
 
-template <class T, int MT, int NT, int WAVES, int F>
-hipError_t launch_w4_shape(const W4Params& p, hipStream_t stream) {
-  const dim3 grid = long_grid(((int64_t)p.N + 16 * NT - 1) / (16 * NT) *
-                              (((int64_t)p.M + 16 * MT - 1) / (16 * MT)));
-  void (*k)(W4Params) = p.zeros != nullptr ? gemm_w4_kernel<T, MT, NT, WAVES, F, true>
-                                           : gemm_w4_kernel<T, MT, NT, WAVES, F, false>;
-  hipLaunchKernelGGL(k, grid, dim3(64 * WAVES), 0, stream, p);
+template <class T, int MT, int F>
+hipError_t launch_w4_tile(const W4Params& p, hipStream_t stream) {
+  const int64_t tiles = (((int64_t)p.N + kW4TileN - 1) / kW4TileN) *
+                        (((int64_t)p.M + 16 * MT - 1) / (16 * MT));
+  void (*k)(W4Params) = p.zeros != nullptr ? gemm_w4_tile_kernel<T, MT, F, true>
+                                           : gemm_w4_tile_kernel<T, MT, F, false>;
+  hipLaunchKernelGGL(k, long_grid(tiles * p.splits), dim3(512), 0, stream, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
+  hipLaunchKernelGGL(gemm_w4_join_kernel<T>, long_grid(((int64_t)p.M * (p.N / 8) + 255) / 256),
+                     dim3(256), 0, stream, p);
   return hipGetLastError();
 }
 
-template <class T, int MT, int NT, int WAVES>
+template <class T, int MT>
 hipError_t launch_w4_group(const W4Params& p, hipStream_t stream) {
-  if (p.group_shift == 5) return launch_w4_shape<T, MT, NT, WAVES, 32>(p, stream);
-  if (p.group_shift == 6) return launch_w4_shape<T, MT, NT, WAVES, 64>(p, stream);
-  return launch_w4_shape<T, MT, NT, WAVES, 128>(p, stream);
+  if (p.group_shift == 5) return launch_w4_tile<T, MT, 32>(p, stream);
+  if (p.group_shift == 6) return launch_w4_tile<T, MT, 64>(p, stream);
+  return launch_w4_tile<T, MT, 128>(p, stream);
+}
+
+// 16-row tiles of A that a workgroup of the tile kernel takes.
+int w4_m_tiles(int64_t M) { return M <= 16 ? 1 : M <= 32 ? 2 : M <= 48 ? 3 : 4; }
+
+// Workgroups that share a tile's K: as many as fill the CUs, two stages each
+// at least. One to four rows are the other kernel's, which needs none.
+int w4_splits(int64_t M, int64_t N, int64_t K) {
+  if (M <= 4) return 1;
+  const int64_t mt = 16 * w4_m_tiles(M);
+  const int64_t tiles = (N + kW4TileN - 1) / kW4TileN * ((M + mt - 1) / mt);
+  const int64_t stages = (K + kW4StageK - 1) / kW4StageK;
+  int64_t splits = tiles < 256 ? 256 / tiles : 1;
+  splits = splits < stages / 2 ? splits : stages / 2;
+  if (splits <= 1) return 1;
+  const int64_t per = (stages + splits - 1) / splits;
+  return (int)((stages + per - 1) / per);   // no empty split
 }
 
 template <class T>
@@ -515,15 +546,23 @@ hipError_t launch_w4_type(const W4Params& p, hipStream_t stream) {
   if (p.M == 1) return launch_w4_vec_k<T, 1>(p, stream);
   if (p.M == 2) return launch_w4_vec_k<T, 2>(p, stream);
   if (p.M <= 4) return launch_w4_vec_k<T, 4>(p, stream);
-  if (p.M <= 16) return launch_w4_group<T, 1, 2, 8>(p, stream);
-  if (p.M <= 32) return launch_w4_group<T, 2, 2, 8>(p, stream);
-  if (p.M <= 48) return launch_w4_group<T, 3, 2, 8>(p, stream);
-  return launch_w4_group<T, 4, 2, 8>(p, stream);
+  switch (w4_m_tiles(p.M)) {
+    case 1: return launch_w4_group<T, 1>(p, stream);
+    case 2: return launch_w4_group<T, 2>(p, stream);
+    case 3: return launch_w4_group<T, 3>(p, stream);
+    default: return launch_w4_group<T, 4>(p, stream);
+  }
 }
 
 }  // namespace
 
-hipError_t launch_gemm_w4(const W4Params& p, int type, hipStream_t stream) {
+int64_t gemm_w4_partials(int64_t M, int64_t N, int64_t K) {
+  const int splits = w4_splits(M, N, K);
+  return splits > 1 ? splits * M * N : 0;
+}
+
+hipError_t launch_gemm_w4(W4Params p, int type, hipStream_t stream) {
+  p.splits = w4_splits(p.M, p.N, p.K);
   return type == 0 ? launch_w4_type<__bf16>(p, stream) : launch_w4_type<_Float16>(p, stream);
 }
 

@@ -41,9 +41,11 @@ struct W4Params {
   const uint8_t *A, *codes, *zeros;
   const uint16_t* scales;
   uint8_t* C;
+  float* partials;                    // [splits][M][N] where splits > 1
   int64_t lda, ld_codes, ld_scales, ld_zeros, ldc;  // bytes, bytes, elements, bytes, elements
   int32_t M, N, K;
   int32_t group_shift;  // log2 of the group size; 31 for one group a row
+  int32_t splits;
 };
 
 // Each launcher takes what its entry point has checked. Types: 0 bf16, 1 fp16,
@@ -54,7 +56,8 @@ hipError_t launch_rmsnorm_grad(const NormGradParams& p, float* dweight, int type
                                hipStream_t stream);
 int64_t gemm_fp8_partials(int64_t M, int64_t N, int64_t K);  // floats of workspace
 hipError_t launch_gemm_fp8(Fp8Params p, int out_type, hipStream_t stream);
-hipError_t launch_gemm_w4(const W4Params& p, int type, hipStream_t stream);
+int64_t gemm_w4_partials(int64_t M, int64_t N, int64_t K);  // floats of workspace
+hipError_t launch_gemm_w4(W4Params p, int type, hipStream_t stream);
 
 // A one-dimensional grid of any length in two dimensions (a launch takes fewer
 // than 2^32 threads along x). Workgroups past the end leave at once or compute

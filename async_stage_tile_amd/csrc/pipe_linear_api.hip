@@ -194,14 +194,27 @@ pipe_status_t pipe_gemm_fp8(const void* A, const float* a_scales, const void* B,
   return hip_status(launch_gemm_fp8(p, out_type, st));
 }
 
+pipe_status_t pipe_gemm_w4_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes) {
+  if (bytes == nullptr) return PIPE_ERR_NULL;
+  *bytes = 0;
+  if (M < 0 || N < 0 || K < 0 || M > INT32_MAX || N > INT32_MAX || K > INT32_MAX - 1024 ||
+      N % 8 != 0 || K % 32 != 0)
+    return PIPE_ERR_SHAPE;
+  if (M == 0 || N == 0 || K == 0) return PIPE_OK;
+  if ((M + 15) / 16 * ((N + 127) / 128) > INT32_MAX) return PIPE_ERR_SHAPE;  // output tiles
+  *bytes = (size_t)gemm_w4_partials(M, N, K) * sizeof(float);
+  return PIPE_OK;
+}
+
 pipe_status_t pipe_gemm_w4(const void* A, const void* codes, const void* scales,
                            const void* zeros, void* C, int64_t M, int64_t N, int64_t K,
                            int64_t group, int64_t lda, int64_t ld_codes, int64_t ld_scales,
-                           int64_t ld_zeros, int64_t ldc, pipe_dtype_t type, void* stream) {
+                           int64_t ld_zeros, int64_t ldc, pipe_dtype_t type, void* workspace,
+                           size_t workspace_bytes, void* stream) {
   if (!is16(type)) return PIPE_ERR_CONFIG;
-  if (M < 0 || N < 0 || K < 0 || M > INT32_MAX || N > INT32_MAX || K > INT32_MAX - 256 ||
-      N % 8 != 0 || K % 32 != 0)
-    return PIPE_ERR_SHAPE;
+  size_t need = 0;
+  const pipe_status_t shape = pipe_gemm_w4_workspace_bytes(M, N, K, &need);
+  if (shape != PIPE_OK) return shape;
   const bool pow2 = group >= 32 && (group & (group - 1)) == 0;
   if (K > 0 && !(group == K || (pow2 && K % group == 0))) return PIPE_ERR_SHAPE;
   const int64_t groups = K > 0 ? K / group : 0;
@@ -220,7 +233,12 @@ pipe_status_t pipe_gemm_w4(const void* A, const void* codes, const void* scales,
   if (!aligned(A, 16) || lda % 8 != 0 || !aligned(codes, 16) || ld_codes % 16 != 0 ||
       !aligned(scales, 2))
     return PIPE_ERR_ALIGN;
+  if (need > 0) {
+    if (workspace == nullptr || workspace_bytes < need) return PIPE_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return PIPE_ERR_ALIGN;
+  }
   W4Params p{};
+  p.partials = static_cast<float*>(workspace);
   p.A = static_cast<const uint8_t*>(A);
   p.codes = static_cast<const uint8_t*>(codes);
   p.scales = static_cast<const uint16_t*>(scales);

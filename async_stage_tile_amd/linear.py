@@ -32,7 +32,8 @@ _LINEAR_SIGS = {
     "pipe_rmsnorm_backward": [_V] * 6 + [_L] * 6 + [_F, _I, _V, _Z, _V],
     "pipe_gemm_fp8_workspace_bytes": [_L, _L, _L, _c.POINTER(_Z)],
     "pipe_gemm_fp8": [_V] * 5 + [_L] * 6 + [_I, _V, _Z, _V],
-    "pipe_gemm_w4": [_V] * 5 + [_L] * 9 + [_I, _V],
+    "pipe_gemm_w4_workspace_bytes": [_L, _L, _L, _c.POINTER(_Z)],
+    "pipe_gemm_w4": [_V] * 5 + [_L] * 9 + [_I, _V, _Z, _V],
 }
 
 _fns = None
@@ -287,7 +288,14 @@ def pipe_gemm_fp8(A, a_scales, B, b_scales, C=None, out_dtype=None, workspace=No
     return C
 
 
-def pipe_gemm_w4(A, codes, scales, zeros=None, C=None, stream=None):
+def pipe_gemm_w4_workspace_bytes(M, N, K) -> int:
+    need = _Z(0)
+    st = (_fns or _setup()).pipe_gemm_w4_workspace_bytes(M, N, K, ctypes.byref(need))
+    _pt._check(st, "pipe_gemm_w4_workspace_bytes")
+    return need.value
+
+
+def pipe_gemm_w4(A, codes, scales, zeros=None, C=None, workspace=None, stream=None):
     """C = A @ W.T for 4-bit weights W[n][k] = (q[n][k] - z[n][k // group]) * scales[n][k // group].
 
     A: (M, K) bfloat16 or float16; codes: (N, K // 2) uint8, the code of an
@@ -315,7 +323,9 @@ def pipe_gemm_w4(A, codes, scales, zeros=None, C=None, stream=None):
         ldc = N
     else:
         ldc = _matrix(C, "C", dtype, dev, (M, N))[2]
+    ws, ws_bytes = _workspace(fns.pipe_gemm_w4_workspace_bytes, "pipe_gemm_w4_workspace_bytes",
+                              (M, N, K), workspace, A, made)
     _call(fns.pipe_gemm_w4, "pipe_gemm_w4", dev, stream, made, A.data_ptr(), codes.data_ptr(),
           scales.data_ptr(), z_ptr, C.data_ptr(), M, N, K, K // groups if groups else 0, lda,
-          ld_codes, ld_scales, ld_zeros, ldc, _codes[dtype])
+          ld_codes, ld_scales, ld_zeros, ldc, _codes[dtype], ws, ws_bytes)
     return C

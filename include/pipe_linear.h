@@ -90,6 +90,9 @@ pipe_status_t pipe_gemm_fp8(const void* A, const float* a_scales, const void* B,
                             int64_t lda, int64_t ldb, int64_t ldc, pipe_dtype_t out_type,
                             void* workspace, size_t workspace_bytes, void* stream);
 
+/* Bytes of workspace pipe_gemm_w4 needs for a shape, as above. */
+pipe_status_t pipe_gemm_w4_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes);
+
 /* C[m][n] = sum_k A[m][k] * (q[n][k] - z[n][k / group]) * scales[n][k / group]
  * with A (M x K), scales (N x K / group) and C in `type` (PIPE_BF16 or
  * PIPE_FP16), 4-bit codes q (two a byte, the even k's in the low half; rows of
@@ -103,11 +106,12 @@ pipe_status_t pipe_gemm_fp8(const void* A, const float* a_scales, const void* B,
  *   for up to 64 rows; more run in passes of 64). M == 0 or N == 0 is a no-op,
  *   K == 0 gives C = 0. A, codes and C bases 16-byte aligned, lda and ldc
  *   multiples of 8, ld_codes a multiple of 16 and >= K / 2; ld_scales and
- *   ld_zeros >= K / group, scales 2-byte aligned. */
+ *   ld_zeros >= K / group, scales 2-byte, the workspace 16-byte aligned. */
 pipe_status_t pipe_gemm_w4(const void* A, const void* codes, const void* scales,
                            const void* zeros, void* C, int64_t M, int64_t N, int64_t K,
                            int64_t group, int64_t lda, int64_t ld_codes, int64_t ld_scales,
-                           int64_t ld_zeros, int64_t ldc, pipe_dtype_t type, void* stream);
+                           int64_t ld_zeros, int64_t ldc, pipe_dtype_t type, void* workspace,
+                           size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

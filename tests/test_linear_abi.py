@@ -110,12 +110,13 @@ def test_gemm_fp8_workspace():
     with pytest.raises(pt.PipeError) as e:
         pt.pipe_gemm_fp8_workspace_bytes(1, 255, 64)
     assert e.value.status == pt.PIPE_ERR_SHAPE
-    for name, n in (("pipe_gemm_fp8_workspace_bytes", 3), ("pipe_rmsnorm_backward_workspace_bytes", 2)):
+    for name, n in (("pipe_gemm_fp8_workspace_bytes", 3), ("pipe_gemm_w4_workspace_bytes", 3), ("pipe_rmsnorm_backward_workspace_bytes", 2)):
         assert getattr(fns(), name)(*[64] * n, None) == pt.PIPE_ERR_NULL
 
 
-def w4(A=P, q=P, s=P, z=0, C=P, M=4, N=64, K=256, G=64, lda=256, ldq=128, lds=4, ldz=4, ldc=64, t=BF):
-    return fns().pipe_gemm_w4(A, q, s, z, C, M, N, K, G, lda, ldq, lds, ldz, ldc, t, None)
+def w4(A=P, q=P, s=P, z=0, C=P, M=4, N=64, K=256, G=64, lda=256, ldq=128, lds=4, ldz=4, ldc=64, t=BF,
+       ws=0, wsb=0):
+    return fns().pipe_gemm_w4(A, q, s, z, C, M, N, K, G, lda, ldq, lds, ldz, ldc, t, ws, wsb, None)
 
 
 @pytest.mark.parametrize("change,status", [
@@ -133,6 +134,17 @@ def w4(A=P, q=P, s=P, z=0, C=P, M=4, N=64, K=256, G=64, lda=256, ldq=128, lds=4,
 ])
 def test_gemm_w4_refusals(change, status):
     assert w4(**change) == status
+
+
+def test_gemm_w4_workspace():
+    M, N, K = 40, 256, 4096
+    need = pt.pipe_gemm_w4_workspace_bytes(M, N, K)
+    assert need > 0 and need % (4 * M * N) == 0
+    kw = dict(M=M, N=N, K=K, G=128, lda=K, ldq=K // 2, lds=32, ldc=N)
+    assert w4(**kw) == pt.PIPE_ERR_WORKSPACE
+    assert w4(ws=P, wsb=need - 1, **kw) == pt.PIPE_ERR_WORKSPACE
+    assert w4(ws=P + 8, wsb=need, **kw) == pt.PIPE_ERR_ALIGN
+    assert pt.pipe_gemm_w4_workspace_bytes(1, N, K) == 0
 
 
 def test_wrappers_refuse_host_tensors_and_wrong_types():
