@@ -93,15 +93,17 @@ __device__ __forceinline__ u32x4 expand_in_order(uint32_t codes) {
 }
 
 // ---------------------------------------------------------------------------
-// Five rows of A and more. A workgroup of 8 waves computes 16 MT rows of A
-// times 128 weight rows; stages of 256 k pass through an LDS ring, filled by direct-to-LDS loads alone, so that one wait count covers a
+// Five rows of A and more. A workgroup computes 16 MT rows of A times
+// 128 weight rows; stages of 256 k pass through an LDS ring, filled by direct-to-LDS loads alone, so that one wait count covers a
 // stage: codes (128 rows of 128 bytes, 16-byte chunk c of row r at place
-// c ^ ((r >> 1) & 7)), A (rows of 512 bytes, chunk c of row r at
-// c ^ (r & 15)), and the scales and zero points of the stage's groups, widened
-// to 32 bits by the load. Wave (wn, kh) takes weight rows 32 wn .. + 31 and the
-// stage's half kh; with the codes of 8 k's in one LDS word, an MFMA step of 32
-// k's reads its operand as it lies: quarter q of the lanes holds
-// k = 8 q .. 8 q + 7. The halves' sums meet in LDS at the end.
+// c ^ ((r >> 1) & 7)) and A (rows of 512 bytes, chunk c of row r at
+// c ^ (r & 15)). The scales and zero points of as many stages as there is room
+// for are copied to a table in LDS between stages, a row's groups at a time:
+// fetched stage by stage, they cost a cache line a row for each few bytes, more
+// requests than the codes themselves. Wave (wn, kh) takes weight rows
+// 32 wn .. + 31 and part kh of the stage's k's; with the codes of 8 k's in one
+// LDS word, an MFMA step of 32 k's reads its operand as it lies: quarter q of
+// the lanes holds k = 8 q .. 8 q + 7. The parts' sums meet in LDS at the end.
 //
 // One barrier a stage: at its top a wave's own loads of the stage have landed
 // and its reads of the stage before have returned. After the barrier that
@@ -121,32 +123,39 @@ struct W4Flag {
 
 constexpr int kW4TileN = 128, kW4StageK = 256;
 
+// Waves along K, each with its part of a stage: the vector units are the bound
+// with one and two row tiles and want four waves a SIMD; more row tiles need
+// the registers of two.
+constexpr int w4_parts(int mt) { return mt <= 2 ? 4 : 2; }
+constexpr int w4_threads(int mt) { return 64 * 4 * w4_parts(mt); }
+
 template <int MT, int F>
 struct W4Tile {
+  static constexpr int kParts = w4_parts(MT);
+  static constexpr int kWaves = 4 * kParts;
+  static constexpr int kSpan = kW4StageK / kParts;         // k's of a part
+  static constexpr int kSum = F < kSpan ? F : kSpan;       // k's between two scalings
   static constexpr int kGroups = kW4StageK / F;            // groups of a stage
   static constexpr int kCodes = kW4TileN * kW4StageK / 2;  // bytes of a slot's parts
   static constexpr int kA = 16 * MT * kW4StageK * 2;
-  static constexpr int kScales = kGroups * kW4TileN * 4;
-  static constexpr int kSlot = kCodes + kA + 2 * kScales;
+  static constexpr int kSlot = kCodes + kA;
   static constexpr int kPitch = kW4TileN + 4;              // floats of a row of sums
-  static constexpr int kSums = 16 * MT * kPitch * 4;
-  // One row tile: three slots, so that two workgroups fit a CU. More: what fits.
-  static constexpr int kSlots = MT == 1 ? 3 : 163840 / kSlot;
-  static constexpr int kLds = kSlots * kSlot > kSums ? kSlots * kSlot : kSums;
-  static constexpr int kLoads = 2 + MT + kGroups / 2;      // a wave and stage
+  static constexpr int kLds = 163840;
+  static constexpr int kFit = (kLds - 8192) / kSlot;
+  static constexpr int kSlots = kFit > 5 ? 5 : kFit;
+  static constexpr int kTable = kLds - kSlots * kSlot;     // scales (2 bytes), zero points (1)
+  static constexpr int kRoom = kTable / (3 * kW4TileN * kGroups);
+  static constexpr int kChunk = kRoom < 32 ? kRoom : 32;   // stages of a table
+  static constexpr int kChunkGroups = kChunk * kGroups;
+  static constexpr int kCodeLoads = 16 / kWaves, kALoads = (8 * MT + kWaves - 1) / kWaves;
+  static constexpr int kLoads = kCodeLoads + kALoads;      // a wave and stage
+  static_assert(kSlots >= 3 && kChunk >= 1 && 16 * MT * kPitch * 4 <= kSlots * kSlot, "LDS");
 };
 
-template <int BYTES>
-__device__ __forceinline__ void dma_words(const void* g, uint32_t lds_base) {
-  if constexpr (BYTES == 2)
-    asm volatile("s_nop 0\n\tglobal_load_lds_ushort %0, off" : : "v"(g), "{m0}"(lds_base) : "memory");
-  else
-    asm volatile("s_nop 0\n\tglobal_load_lds_ubyte %0, off" : : "v"(g), "{m0}"(lds_base) : "memory");
-}
-
 template <class T, int MT, int F, bool ZEROS>
-__global__ void __launch_bounds__(512) gemm_w4_tile_kernel(W4Params p) {
+__global__ void __launch_bounds__(w4_threads(MT)) gemm_w4_tile_kernel(W4Params p) {
   using Tile = W4Tile<MT, F>;
+  constexpr int kSteps = Tile::kSpan / 32, kSums = Tile::kSpan / Tile::kSum;
   __shared__ __align__(1024) uint8_t lds[Tile::kLds];
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int lane = lane_id();
@@ -165,49 +174,64 @@ __global__ void __launch_bounds__(512) gemm_w4_tile_kernel(W4Params p) {
   const int first = split * per, count = min(per, stages - first);   // >= 1
 
   // This wave's loads of a stage.
-  const uint8_t* code_src[2];
-  int code_k[2];
+  const uint8_t* code_src[Tile::kCodeLoads];
+  int code_k[Tile::kCodeLoads];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int r = (wave * 2 + j) * 8 + (lane >> 3);
+  for (int j = 0; j < Tile::kCodeLoads; ++j) {
+    const int r = (wave * Tile::kCodeLoads + j) * 8 + (lane >> 3);
     const int c = (lane & 7) ^ ((r >> 1) & 7);
     code_src[j] = p.codes + (int64_t)min(n0 + r, p.N - 1) * p.ld_codes;
     code_k[j] = 32 * c;
   }
-  const uint8_t* a_src[MT];
-  int a_k[MT];
+  const uint8_t* a_src[Tile::kALoads];
+  int a_k[Tile::kALoads], a_block[Tile::kALoads];
 #pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    const int r = (wave * MT + j) * 2 + (lane >> 5);
+  for (int j = 0; j < Tile::kALoads; ++j) {
+    a_block[j] = (wave * Tile::kALoads + j) % (8 * MT);   // with 8 blocks for 16 waves each comes twice
+    const int r = a_block[j] * 2 + (lane >> 5);
     a_src[j] = p.A + (int64_t)min(m0 + r, p.M - 1) * p.lda;
     a_k[j] = 8 * ((lane & 31) ^ (r & 15));
   }
-  // Groups: waves 0-3 load scales, 4-7 zero points (or the scales again), half
-  // of the 128 rows an instruction.
-  const int64_t group_row = min(n0 + 64 * (wave & 1) + lane, p.N - 1);
   auto load = [&](int ks, int slot) {
     const int k0 = (first + min(ks, count - 1)) * kW4StageK;
     const uint32_t to = base + slot * Tile::kSlot;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < Tile::kCodeLoads; ++j) {
       const int k = k0 + (k0 + code_k[j] < p.K ? code_k[j] : 0);
-      dma_block_nt(code_src[j] + (k >> 1), to + (wave * 2 + j) * kBlockBytes);
+      dma_block_nt(code_src[j] + (k >> 1), to + (wave * Tile::kCodeLoads + j) * kBlockBytes);
     }
 #pragma unroll
-    for (int j = 0; j < MT; ++j) {
+    for (int j = 0; j < Tile::kALoads; ++j) {
       const int k = k0 + (k0 + a_k[j] < p.K ? a_k[j] : 0);
-      dma_block(a_src[j] + 2 * (int64_t)k, to + Tile::kCodes + (wave * MT + j) * kBlockBytes);
+      dma_block(a_src[j] + 2 * (int64_t)k, to + Tile::kCodes + a_block[j] * kBlockBytes);
     }
+  };
+  // The table of the stages from ks on: this wave takes 128 / kWaves rows, 4 at
+  // a time, 16 groups of each. Group g of the table's n-th row lies at [g][n].
+  uint16_t* table_s = reinterpret_cast<uint16_t*>(&lds[Tile::kSlots * Tile::kSlot]);
+  uint8_t* table_z = reinterpret_cast<uint8_t*>(table_s + Tile::kChunkGroups * kW4TileN);
+  constexpr int kRounds = (Tile::kChunkGroups + 15) / 16;
+  auto fill_table = [&](int ks) {
+    const int g_end = min(Tile::kChunk, count - ks) * Tile::kGroups;
+    for (int h = 0; h < kRounds && 16 * h < g_end; ++h) {
+      const int g = 16 * h + li;
+      const int at = min((first + ks) * kW4StageK + g * F, p.K - 1) >> p.group_shift;
+      constexpr int kQuads = 32 / Tile::kWaves;
+      uint16_t sv[kQuads];
+      uint8_t zv[kQuads];
 #pragma unroll
-    for (int j = 0; j < Tile::kGroups / 2; ++j) {
-      const int g = 2 * j + ((wave >> 1) & 1);   // this wave's groups of the stage
-      const int at = min(k0 + g * F, p.K - 1) >> p.group_shift;
-      const uint32_t word = Tile::kCodes + Tile::kA + (g * kW4TileN + 64 * (wave & 1)) * 4;
-      if (ZEROS && kh == 1)
-        dma_words<1>(p.zeros + group_row * p.ld_zeros + at, to + word + Tile::kScales);
-      else
-        dma_words<2>(p.scales + group_row * p.ld_scales + at,
-                     to + word + (kh == 1 ? Tile::kScales : 0));
+      for (int r = 0; r < kQuads; ++r) {
+        const int64_t n = min(n0 + 4 * (kQuads * wave + r) + lq, p.N - 1);
+        sv[r] = p.scales[n * p.ld_scales + at];
+        if constexpr (ZEROS) zv[r] = p.zeros[n * p.ld_zeros + at];
+      }
+#pragma unroll
+      for (int r = 0; r < kQuads; ++r)
+        if (g < g_end) {
+          const int to = g * kW4TileN + 4 * (kQuads * wave + r) + lq;
+          table_s[to] = sv[r];
+          if constexpr (ZEROS) table_z[to] = zv[r];
+        }
     }
   };
 
@@ -218,16 +242,39 @@ __global__ void __launch_bounds__(512) gemm_w4_tile_kernel(W4Params p) {
     for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   const u32x4 ones = {Mma<T>::kOnes, Mma<T>::kOnes, Mma<T>::kOnes, Mma<T>::kOnes};
 
-  // The 128 k's of this wave's half of a slot, of which `left` are inside K.
-  auto compute = [&](int slot, auto CUT, int left) {
+  // This wave's part of a slot, of which `left` k's are inside K.
+  auto compute = [&](int slot, int table, auto CUT, int left) {   // table: the stage's first group there
     constexpr bool cut = decltype(CUT)::value;
     const uint8_t* codes = &lds[slot * Tile::kSlot] + (32 * wn + li) * 128 + 4 * lq;
     const uint8_t* rows = &lds[slot * Tile::kSlot + Tile::kCodes] + li * 512;
-    const uint32_t* groups = reinterpret_cast<const uint32_t*>(
-        &lds[slot * Tile::kSlot + Tile::kCodes + Tile::kA]) + 32 * wn + li;
+    // All LDS reads of the part go out first: left to the compiler they
+    // come one MFMA step at a time, each with its own wait.
+    u32x4 a[kSteps][MT];
+    uint32_t word[kSteps][2];
+    float scale[kSums][2], zero[kSums][2];
 #pragma unroll
-    for (int f = 0; f < 128 / F; ++f) {
-      if (cut && f * F >= left) break;
+    for (int t = 0; t < kSteps; ++t) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)   // row 16 j + li of the wave's: (r >> 1) & 7 is (li >> 1) & 7
+        word[t][j] = *reinterpret_cast<const uint32_t*>(
+            codes + j * 16 * 128 + ((kSteps * kh + t) ^ ((li >> 1) & 7)) * 16);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        a[t][i] = *reinterpret_cast<const u32x4*>(rows + i * 16 * 512 +
+                                                  ((4 * (kSteps * kh + t) + lq) ^ li) * 16);
+    }
+#pragma unroll
+    for (int f = 0; f < kSums; ++f)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int at = (table + (kh * Tile::kSpan + f * Tile::kSum) / F) * kW4TileN + 32 * wn + 16 * j + li;
+        scale[f][j] = Mma<T>::to_float(table_s[at]);
+        zero[f][j] = ZEROS ? (float)table_z[at] : 8.f;
+      }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int f = 0; f < kSums; ++f) {
+      if (cut && f * Tile::kSum >= left) break;
       f32x4 sum[MT], part[MT][2];
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
@@ -236,49 +283,57 @@ __global__ void __launch_bounds__(512) gemm_w4_tile_kernel(W4Params p) {
         for (int j = 0; j < 2; ++j) part[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
 #pragma unroll
-      for (int t = f * (F / 32); t < (f + 1) * (F / 32); ++t) {
+      for (int t = f * (Tile::kSum / 32); t < (f + 1) * (Tile::kSum / 32); ++t) {
         if (cut && 32 * t >= left) break;
-        u32x4 a[MT];
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          a[i] = *reinterpret_cast<const u32x4*>(rows + i * 16 * 512 +
-                                                 ((16 * kh + 4 * t + lq) ^ li) * 16);
-          sum[i] = Mma<T>::mfma(a[i], ones, sum[i]);
-        }
+        for (int i = 0; i < MT; ++i) sum[i] = Mma<T>::mfma(a[t][i], ones, sum[i]);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          // Row 16 j + li of the wave's: (r >> 1) & 7 is (li >> 1) & 7.
-          const uint32_t word = *reinterpret_cast<const uint32_t*>(
-              codes + j * 16 * 128 + ((4 * kh + t) ^ ((li >> 1) & 7)) * 16);
-          const u32x4 q = expand_in_order<T>(word);
+          const u32x4 q = expand_in_order<T>(word[t][j]);
 #pragma unroll
-          for (int i = 0; i < MT; ++i) part[i][j] = Mma<T>::mfma(a[i], q, part[i][j]);
+          for (int i = 0; i < MT; ++i) part[i][j] = Mma<T>::mfma(a[t][i], q, part[i][j]);
         }
       }
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int at = (kh * (128 / F) + f) * kW4TileN + 16 * j;
-        const float s = Mma<T>::to_float((uint16_t)groups[at]);
-        const float z = ZEROS ? (float)(groups[Tile::kScales / 4 + at] & 0xFFu) : 8.f;
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] += s * (part[i][j][e] - z * sum[i][e]);
-      }
+          for (int e = 0; e < 4; ++e)
+            acc[i][j][e] += scale[f][j] * (part[i][j][e] - zero[f][j] * sum[i][e]);
     }
   };
 
   for (int i = 0; i < Tile::kSlots - 1; ++i) load(i, i);
-  int slot = 0;
-  for (int ks = 0; ks < count; ++ks) {
+  fill_table(0);   // seen by the other waves after the first stage's barrier
+  int slot = 0, turn = 0;   // the stage's slot, and its place in the table
+  auto begin = [&](int ks) {
     wait_vmcnt<(Tile::kSlots - 2) * Tile::kLoads>();   // those of younger stages
     wait_lgkmcnt0();
     __syncthreads();
+    if (turn == Tile::kChunk) {
+      turn = 0;
+      fill_table(ks);
+      __syncthreads();
+    }
     load(ks + Tile::kSlots - 1, slot == 0 ? Tile::kSlots - 1 : slot - 1);
-    const int left = p.K - (first + ks) * kW4StageK - 128 * kh;
-    if (left >= 128) compute(slot, W4Flag<false>{}, 128);
-    else if (left > 0) compute(slot, W4Flag<true>{}, left);
+  };
+  auto end = [&]() {
     slot = slot + 1 == Tile::kSlots ? 0 : slot + 1;
+    ++turn;
+  };
+  // Whole stages, then what K leaves of the last one (apart: with both in one
+  // loop the accumulators are copied to and fro between the two).
+  const int whole = (first + count) * kW4StageK <= p.K ? count : count - 1;
+  for (int ks = 0; ks < whole; ++ks) {
+    begin(ks);
+    compute(slot, turn * Tile::kGroups, W4Flag<false>{}, Tile::kSpan);
+    end();
+  }
+  if (whole < count) {
+    begin(whole);
+    const int left = p.K - (first + whole) * kW4StageK - Tile::kSpan * kh;
+    if (left > 0) compute(slot, turn * Tile::kGroups, W4Flag<true>{}, left);
   }
   // The ring's last loads have landed and its last reads returned: its place
   // holds the sums now, a row of A each.
@@ -290,19 +345,20 @@ __global__ void __launch_bounds__(512) gemm_w4_tile_kernel(W4Params p) {
     return (16 * i + 4 * lq + e) * Tile::kPitch + 32 * wn + 16 * j + li;
   };
 #pragma unroll
-  for (int half = 1; half >= 0; --half) {
-    if (kh == half) {
+  for (int part = Tile::kParts - 1; part >= 0; --part) {
+    if (kh == part) {
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            sums[at(i, j, e)] = half == 1 ? acc[i][j][e] : acc[i][j][e] + sums[at(i, j, e)];
+            sums[at(i, j, e)] =
+                part == Tile::kParts - 1 ? acc[i][j][e] : acc[i][j][e] + sums[at(i, j, e)];
     }
     __syncthreads();
   }
-  for (int u = (int)threadIdx.x; u < 16 * MT * (kW4TileN / 8); u += 512) {
+  for (int u = (int)threadIdx.x; u < 16 * MT * (kW4TileN / 8); u += 64 * Tile::kWaves) {
     const int r = u / (kW4TileN / 8), c = u % (kW4TileN / 8) * 8;
     const int m = m0 + r, n = n0 + c;
     if (m >= p.M || n >= p.N) continue;
@@ -429,6 +485,7 @@ __global__ void __launch_bounds__(64 * kVecWaves) gemv_w4_kernel(W4Params p) {
     }
 #pragma unroll
     for (int r = 0; r < kVecRows; ++r) {
+      const float zp = ZEROS ? (float)z[r] : 8.f;
       float part[MM];
 #pragma unroll
       for (int m = 0; m < MM; ++m) part[m] = 0.f;
@@ -441,9 +498,9 @@ __global__ void __launch_bounds__(64 * kVecWaves) gemv_w4_kernel(W4Params p) {
           for (int e = 0; e < 4; ++e) part[m] = Mma<T>::dot2(a[m][t][e], q[e], part[m]);
       }
       const float sc = in ? Mma<T>::to_float(s[r]) : 0.f;
-      const float zp = ZEROS ? (float)z[r] : 8.f;
 #pragma unroll
-      for (int m = 0; m < MM; ++m) acc[m][r] += sc * (part[m] - zp * total[m]);
+      for (int m = 0; m < MM; ++m)
+        acc[m][r] += sc * (part[m] - zp * total[m]);
     }
   }
 #pragma unroll
@@ -509,7 +566,8 @@ hipError_t launch_w4_tile(const W4Params& p, hipStream_t stream) {
                         (((int64_t)p.M + 16 * MT - 1) / (16 * MT));
   void (*k)(W4Params) = p.zeros != nullptr ? gemm_w4_tile_kernel<T, MT, F, true>
                                            : gemm_w4_tile_kernel<T, MT, F, false>;
-  hipLaunchKernelGGL(k, long_grid(tiles * p.splits), dim3(512), 0, stream, p);
+  hipLaunchKernelGGL(k, long_grid(tiles * p.splits), dim3(64 * W4Tile<MT, F>::kWaves), 0, stream,
+                     p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   hipLaunchKernelGGL(gemm_w4_join_kernel<T>, long_grid(((int64_t)p.M * (p.N / 8) + 255) / 256),
