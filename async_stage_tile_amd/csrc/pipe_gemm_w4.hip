@@ -123,17 +123,12 @@ struct W4Flag {
 
 constexpr int kW4TileN = 128, kW4StageK = 256;
 
-// Waves along K, each with its part of a stage: the vector units are the bound
-// with one and two row tiles and want four waves a SIMD; more row tiles need
-// the registers of two.
-constexpr int w4_parts(int mt) { return mt <= 2 ? 4 : 2; }
-constexpr int w4_threads(int mt) { return 64 * 4 * w4_parts(mt); }
+constexpr int kW4Parts = 2;   // waves along K, each with its part of a stage
 
 template <int MT, int F>
 struct W4Tile {
-  static constexpr int kParts = w4_parts(MT);
-  static constexpr int kWaves = 4 * kParts;
-  static constexpr int kSpan = kW4StageK / kParts;         // k's of a part
+  static constexpr int kWaves = 4 * kW4Parts;
+  static constexpr int kSpan = kW4StageK / kW4Parts;         // k's of a part
   static constexpr int kSum = F < kSpan ? F : kSpan;       // k's between two scalings
   static constexpr int kGroups = kW4StageK / F;            // groups of a stage
   static constexpr int kCodes = kW4TileN * kW4StageK / 2;  // bytes of a slot's parts
@@ -147,13 +142,13 @@ struct W4Tile {
   static constexpr int kRoom = kTable / (3 * kW4TileN * kGroups);
   static constexpr int kChunk = kRoom < 32 ? kRoom : 32;   // stages of a table
   static constexpr int kChunkGroups = kChunk * kGroups;
-  static constexpr int kCodeLoads = 16 / kWaves, kALoads = (8 * MT + kWaves - 1) / kWaves;
+  static constexpr int kCodeLoads = 16 / kWaves, kALoads = 8 * MT / kWaves;
   static constexpr int kLoads = kCodeLoads + kALoads;      // a wave and stage
   static_assert(kSlots >= 3 && kChunk >= 1 && 16 * MT * kPitch * 4 <= kSlots * kSlot, "LDS");
 };
 
 template <class T, int MT, int F, bool ZEROS>
-__global__ void __launch_bounds__(w4_threads(MT)) gemm_w4_tile_kernel(W4Params p) {
+__global__ void __launch_bounds__(64 * 4 * kW4Parts) gemm_w4_tile_kernel(W4Params p) {
   using Tile = W4Tile<MT, F>;
   constexpr int kSteps = Tile::kSpan / 32, kSums = Tile::kSpan / Tile::kSum;
   __shared__ __align__(1024) uint8_t lds[Tile::kLds];
@@ -184,11 +179,10 @@ __global__ void __launch_bounds__(w4_threads(MT)) gemm_w4_tile_kernel(W4Params p
     code_k[j] = 32 * c;
   }
   const uint8_t* a_src[Tile::kALoads];
-  int a_k[Tile::kALoads], a_block[Tile::kALoads];
+  int a_k[Tile::kALoads];
 #pragma unroll
   for (int j = 0; j < Tile::kALoads; ++j) {
-    a_block[j] = (wave * Tile::kALoads + j) % (8 * MT);   // with 8 blocks for 16 waves each comes twice
-    const int r = a_block[j] * 2 + (lane >> 5);
+    const int r = (wave * Tile::kALoads + j) * 2 + (lane >> 5);
     a_src[j] = p.A + (int64_t)min(m0 + r, p.M - 1) * p.lda;
     a_k[j] = 8 * ((lane & 31) ^ (r & 15));
   }
@@ -203,7 +197,7 @@ __global__ void __launch_bounds__(w4_threads(MT)) gemm_w4_tile_kernel(W4Params p
 #pragma unroll
     for (int j = 0; j < Tile::kALoads; ++j) {
       const int k = k0 + (k0 + a_k[j] < p.K ? a_k[j] : 0);
-      dma_block(a_src[j] + 2 * (int64_t)k, to + Tile::kCodes + a_block[j] * kBlockBytes);
+      dma_block(a_src[j] + 2 * (int64_t)k, to + Tile::kCodes + (wave * Tile::kALoads + j) * kBlockBytes);
     }
   };
   // The table of the stages from ks on: this wave takes 128 / kWaves rows, 4 at
@@ -345,7 +339,7 @@ __global__ void __launch_bounds__(w4_threads(MT)) gemm_w4_tile_kernel(W4Params p
     return (16 * i + 4 * lq + e) * Tile::kPitch + 32 * wn + 16 * j + li;
   };
 #pragma unroll
-  for (int part = Tile::kParts - 1; part >= 0; --part) {
+  for (int part = kW4Parts - 1; part >= 0; --part) {
     if (kh == part) {
 #pragma unroll
       for (int i = 0; i < MT; ++i)
@@ -354,7 +348,7 @@ __global__ void __launch_bounds__(w4_threads(MT)) gemm_w4_tile_kernel(W4Params p
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             sums[at(i, j, e)] =
-                part == Tile::kParts - 1 ? acc[i][j][e] : acc[i][j][e] + sums[at(i, j, e)];
+                part == kW4Parts - 1 ? acc[i][j][e] : acc[i][j][e] + sums[at(i, j, e)];
     }
     __syncthreads();
   }

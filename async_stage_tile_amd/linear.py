@@ -40,6 +40,7 @@ _fns = None
 _lock = threading.Lock()
 _torch = None
 _codes = {}         # torch dtype -> pipe_dtype_t
+_current_stream = None      # address of a device's current stream
 
 
 def linear_symbols():
@@ -50,7 +51,7 @@ def linear_symbols():
 def _setup():
     """Loads the library once and binds the functions; torch is imported with
     the first call, as everywhere in this package."""
-    global _fns, _torch
+    global _fns, _torch, _current_stream
     with _lock:
         if _fns is None:
             L = _pt.lib()
@@ -67,6 +68,9 @@ def _setup():
             import torch
             _codes.update({torch.bfloat16: PIPE_BF16, torch.float16: PIPE_FP16,
                            torch.float32: PIPE_FP32, torch.float8_e4m3fn: PIPE_E4M3})
+            # The address alone, without the Stream object around it (1 us a call).
+            _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+                lambda device: torch.cuda.current_stream(device).cuda_stream)
             _torch = torch
             _fns = fns
     return _fns
@@ -74,27 +78,37 @@ def _setup():
 
 def _matrix(t, name, dtype, device, shape=None):
     """(rows, cols, pitch) of a 2-D row-major device tensor of the dtype on
-    the device; the shape, where one is given, must match."""
+    the device; the shape, where one is given, must match. The calls here are
+    as long as a small kernel, so the common case asks little."""
+    try:
+        if (t.dtype is dtype and t.get_device() == device and device >= 0
+                and (shape is None or t.shape == shape) and t.is_contiguous()):
+            rows, cols = t.shape
+            return rows, cols, cols
+    except (AttributeError, ValueError):    # no tensor, or not two axes
+        pass
     if not isinstance(t, _torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.get_device() != device or device < 0:
-        raise ValueError(f"{name} must be a tensor on device cuda:{device}" if device >= 0 else
-                         f"{name} must be a device tensor")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    if device < 0:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be a tensor on device cuda:{device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     return _pt.matrix_geometry(t.shape, t.stride(), name)
 
 
 def _vector(t, name, dtype, device, n):
+    """Address of a contiguous vector of n elements."""
     if not isinstance(t, _torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if t.get_device() != device:
         raise ValueError(f"{name} must be a tensor on device cuda:{device}")
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector of {n} elements")
     return t.data_ptr()
 
@@ -103,7 +117,7 @@ def _dtype16(t, name):
     if not isinstance(t, _torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     dtype = t.dtype
-    if dtype != _torch.bfloat16 and dtype != _torch.float16:
+    if _codes.get(dtype, PIPE_FP32) > PIPE_FP16:
         raise TypeError(f"{name} must be bfloat16 or float16, not {dtype}")
     return dtype
 
@@ -112,7 +126,7 @@ def _call(fn, name, device, stream, made, *args):
     """The C call with the tensors' device current, on the given stream or the
     device's current one, which goes last; `made`: the tensors allocated here."""
     if stream is None:
-        raw = _torch.cuda.current_stream(device).cuda_stream
+        raw = _current_stream(device)
     else:
         if stream.device.index != device:
             raise ValueError(f"stream of {stream.device} for tensors on cuda:{device}")
@@ -143,21 +157,21 @@ def pipe_rmsnorm(x, weight, residual=None, eps=1e-6, out_dtype=None, y=None, y_s
     dev = x.get_device()
     M, N, ld_x = _matrix(x, "x", dtype, dev)
     out_dtype = out_dtype or (dtype if y is None else y.dtype)
-    if out_dtype != dtype and out_dtype != _torch.float8_e4m3fn:
+    if out_dtype is not dtype and out_dtype is not _torch.float8_e4m3fn:
         raise TypeError(f"out_dtype must be {dtype} or float8_e4m3fn, not {out_dtype}")
     w = _vector(weight, "weight", dtype, dev, N)
     made = []
     if y is None:
-        y = x.new_empty((M, N), dtype=out_dtype)
+        y = _torch.empty_like(x, dtype=out_dtype, memory_format=_torch.contiguous_format)
         made.append(y)
         ld_y = N
     else:
         ld_y = _matrix(y, "y", out_dtype, dev, (M, N))[2]
-    q8 = out_dtype != dtype
+    q8 = out_dtype is not dtype
     scales = 0
     if q8:
         if y_scales is None:
-            y_scales = x.new_empty((M,), dtype=_torch.float32)
+            y_scales = x.new_empty(M, dtype=_torch.float32)
             made.append(y_scales)
             scales = y_scales.data_ptr()
         else:
@@ -169,7 +183,7 @@ def pipe_rmsnorm(x, weight, residual=None, eps=1e-6, out_dtype=None, y=None, y_s
         ld_r = _matrix(residual, "residual", dtype, dev, (M, N))[2]
         r_ptr = residual.data_ptr()
         if h is None:
-            h = x.new_empty((M, N))
+            h = _torch.empty_like(x, memory_format=_torch.contiguous_format)
             made.append(h)
             ld_h = N
         else:
@@ -202,13 +216,13 @@ def pipe_rmsnorm_backward(dy, x, weight, dh=None, eps=1e-6, dx=None, dweight=Non
         dh_ptr = dh.data_ptr()
     made = []
     if dx is None:
-        dx = x.new_empty((M, N))
+        dx = _torch.empty_like(x, memory_format=_torch.contiguous_format)
         made.append(dx)
         ld_dx = N
     else:
         ld_dx = _matrix(dx, "dx", dtype, dev, (M, N))[2]
     if dweight is None:
-        dweight = x.new_empty((N,), dtype=_torch.float32)
+        dweight = x.new_empty(N, dtype=_torch.float32)
         made.append(dweight)
     else:
         _vector(dweight, "dweight", _torch.float32, dev, N)
@@ -230,11 +244,12 @@ def _workspace(fn, name, shape, given, like, made):
     st = fn(*shape, ctypes.byref(need))
     if st:
         raise _pt.PipeError(st, name)
-    if need.value == 0:
+    size = need.value
+    if size == 0:
         return 0, 0
-    ws = like.new_empty((need.value,), dtype=_torch.uint8)
+    ws = like.new_empty(size, dtype=_torch.uint8)
     made.append(ws)
-    return ws.data_ptr(), need.value
+    return ws.data_ptr(), size
 
 
 def pipe_rmsnorm_backward_workspace_bytes(M, N) -> int:
