@@ -20,7 +20,7 @@ struct NormParams {
 struct NormGradParams {
   const uint8_t *dy, *x, *weight, *dh;
   uint8_t* dx;
-  float* partials;  // [grid * rows in flight a workgroup][N]
+  float* partials;  // [workgroups][N]
   int64_t ld_dy, ld_x, ld_dh, ld_dx;  // bytes
   int64_t M;
   int32_t chunks;

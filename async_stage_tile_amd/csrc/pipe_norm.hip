@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(WG) rmsnorm_kernel(NormParams p) {
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = t + TPR * i;
-      if (c < p.chunks) __builtin_nontemporal_store(v[i], h + c);
+      if (c < p.chunks) h[c] = v[i];
     }
   }
   if constexpr (Q8) {
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(WG) rmsnorm_kernel(NormParams p) {
         int b = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * e], f[4 * e + 1], 0, false);
         o[e] = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * e + 2], f[4 * e + 3], b, true);
       }
-      if (c < p.chunks) __builtin_nontemporal_store(o, y + c);
+      if (c < p.chunks) y[c] = o;
     }
   } else {
     u32x4* y = reinterpret_cast<u32x4*>(p.y + row * p.ld_y);
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(WG) rmsnorm_kernel(NormParams p) {
       for (int e = 0; e < 4; ++e)
         o[e] = Pair<T>::pack(Pair<T>::lo(v[i][e]) * r * Pair<T>::lo(wt[i][e]),
                              Pair<T>::hi(v[i][e]) * r * Pair<T>::hi(wt[i][e]));
-      if (c < p.chunks) __builtin_nontemporal_store(o, y + c);
+      if (c < p.chunks) y[c] = o;
     }
   }
 }
@@ -186,7 +186,7 @@ hipError_t launch_norm_type(const NormParams& p, bool q8, hipStream_t stream) {
   if (p.chunks <= 128) return launch_norm_shape<T, 64, 256, 2>(p, q8, stream);
   if (p.chunks <= 256) return launch_norm_shape<T, 64, 256, 4>(p, q8, stream);
   if (p.chunks <= 512) return launch_norm_shape<T, 256, 256, 2>(p, q8, stream);
-  if (p.chunks <= 1024) return launch_norm_shape<T, 256, 256, 4>(p, q8, stream);
+  if (p.chunks <= 1024) return launch_norm_shape<T, 512, 512, 2>(p, q8, stream);
   if (p.chunks <= 2048) return launch_norm_shape<T, 512, 512, 4>(p, q8, stream);
   return launch_norm_shape<T, 1024, 1024, 4>(p, q8, stream);
 }
@@ -212,33 +212,46 @@ __global__ void __launch_bounds__(WG) rmsnorm_grad_kernel(NormGradParams p) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[i][e] = 0.f;
   }
-  int turn = 0;
-  for (int64_t base = (int64_t)blockIdx.x * kRows; base < p.M;
-       base += (int64_t)gridDim.x * kRows, turn ^= 1) {
-    const int64_t row = base + sub;
-    const bool live = row < p.M;
-    const int64_t at = live ? row : p.M - 1;
+  // A row's loads go out before the row ahead of it is reduced. Past the last
+  // row they take the last one again: a branch around them would make the
+  // compiler wait for them with the row in use.
+  u32x4 h[CH], d[CH], s[RES ? CH : 1], nh[CH], nd[CH], ns[RES ? CH : 1];
+  const auto load = [&](int64_t row) {
+    const int64_t at = row < p.M ? row : p.M - 1;
     const u32x4* dy = reinterpret_cast<const u32x4*>(p.dy + at * p.ld_dy);
     const u32x4* x = reinterpret_cast<const u32x4*>(p.x + at * p.ld_x);
     const u32x4* dh = reinterpret_cast<const u32x4*>(p.dh + at * p.ld_dh);
-    u32x4 d[CH], h[CH], s[RES ? CH : 1];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = t + TPR * i;
-      h[i] = d[i] = u32x4{0, 0, 0, 0};
+      nh[i] = nd[i] = u32x4{0, 0, 0, 0};
       if (c < p.chunks) {
-        h[i] = __builtin_nontemporal_load(x + c);
-        d[i] = __builtin_nontemporal_load(dy + c);
+        nh[i] = __builtin_nontemporal_load(x + c);
+        nd[i] = __builtin_nontemporal_load(dy + c);
       }
     }
     if constexpr (RES) {
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         const int c = t + TPR * i;
-        s[i] = u32x4{0, 0, 0, 0};
-        if (c < p.chunks) s[i] = __builtin_nontemporal_load(dh + c);
+        ns[i] = u32x4{0, 0, 0, 0};
+        if (c < p.chunks) ns[i] = __builtin_nontemporal_load(dh + c);
       }
     }
+  };
+  int turn = 0;
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  load((int64_t)blockIdx.x * kRows + sub);
+  for (int64_t base = (int64_t)blockIdx.x * kRows; base < p.M; base += step, turn ^= 1) {
+    const int64_t row = base + sub;
+    const bool live = row < p.M;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      h[i] = nh[i];
+      d[i] = nd[i];
+      if constexpr (RES) s[i] = ns[i];
+    }
+    load(row + step);
     float hh = 0.f, gh = 0.f;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -294,18 +307,35 @@ __global__ void __launch_bounds__(WG) rmsnorm_grad_kernel(NormGradParams p) {
           dw[i][2 * e] += dl * (hl * r);
           dw[i][2 * e + 1] += du * (hu * r);
         }
-        if (c < p.chunks) __builtin_nontemporal_store(o, dx + c);
+        if (c < p.chunks) dx[c] = o;
       }
     }
   }
-  f32x4* out = reinterpret_cast<f32x4*>(p.partials + ((int64_t)blockIdx.x * kRows + sub) *
-                                                         ((int64_t)p.chunks * 8));
+  f32x4* out = reinterpret_cast<f32x4*>(p.partials + (int64_t)blockIdx.x * ((int64_t)p.chunks * 8));
+  if constexpr (kRows == 1) {
 #pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    const int c = t + TPR * i;
-    if (c < p.chunks) {
-      out[2 * c] = f32x4{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
-      out[2 * c + 1] = f32x4{dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
+    for (int i = 0; i < CH; ++i) {
+      const int c = t + TPR * i;
+      if (c < p.chunks) {
+        out[2 * c] = f32x4{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
+        out[2 * c + 1] = f32x4{dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
+      }
+    }
+  } else {
+    // The rows in flight add up in LDS first, in order.
+    __shared__ f32x4 sums[kRows][2 * CH * TPR];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = t + TPR * i;
+      sums[sub][2 * c] = f32x4{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
+      sums[sub][2 * c + 1] = f32x4{dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
+    }
+    __syncthreads();
+    for (int u = (int)threadIdx.x; u < 2 * p.chunks; u += WG) {
+      f32x4 v = sums[0][u];
+#pragma unroll
+      for (int r = 1; r < kRows; ++r) v += sums[r][u];
+      out[u] = v;
     }
   }
 }
@@ -336,17 +366,17 @@ __global__ void __launch_bounds__(256) rmsnorm_dweight_kernel(const float* __res
 }
 
 struct GradShape {
-  int rows;        // rows in flight a workgroup
+  int rows;      // in flight a workgroup
   int64_t grid;
 };
 
-// Workgroups of the gradient: enough to fill the card twice over, and no more
-// than there are rows to start on, since each writes a row of partials.
+// Workgroups: two a CU (one of 1024 threads), and no more than there are rows to
+// start on, since each writes a row of partials.
 GradShape grad_shape(int64_t M, int64_t chunks) {
   GradShape g;
   g.rows = chunks <= 256 ? 4 : 1;
-  const int64_t need = (M + g.rows - 1) / g.rows;
-  g.grid = need < 512 ? need : 512;
+  const int64_t need = (M + g.rows - 1) / g.rows, fill = chunks <= 1024 ? 512 : 256;
+  g.grid = need < fill ? need : fill;
   return g;
 }
 
@@ -364,7 +394,7 @@ hipError_t launch_grad_type(const NormGradParams& p, int64_t grid, hipStream_t s
   if (p.chunks <= 128) return launch_grad_shape<T, 64, 256, 2>(p, grid, stream);
   if (p.chunks <= 256) return launch_grad_shape<T, 64, 256, 4>(p, grid, stream);
   if (p.chunks <= 512) return launch_grad_shape<T, 256, 256, 2>(p, grid, stream);
-  if (p.chunks <= 1024) return launch_grad_shape<T, 512, 512, 2>(p, grid, stream);
+  if (p.chunks <= 1024) return launch_grad_shape<T, 256, 256, 4>(p, grid, stream);
   if (p.chunks <= 2048) return launch_grad_shape<T, 1024, 1024, 2>(p, grid, stream);
   return launch_grad_shape<T, 1024, 1024, 4>(p, grid, stream);
 }
@@ -378,7 +408,7 @@ hipError_t launch_rmsnorm(const NormParams& p, int type, bool q8, hipStream_t st
 
 int64_t rmsnorm_grad_partials(int64_t M, int64_t N) {
   const GradShape g = grad_shape(M, N / 8);
-  return g.grid * g.rows;
+  return g.grid;
 }
 
 hipError_t launch_rmsnorm_grad(const NormGradParams& p, float* dweight, int type,
@@ -391,7 +421,7 @@ hipError_t launch_rmsnorm_grad(const NormGradParams& p, float* dweight, int type
   }
   const int n = p.chunks * 8;
   hipLaunchKernelGGL(rmsnorm_dweight_kernel, dim3((n + 31) / 32), dim3(256), 0, stream, p.partials,
-                     dweight, (int)(g.grid * g.rows), n);
+                     dweight, (int)g.grid, n);
   return hipGetLastError();
 }
 
