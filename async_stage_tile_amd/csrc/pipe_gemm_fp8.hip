@@ -7,9 +7,9 @@
 // both operands use it; the loads below choose the one that reads memory or
 // LDS in the best order.
 //
-// Few rows: the call is bound by reading B once, so B goes from memory straight
-// into registers (gemm_fp8_skinny_kernel). Many rows: A and B tiles pass
-// through an LDS ring (gemm_fp8_tile_kernel).
+// Few rows: the call is bound by reading B once, from memory straight into
+// registers for up to four (gemv_fp8_kernel), through a deep LDS ring for up to
+// 64 (gemm_fp8_rows_kernel). Many rows: gemm_fp8_tile_kernel.
 #include "pipe_device.hpp"
 #include "pipe_linear.hpp"
 
@@ -17,97 +17,271 @@ namespace pipe {
 
 namespace {
 
+template <int T>
+struct Step {
+  static constexpr int value = T;
+};
+
 __device__ __forceinline__ i32x8 join(u32x4 a, u32x4 b) {
   return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
 }
 
+__device__ __forceinline__ void dma_block_at(const uint8_t* base, uint32_t offset,
+                                             uint32_t lds_base) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :
+               : "v"(offset), "s"(base), "{m0}"(lds_base)
+               : "memory");
+}
+
 // ---------------------------------------------------------------------------
-// Few rows. A wave holds 16 NT rows of B and 16 MT of A; the waves of a
-// workgroup split K in steps of 128 bytes, each next step going to the next
-// wave, so that the workgroup as a whole reads long runs of each row. Their
-// sums meet in LDS, in wave order. Rows of A and B past the end are read from
-// the last row and dropped; bytes past K are zeros in both.
+// One to four rows of A. A lane keeps 16 k's of every row in registers, as fp16
+// pairs (e4m3 values are fp16 values), and meets them with the same k's of
+// kVecRows rows of B, one 16-byte load each: a wave reads 1 KiB of a row at a
+// time (LPR lanes make up a row where K is shorter) and all loads of its rows
+// are in flight together. v_dot2 adds up two products at a time in fp32. The
+// MFMAs, which want 16 rows of B side by side and so 64-byte pieces of each,
+// streamed B at 3.6 TB/s where this reads 5.
 // ---------------------------------------------------------------------------
-template <int MT, int NT, int WAVES, int OUT>
-__global__ void __launch_bounds__(64 * WAVES) gemm_fp8_skinny_kernel(Fp8Params p) {
-  constexpr int kTiles = MT * NT;
-  __shared__ f32x4 red[WAVES][kTiles][64];
+constexpr int kVecRows = 8;
+constexpr int kVecWaves = 8;    // at most, each with slices of K of its own
+constexpr int kVecSlice = 1024;
+
+__device__ __forceinline__ f16x2 e4m3_pair(uint32_t w, bool hi) {
+  return hi ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, true)
+            : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, false);
+}
+
+template <int MM, int LPR, int OUT>
+__global__ void __launch_bounds__(64 * kVecWaves) gemv_fp8_kernel(Fp8Params p) {
+  constexpr int kRowsPer = 64 / LPR;   // rows of B a load
+  __shared__ float red[kVecWaves][MM][kVecRows * kRowsPer];
   const int lane = (int)(threadIdx.x & 63);
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int li = lane & 15, lq = lane >> 4;
-  const int m_tiles = (p.M + 16 * MT - 1) / (16 * MT);
-  const int64_t wg = long_block();
-  if (wg >= (int64_t)m_tiles * ((p.N + 16 * NT - 1) / (16 * NT))) return;
-  const int n0 = (int)(wg / m_tiles) * (16 * NT), m0 = (int)(wg % m_tiles) * (16 * MT);
-  const uint8_t *b_row[NT], *a_row[MT];
+  const int waves = (int)(blockDim.x >> 6);
+  const int64_t row0 = long_block() * (kVecRows * kRowsPer);
+  if (row0 >= p.N) return;
+  float acc[MM][kVecRows];
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
-    b_row[j] = p.B + (int64_t)min(n0 + 16 * j + li, p.N - 1) * p.ldb + 16 * lq;
+  for (int m = 0; m < MM; ++m)
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-    a_row[i] = p.A + (int64_t)min(m0 + 16 * i + li, p.M - 1) * p.lda + 16 * lq;
-  f32x4 acc[NT][MT];
+    for (int r = 0; r < kVecRows; ++r) acc[m][r] = 0.f;
+  const int slices = LPR < 64 ? 1 : (p.K + kVecSlice - 1) / kVecSlice;
+  for (int slice = wave; slice < slices; slice += waves) {
+    const int k = slice * kVecSlice + (lane % LPR) * 16;
+    const bool in = k < p.K;
+    const int kk = in ? k : 0;      // lanes past K read the row's start, and add nothing
+    u32x4 a[MM], w[kVecRows];
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
+    for (int m = 0; m < MM; ++m)
+      a[m] = *reinterpret_cast<const u32x4*>(p.A + min(m, p.M - 1) * p.lda + kk);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  const auto use = [&](i32x8(&b)[NT], i32x8(&a)[MT]) {
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-        acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j], a[i], acc[j][i], 0, 0, 0,
-                                                                     0, 0, 0);
-  };
-  const int full = p.K >> 7;
-#pragma unroll 4
-  for (int st = wave; st < full; st += WAVES) {
-    const int k0 = st << 7;
-    i32x8 b[NT], a[MT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-      b[j] = join(__builtin_nontemporal_load(reinterpret_cast<const u32x4*>(b_row[j] + k0)),
-                  __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(b_row[j] + k0 + 64)));
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-      a[i] = join(*reinterpret_cast<const u32x4*>(a_row[i] + k0),
-                  *reinterpret_cast<const u32x4*>(a_row[i] + k0 + 64));
-    use(b, a);
-  }
-  if ((p.K & 127) != 0 && wave == full % WAVES) {
-    // Lanes past K read the row's chunk 0 of the step; A's is zeroed.
-    const int k0 = full << 7, left = p.K - k0;
-    const int at0 = 16 * lq < left ? 0 : -16 * lq, at1 = 64 + 16 * lq < left ? 64 : -16 * lq;
-    const u32x4 zero4 = {0, 0, 0, 0};
-    i32x8 b[NT], a[MT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-      b[j] = join(*reinterpret_cast<const u32x4*>(b_row[j] + k0 + at0),
-                  *reinterpret_cast<const u32x4*>(b_row[j] + k0 + at1));
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const u32x4 lo = *reinterpret_cast<const u32x4*>(a_row[i] + k0 + at0);
-      const u32x4 hi = *reinterpret_cast<const u32x4*>(a_row[i] + k0 + at1);
-      a[i] = join(16 * lq < left ? lo : zero4, 64 + 16 * lq < left ? hi : zero4);
+    for (int r = 0; r < kVecRows; ++r) {
+      int64_t n = row0 + r * kRowsPer;
+      if constexpr (LPR < 64) n += lane / LPR;
+      if (n > p.N - 1) n = p.N - 1;
+      w[r] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p.B + n * p.ldb + kk));
     }
-    use(b, a);
+    f16x2 av[MM][8];
+#pragma unroll
+    for (int m = 0; m < MM; ++m)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) av[m][e] = e4m3_pair(a[m][e >> 1], e & 1);
+    if (in) {
+#pragma unroll
+      for (int r = 0; r < kVecRows; ++r)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const f16x2 b = e4m3_pair(w[r][e >> 1], e & 1);
+#pragma unroll
+          for (int m = 0; m < MM; ++m)
+            acc[m][r] = __builtin_amdgcn_fdot2(av[m][e], b, acc[m][r], false);
+        }
+    }
   }
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
+  for (int m = 0; m < MM; ++m) {
+    if constexpr (LPR == 64) {
+      float out[2];
+      sum_rows(acc[m], out);
+      if ((lane & 15) == 0) {
+        const int part = (lane >> 4), at = ((part & 1) << 1) | (part >> 1);
+        red[wave][m][at] = out[0];
+        red[wave][m][4 + at] = out[1];
+      }
+    } else {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) red[wave][j * MT + i][lane] = acc[j][i];
+      for (int r = 0; r < kVecRows; ++r) {
+        float v = acc[m][r];
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+        if (lane % LPR == 0) red[wave][m][r * kRowsPer + lane / LPR] = v;
+      }
+    }
+  }
   __syncthreads();
-  // Lane l of a tile holds columns n = 4 (l / 16) .. + 3 of row m = l % 16.
-  for (int u = (int)threadIdx.x; u < kTiles * 64; u += 64 * WAVES) {
-    const int tile = u >> 6, l = u & 63;
-    f32x4 v = red[0][tile][l];
+  constexpr int kQuads = MM * kVecRows * kRowsPer / 4;
+  for (int u = (int)threadIdx.x; u < kQuads; u += (int)blockDim.x) {
+    const int m = u / (kQuads / MM), r = u % (kQuads / MM) * 4;
+    const int64_t n = row0 + r;
+    if (m >= p.M || n >= p.N) continue;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < waves; ++s)
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) v += red[w][tile][l];
-    const int m = m0 + 16 * (tile % MT) + (l & 15), n = n0 + 16 * (tile / MT) + 4 * (l >> 4);
-    if (m < p.M && n < p.N) {
+      for (int e = 0; e < 4; ++e) v[e] += red[s][m][r + e];
+    const float sa = p.a_scales[m];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = v[e] * sa * p.b_scales[n + e];
+    store4<OUT>(p.C, m * p.ldc + n, v);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Five to 64 rows: bound by reading B once, through few CUs' worth of tiles. A
+// workgroup of 8 waves computes 32 FM rows of A times 32 WN rows of B. Stages
+// of 512 k pass through an LDS ring (rows of 512 bytes, 16-byte chunk c of row
+// r at place c ^ (r & 15), 2 rows a direct-to-LDS block); wave (wn, wk) takes 32
+// rows of B and part wk of the stage's k's. The parts' sums meet in LDS at the
+// end. One CU's ring holds about 100 KiB of loads in flight, which at the
+// memory's latency is 35 KB a us: what counts is that every CU has a tile, so
+// tiles are 32 columns wide up to N = 12288, and with fewer than 96 of them K
+// is split over workgroups too.
+// ---------------------------------------------------------------------------
+constexpr int kRowsStageK = 512;
+
+template <int FM, int WN>
+struct Fp8Rows {
+  static constexpr int kN = 32 * WN, kParts = 8 / WN;
+  static constexpr int kSteps = kRowsStageK / kParts / 64;   // MFMA steps of a part
+  static constexpr int kA = 32 * FM * kRowsStageK, kB = kN * kRowsStageK;
+  static constexpr int kSlot = kA + kB;
+  static constexpr int kSlots = 163840 / kSlot;
+  static constexpr int kLoadsA = kA / kBlockBytes / 8, kLoadsB = kB / kBlockBytes / 8;
+  static constexpr int kLoads = kLoadsA + kLoadsB;     // a wave and stage
+  static constexpr int kPitch = kN + 4;                // floats of a row of sums
+  static_assert(kSlots >= 2 && kParts * 32 * FM * kPitch * 4 <= kSlots * kSlot, "LDS");
+};
+
+template <int FM, int WN, int OUT>
+__global__ void __launch_bounds__(512) gemm_fp8_rows_kernel(Fp8Params p) {
+  using Tile = Fp8Rows<FM, WN>;
+  constexpr int kN = Tile::kN, kSteps = Tile::kSteps;
+  __shared__ __align__(1024) uint8_t lds[Tile::kSlots * Tile::kSlot];
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int lane = lane_id();
+  const int li = lane & 31, lh = lane >> 5;
+  const int wn = wave % WN, wk = wave / WN;
+  const uint32_t base = uniform(lds_addr(&lds[0]));
+  const int64_t wg = long_block();
+  if (wg >= (int64_t)p.tiles_n * p.splits) return;
+  const int split = (int)(wg / p.tiles_n), n0 = (int)(wg % p.tiles_n) * kN;
+  const int per = (p.steps + p.splits - 1) / p.splits;
+  const int first = split * per, count = min(per, p.steps - first);   // >= 1
+
+  const uint8_t* src[Tile::kLoads];
+  int src_k[Tile::kLoads];
+#pragma unroll
+  for (int j = 0; j < Tile::kLoads; ++j) {
+    const bool of_a = j < Tile::kLoadsA;
+    const int block = of_a ? wave * Tile::kLoadsA + j : wave * Tile::kLoadsB + j - Tile::kLoadsA;
+    const int r = block * 2 + (lane >> 5);
+    src[j] = of_a ? p.A + (int64_t)min(r, p.M - 1) * p.lda
+                  : p.B + (int64_t)min(n0 + r, p.N - 1) * p.ldb;
+    src_k[j] = 16 * ((lane & 31) ^ (r & 15));
+  }
+  // Loads past K take the stage's first chunk, past the last stage that one again.
+  auto load = [&](int ks, int slot) {
+    const int k0 = (first + min(ks, count - 1)) * kRowsStageK;
+    const uint32_t to = base + slot * Tile::kSlot;
+#pragma unroll
+    for (int j = 0; j < Tile::kLoads; ++j) {
+      const uint8_t* g = src[j] + k0 + (k0 + src_k[j] < p.K ? src_k[j] : 0);
+      if (j < Tile::kLoadsA)
+        dma_block(g, to + (wave * Tile::kLoadsA + j) * kBlockBytes);
+      else
+        dma_block_nt(g, to + Tile::kA + (wave * Tile::kLoadsB + j - Tile::kLoadsA) * kBlockBytes);
+    }
+  };
+  f32x16 acc[FM];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[i][e] = 0.f;
+  // This wave's part of a slot, of which `left` k's are inside K; half h of a
+  // fragment of step t takes chunks 4 t + h and 4 t + 2 + h of it.
+  auto compute = [&](int slot, auto CUT, int left) {
+    constexpr bool cut = decltype(CUT)::value != 0;
+    const uint8_t* a_row = &lds[slot * Tile::kSlot] + li * kRowsStageK;
+    const uint8_t* b_row = &lds[slot * Tile::kSlot + Tile::kA] + (32 * wn + li) * kRowsStageK;
+    auto read = [&](const uint8_t* row, int t) {
+      const int c = 4 * (kSteps * wk + t) + lh;
+      return join(*reinterpret_cast<const u32x4*>(row + (c ^ (li & 15)) * 16),
+                  *reinterpret_cast<const u32x4*>(row + ((c + 2) ^ (li & 15)) * 16));
+    };
+    i32x8 a[kSteps][FM], b[kSteps];
+#pragma unroll
+    for (int t = 0; t < kSteps; ++t) {
+      b[t] = read(b_row, t);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        a[t][i] = read(a_row + i * 32 * kRowsStageK, t);
+        if constexpr (cut)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if ((4 * t + 2 * (e >> 2) + lh) * 16 >= left) a[t][i][e] = 0;
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kSteps; ++t)
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+        acc[i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b[t], a[t][i], acc[i], 0, 0, 0, 0,
+                                                                 0, 0);
+  };
+
+  for (int i = 0; i < Tile::kSlots - 1; ++i) load(i, i);
+  int slot = 0;
+  auto begin = [&](int ks) {
+    wait_vmcnt<(Tile::kSlots - 2) * Tile::kLoads>();   // those of younger stages
+    wait_lgkmcnt0();
+    __syncthreads();
+    load(ks + Tile::kSlots - 1, slot == 0 ? Tile::kSlots - 1 : slot - 1);
+  };
+  const int whole = (first + count) * kRowsStageK <= p.K ? count : count - 1;
+  for (int ks = 0; ks < whole; ++ks) {
+    begin(ks);
+    compute(slot, Step<0>{}, 64 * kSteps);
+    slot = slot + 1 == Tile::kSlots ? 0 : slot + 1;
+  }
+  if (whole < count) {
+    begin(whole);
+    compute(slot, Step<1>{}, p.K - (first + whole) * kRowsStageK - 64 * kSteps * wk);
+  }
+  // The last loads have landed and the last reads returned: the sums' place.
+  wait_vmcnt<0>();
+  wait_lgkmcnt0();
+  __syncthreads();
+  float* sums = reinterpret_cast<float*>(&lds[0]);
+  // Lane l holds row l % 32 and columns 8 (e / 4) + 4 (l / 32) + e % 4 of a block.
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<f32x4*>(sums + ((wk * FM + i) * 32 + li) * Tile::kPitch + 32 * wn + 8 * q +
+                                4 * lh) =
+          f32x4{acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]};
+  __syncthreads();
+  for (int u = (int)threadIdx.x; u < 32 * FM * (kN / 4); u += 512) {
+    const int m = u / (kN / 4), c = u % (kN / 4) * 4, n = n0 + c;
+    if (m >= p.M || n >= p.N) continue;
+    f32x4 v = *reinterpret_cast<const f32x4*>(sums + m * Tile::kPitch + c);
+#pragma unroll
+    for (int s = 1; s < Tile::kParts; ++s)
+      v += *reinterpret_cast<const f32x4*>(sums + (s * 32 * FM + m) * Tile::kPitch + c);
+    if (p.splits > 1) {
+      *reinterpret_cast<f32x4*>(p.partials + ((int64_t)split * p.M + m) * p.N + n) = v;
+    } else {
       const float sa = p.a_scales[m];
-      // b_scales may start at any 4-byte boundary: four single loads.
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = v[e] * sa * p.b_scales[n + e];
       store4<OUT>(p.C, (int64_t)m * p.ldc + n, v);
@@ -139,14 +313,6 @@ __global__ void __launch_bounds__(64 * WAVES) gemm_fp8_skinny_kernel(Fp8Params p
 // are zeroed there, so that chunk's finite values add nothing, and a NaN in it
 // is in the row's product anyway.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void dma_block_at(const uint8_t* base, uint32_t offset,
-                                             uint32_t lds_base) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-               :
-               : "v"(offset), "s"(base), "{m0}"(lds_base)
-               : "memory");
-}
-
 constexpr int kFp8StageK = 128;
 constexpr int kFp8Staging = 4096;   // bytes of a wave's part of the epilogue
 
@@ -162,11 +328,6 @@ struct Out16<1> {
 };
 // Four floats at any 4-byte boundary.
 typedef float f32x4_by4 __attribute__((ext_vector_type(4), aligned(4)));
-
-template <int T>
-struct Step {
-  static constexpr int value = T;
-};
 
 template <int FM, int FN, int WM, int WN, int S>
 struct Fp8Tile {
@@ -460,59 +621,88 @@ __global__ void __launch_bounds__(256) gemm_fp8_join_kernel(Fp8Params p) {
 // ---------------------------------------------------------------------------
 // Choice of kernel.
 // ---------------------------------------------------------------------------
-enum Fp8Kind { kSkinny, kTile128, kTile256 };
+enum Fp8Kind { kVec, kRows, kTile128, kTile256 };
 
 struct Fp8Plan {
   Fp8Kind kind;
   int tiles_m, tiles_n, splits, steps;
+  bool wide;   // kRows: 64 columns
 };
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
+// Equal shares of `steps` stages for at most `most` workgroups a tile, `least`
+// stages each; no share is empty.
+int shares(int steps, int64_t most, int least) {
+  int64_t n = most < steps / least ? most : steps / least;
+  if (n <= 1) return 1;
+  return ceil_div(steps, ceil_div(steps, n));
+}
+
 Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K) {
-  Fp8Plan c{kSkinny, 0, 0, 1, ceil_div(K, kFp8StageK)};
-  if (M <= 64) return c;
+  Fp8Plan c{kVec, 0, 0, 1, 0, false};
+  if (M <= 4) return c;
+  if (M <= 64) {
+    c.kind = kRows;
+    c.tiles_m = 1;
+    c.wide = N > 192 * 64;
+    c.tiles_n = ceil_div(N, c.wide ? 64 : 32);
+    c.steps = ceil_div(K, kRowsStageK);
+    c.splits = c.tiles_n < 96 ? shares(c.steps, 192 / c.tiles_n, 2) : 1;
+    return c;
+  }
+  c.steps = ceil_div(K, kFp8StageK);
   const int64_t big = (int64_t)ceil_div(M, 256) * ceil_div(N, 256);
   const int tile = big >= 256 ? 256 : 128;
   c.kind = tile == 256 ? kTile256 : kTile128;
   c.tiles_m = ceil_div(M, tile);
   c.tiles_n = ceil_div(N, tile);
-  if (tile == 128) {
-    // Fill the 512 places for workgroups (two a CU) by splitting K, 4 stages a
-    // split at least.
-    const int64_t tiles = (int64_t)c.tiles_m * c.tiles_n;
-    int splits = (int)(512 / tiles);
-    splits = splits < c.steps / 4 ? splits : c.steps / 4;
-    splits = splits > 16 ? 16 : splits;
-    if (splits > 1) {
-      const int per = ceil_div(c.steps, splits);
-      c.splits = ceil_div(c.steps, per);  // no empty split
-    }
-  }
+  // Small tiles: 512 places for workgroups (two a CU), filled by splitting K.
+  if (tile == 128) c.splits = shares(c.steps, 512 / ((int64_t)c.tiles_m * c.tiles_n), 4);
   return c;
 }
 
+template <int MM, int LPR, int OUT>
+hipError_t launch_fp8_vec(const Fp8Params& p, hipStream_t stream) {
+  constexpr int kRows = kVecRows * (64 / LPR);
+  const int slices = LPR < 64 ? 1 : ceil_div(p.K, kVecSlice);
+  const int waves = ceil_div(slices, ceil_div(slices, kVecWaves));
+  hipLaunchKernelGGL((gemv_fp8_kernel<MM, LPR, OUT>), long_grid(((int64_t)p.N + kRows - 1) / kRows),
+                     dim3(64 * waves), 0, stream, p);
+  return hipGetLastError();
+}
+
+// As many lanes a row as K has 16-byte chunks, up to a wave.
+template <int MM, int OUT>
+hipError_t launch_fp8_vec_k(const Fp8Params& p, hipStream_t stream) {
+  if (p.K <= 16 * 16) return launch_fp8_vec<MM, 16, OUT>(p, stream);
+  if (p.K <= 32 * 16) return launch_fp8_vec<MM, 32, OUT>(p, stream);
+  return launch_fp8_vec<MM, 64, OUT>(p, stream);
+}
+
 template <int OUT>
-hipError_t launch_fp8_out(const Fp8Params& p, Fp8Kind kind, hipStream_t stream) {
-  if (kind == kSkinny) {
-    const auto grid = [&](int mt, int nt) {
-      return long_grid((int64_t)ceil_div(p.N, 16 * nt) * ceil_div(p.M, 16 * mt));
-    };
-    if (p.M <= 16)
-      hipLaunchKernelGGL((gemm_fp8_skinny_kernel<1, 1, 8, OUT>), grid(1, 1), dim3(512), 0, stream, p);
-    else if (p.M <= 32)
-      hipLaunchKernelGGL((gemm_fp8_skinny_kernel<2, 2, 8, OUT>), grid(2, 2), dim3(512), 0, stream, p);
-    else
-      hipLaunchKernelGGL((gemm_fp8_skinny_kernel<4, 2, 8, OUT>), grid(4, 2), dim3(512), 0, stream, p);
-    return hipGetLastError();
-  }
+hipError_t launch_fp8_out(const Fp8Params& p, Fp8Kind kind, bool wide, hipStream_t stream) {
   const int items = p.tiles_m * p.tiles_n * p.splits;
-  if (kind == kTile256)
-    hipLaunchKernelGGL((gemm_fp8_tile_kernel<4, 2, 2, 4, 2, 1, OUT>), dim3(items < 256 ? items : 256),
-                       dim3(512), 0, stream, p);
-  else
-    hipLaunchKernelGGL((gemm_fp8_tile_kernel<2, 2, 2, 2, 2, 2, OUT>), dim3(items < 512 ? items : 512),
-                       dim3(256), 0, stream, p);
+  switch (kind) {
+    case kVec:
+      if (p.M == 1) return launch_fp8_vec_k<1, OUT>(p, stream);
+      if (p.M == 2) return launch_fp8_vec_k<2, OUT>(p, stream);
+      return launch_fp8_vec_k<4, OUT>(p, stream);
+    case kRows: {
+      void (*k)(Fp8Params) =
+          p.M <= 32 ? (wide ? gemm_fp8_rows_kernel<1, 2, OUT> : gemm_fp8_rows_kernel<1, 1, OUT>)
+                    : (wide ? gemm_fp8_rows_kernel<2, 2, OUT> : gemm_fp8_rows_kernel<2, 1, OUT>);
+      hipLaunchKernelGGL(k, long_grid(items), dim3(512), 0, stream, p);
+      break;
+    }
+    case kTile128:
+      hipLaunchKernelGGL((gemm_fp8_tile_kernel<2, 2, 2, 2, 2, 2, OUT>),
+                         dim3(items < 512 ? items : 512), dim3(256), 0, stream, p);
+      break;
+    default:
+      hipLaunchKernelGGL((gemm_fp8_tile_kernel<4, 2, 2, 4, 2, 1, OUT>),
+                         dim3(items < 256 ? items : 256), dim3(512), 0, stream, p);
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   const int64_t quads = (int64_t)p.M * (p.N / 4);
@@ -534,9 +724,9 @@ hipError_t launch_gemm_fp8(Fp8Params p, int out_type, hipStream_t stream) {
   p.tiles_n = c.tiles_n;
   p.splits = c.splits;
   p.steps = c.steps;
-  if (out_type == 0) return launch_fp8_out<0>(p, c.kind, stream);
-  if (out_type == 1) return launch_fp8_out<1>(p, c.kind, stream);
-  return launch_fp8_out<2>(p, c.kind, stream);
+  if (out_type == 0) return launch_fp8_out<0>(p, c.kind, c.wide, stream);
+  if (out_type == 1) return launch_fp8_out<1>(p, c.kind, c.wide, stream);
+  return launch_fp8_out<2>(p, c.kind, c.wide, stream);
 }
 
 }  // namespace pipe

@@ -401,29 +401,6 @@ constexpr int kVecRows = 8;
 constexpr int kVecWaves = 8;    // at most, each with slices of K of its own
 constexpr int kVecSlice = 2048;
 
-// Sums over the 64 lanes of eight registers: each swap and addition halves the
-// registers and keeps, in each part of the lanes, another one's sums. Row
-// 4 q + {0, 2, 1, 3}[lane / 16] of the eight ends up in out[q].
-__device__ __forceinline__ void sum_rows(const float (&v)[8], float (&out)[2]) {
-  float h[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const u32x2 x = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[2 * i]),
-                                                     __float_as_uint(v[2 * i + 1]), false, false);
-    h[i] = __uint_as_float(x[0]) + __uint_as_float(x[1]);
-  }
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const u32x2 x = __builtin_amdgcn_permlane16_swap(__float_as_uint(h[2 * q]),
-                                                     __float_as_uint(h[2 * q + 1]), false, false);
-    float s = __uint_as_float(x[0]) + __uint_as_float(x[1]);
-    s = dpp_add<0x121, 0xF>(s);   // rotations within rows of 16 lanes
-    s = dpp_add<0x122, 0xF>(s);
-    s = dpp_add<0x124, 0xF>(s);
-    out[q] = dpp_add<0x128, 0xF>(s);
-  }
-}
-
 template <class T, int MM, int LPR, bool ZEROS>
 __global__ void __launch_bounds__(64 * kVecWaves) gemv_w4_kernel(W4Params p) {
   constexpr int kRowsPer = 64 / LPR;   // weight rows a load

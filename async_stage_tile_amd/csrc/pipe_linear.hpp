@@ -142,6 +142,29 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   return __builtin_amdgcn_readlane(v, 63);
 }
 
+// Sums over the 64 lanes of eight registers: each swap and addition halves the
+// registers and keeps, in each part of the lanes, another one's sums. Row
+// 4 q + {0, 2, 1, 3}[lane / 16] of the eight ends up in out[q].
+__device__ __forceinline__ void sum_rows(const float (&v)[8], float (&out)[2]) {
+  float h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const u32x2 x = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[2 * i]),
+                                                     __float_as_uint(v[2 * i + 1]), false, false);
+    h[i] = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+  }
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const u32x2 x = __builtin_amdgcn_permlane16_swap(__float_as_uint(h[2 * q]),
+                                                     __float_as_uint(h[2 * q + 1]), false, false);
+    float s = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+    s = dpp_add<0x121, 0xF>(s);   // rotations within rows of 16 lanes
+    s = dpp_add<0x122, 0xF>(s);
+    s = dpp_add<0x124, 0xF>(s);
+    out[q] = dpp_add<0x128, 0xF>(s);
+  }
+}
+
 // Store four consecutive outputs of type OUT (0 bf16, 1 fp16, 2 fp32).
 template <int OUT>
 __device__ __forceinline__ void store4(void* c, int64_t at, f32x4 v) {
