@@ -333,11 +333,11 @@ template <int FM, int FN, int WM, int WN, int S>
 struct Fp8Tile {
   static constexpr int kWaves = WM * WN;
   static constexpr int kRowsA = 32 * FM * WM, kRowsB = 32 * FN * WN;
-  static constexpr int kBlocksA = kRowsA / 8, kBlocksB = kRowsB / 8;
-  static constexpr int kLoads = (kBlocksA + kBlocksB) / kWaves;
+  static constexpr int kLoadsA = kRowsA / 8 / kWaves, kLoadsB = kRowsB / 8 / kWaves;
+  static constexpr int kLoads = kLoadsA + kLoadsB;   // blocks a wave and stage
   static constexpr int kStage = (kRowsA + kRowsB) * kFp8StageK;
-  static_assert((kBlocksA + kBlocksB) % kWaves == 0 && kBlocksA % kLoads == 0 && kLoads % 2 == 0,
-                "a wave loads whole blocks of one operand, an even number");
+  static_assert(kRowsA % (16 * kWaves) == 0 && kRowsB % (16 * kWaves) == 0,
+                "a wave loads an even number of blocks of each operand");
   static_assert(S * kStage + kWaves * kFp8Staging <= 163840, "the ring and the staging fit");
 };
 
@@ -374,15 +374,14 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_fp8_tile_kernel(Fp8
   const int per = (p.steps + p.splits - 1) / p.splits;
 
   // The stream of stages that this wave fetches, over all the workgroup's
-  // items: kLoads blocks of A's, or of B's, a stage.
-  const bool load_a = wave * Tile::kLoads < Tile::kBlocksA;
-  const int block0 = wave * Tile::kLoads - (load_a ? 0 : Tile::kBlocksA);
-  const int64_t ld = load_a ? p.lda : p.ldb;
-  const uint32_t mine = base + wave * Tile::kLoads * kBlockBytes;
-  // In block j, lane l loads the chunk that lies at place l % 8 of row l / 8.
-  const int chunk0 = (lane & 7) ^ (lane >> 4) ^ ((block0 & 1) << 2);
+  // items: kLoadsA blocks of A and kLoadsB of B a stage.
+  const uint32_t mine_a = base + wave * Tile::kLoadsA * kBlockBytes;
+  const uint32_t mine_b = base + (Tile::kRowsA / 8 + wave * Tile::kLoadsB) * kBlockBytes;
+  // In a block, lane l loads the chunk that lies at place l % 8 of row l / 8;
+  // this is the even blocks', odd ones' differs in one bit.
+  const int chunk0 = (lane & 7) ^ (lane >> 4);
   int f_item = (int)blockIdx.x, f_stage, f_last;   // the item and stage that the next loads fetch
-  const uint8_t* g;
+  const uint8_t *ga, *gb;
   uint32_t off[Tile::kLoads], shift[2];
   auto set_shift = [&](int tail) {   // tail: bytes of K in the stage
 #pragma unroll
@@ -395,23 +394,29 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_fp8_tile_kernel(Fp8
   auto open = [&]() {
     int tm, tn, split;
     fp8_item(p, f_item, items, tm, tn, split);
-    const int row0 = load_a ? tm * Tile::kRowsA : tn * Tile::kRowsB;
-    const int rows = (load_a ? p.M : p.N) - row0;   // rows of the tile, and more
+    const int row_a = tm * Tile::kRowsA, row_b = tn * Tile::kRowsB;
 #pragma unroll
-    for (int j = 0; j < Tile::kLoads; ++j)
-      off[j] = (uint32_t)min((block0 + j) * 8 + (lane >> 3), rows - 1) * (uint32_t)ld +
-               (uint32_t)(chunk0 ^ ((j & 1) << 2)) * 16;
+    for (int j = 0; j < Tile::kLoads; ++j) {
+      const bool of_a = j < Tile::kLoadsA;
+      const int q = of_a ? j : j - Tile::kLoadsA;   // block of the wave's, even with j
+      const int r = (wave * (of_a ? Tile::kLoadsA : Tile::kLoadsB) + q) * 8 + (lane >> 3);
+      off[j] = (uint32_t)(of_a ? min(r, p.M - row_a - 1) : min(r, p.N - row_b - 1)) *
+                   (uint32_t)(of_a ? p.lda : p.ldb) +
+               (uint32_t)(chunk0 ^ ((q & 1) << 2)) * 16;
+    }
     f_k = split * per * kFp8StageK;
     f_stage = 0;
     f_last = min(per, p.steps - split * per) - 1;   // >= 0: the host leaves no split empty
-    g = (load_a ? p.A : p.B) + row0 * ld + f_k;
+    ga = p.A + row_a * p.lda + f_k;
+    gb = p.B + row_b * p.ldb + f_k;
     set_shift(p.K - f_k);
   };
   auto advance = [&]() {
     if (f_stage < f_last) {
       ++f_stage;
       f_k += kFp8StageK;
-      g += kFp8StageK;
+      ga += kFp8StageK;
+      gb += kFp8StageK;
       if (f_stage == f_last) set_shift(p.K - f_k);
     } else if (f_item + (int)gridDim.x < items) {
       f_item += (int)gridDim.x;
@@ -419,7 +424,11 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_fp8_tile_kernel(Fp8
     }
   };
   auto load = [&](int slot, int j) {
-    dma_block_at(g, off[j] - shift[j & 1], mine + slot * Tile::kStage + j * kBlockBytes);
+    if (j < Tile::kLoadsA)
+      dma_block_at(ga, off[j] - shift[j & 1], mine_a + slot * Tile::kStage + j * kBlockBytes);
+    else
+      dma_block_at(gb, off[j] - shift[(j - Tile::kLoadsA) & 1],
+                   mine_b + slot * Tile::kStage + (j - Tile::kLoadsA) * kBlockBytes);
   };
   // Row 32 i + li of a wave's rows: (r >> 1) & 7 is (li >> 1) & 7 for every i.
   const uint8_t* frag_a = &ring[0][0] + (wm * FM * 32 + li) * kFp8StageK;
@@ -621,7 +630,7 @@ __global__ void __launch_bounds__(256) gemm_fp8_join_kernel(Fp8Params p) {
 // ---------------------------------------------------------------------------
 // Choice of kernel.
 // ---------------------------------------------------------------------------
-enum Fp8Kind { kVec, kRows, kTile128, kTile256 };
+enum Fp8Kind { kVec, kRows, kTile128, kTile128Pair, kTile192, kTile256 };
 
 struct Fp8Plan {
   Fp8Kind kind;
@@ -651,14 +660,41 @@ Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K) {
     c.splits = c.tiles_n < 96 ? shares(c.steps, 192 / c.tiles_n, 2) : 1;
     return c;
   }
+  // The tile kernels: of all tile shapes and splits of K, the least estimate of
+  // time. A workgroup takes so many us a stage with every CU at work (8192^3 and
+  // 2048 x 4096 x 4096, measured): a tile of 256 x 256 1.63, of 192 x 128 0.70,
+  // of 128 x 128 alone on its CU 0.56, two of these on one CU 0.95 together.
+  // Partial products cost 2 us, and 8 bytes each at 8 TB/s.
+  struct Shape {
+    Fp8Kind kind;
+    int rows, cols, places, most;   // most: splits of K
+    float us;
+  };
+  static constexpr Shape kShapes[] = {{kTile256, 256, 256, 256, 1, 1.63f},
+                                      {kTile192, 192, 128, 256, 8, 0.70f},
+                                      {kTile128, 128, 128, 256, 16, 0.56f},
+                                      {kTile128Pair, 128, 128, 512, 16, 0.95f}};
   c.steps = ceil_div(K, kFp8StageK);
-  const int64_t big = (int64_t)ceil_div(M, 256) * ceil_div(N, 256);
-  const int tile = big >= 256 ? 256 : 128;
-  c.kind = tile == 256 ? kTile256 : kTile128;
-  c.tiles_m = ceil_div(M, tile);
-  c.tiles_n = ceil_div(N, tile);
-  // Small tiles: 512 places for workgroups (two a CU), filled by splitting K.
-  if (tile == 128) c.splits = shares(c.steps, 512 / ((int64_t)c.tiles_m * c.tiles_n), 4);
+  float best = 0.f;
+  for (const Shape& sh : kShapes) {
+    const int tiles_m = ceil_div(M, sh.rows), tiles_n = ceil_div(N, sh.cols);
+    const int64_t tiles = (int64_t)tiles_m * tiles_n;
+    for (int want = 1; want <= sh.most; ++want) {
+      const int splits = shares(c.steps, want, 4);
+      if (splits != want) continue;
+      const int64_t rounds = (tiles * splits + sh.places - 1) / sh.places;
+      float t = (float)rounds * (float)ceil_div(c.steps, splits) * sh.us;
+      if (splits > 1) t += 2.f + (float)splits * (float)M * (float)N * 1e-6f;
+      if (best == 0.f || t < best) {
+        best = t;
+        c.kind = sh.kind;
+        c.tiles_m = tiles_m;
+        c.tiles_n = tiles_n;
+        c.splits = splits;
+      }
+      if (tiles * splits >= sh.places) break;
+    }
+  }
   return c;
 }
 
@@ -696,8 +732,16 @@ hipError_t launch_fp8_out(const Fp8Params& p, Fp8Kind kind, bool wide, hipStream
       break;
     }
     case kTile128:
+      hipLaunchKernelGGL((gemm_fp8_tile_kernel<2, 2, 2, 2, 4, 1, OUT>),
+                         dim3(items < 256 ? items : 256), dim3(256), 0, stream, p);
+      break;
+    case kTile128Pair:
       hipLaunchKernelGGL((gemm_fp8_tile_kernel<2, 2, 2, 2, 2, 2, OUT>),
                          dim3(items < 512 ? items : 512), dim3(256), 0, stream, p);
+      break;
+    case kTile192:
+      hipLaunchKernelGGL((gemm_fp8_tile_kernel<3, 2, 2, 2, 3, 1, OUT>),
+                         dim3(items < 256 ? items : 256), dim3(256), 0, stream, p);
       break;
     default:
       hipLaunchKernelGGL((gemm_fp8_tile_kernel<4, 2, 2, 4, 2, 1, OUT>),
