@@ -2,6 +2,12 @@
 // the 8-bit MFMAs (v_mfma_f32_16x16x128_f8f6f4 and 32x32x64, twice the rate of
 // the 16-bit and of the older 8-bit forms), fp32 sums.
 //
+// The 8-bit MFMAs keep fewer bits than fp32 while they add up their products:
+// sums come out 3e-5 off (of their norm, K 4096; the older 8-bit forms alike).
+// That is a sixteenth of fp16's rounding and less of bf16's, so 16-bit C takes
+// it. For fp32 C the same bytes are turned into fp16 values, exactly, and go
+// through the fp16 MFMAs, at half the rate: 7e-8 off.
+//
 // An MFMA multiplies the bytes that the two operands hold at the same place of
 // a lane, so any assignment of k's to places gives the same product as long as
 // both operands use it; the loads below choose the one that reads memory or
@@ -34,6 +40,36 @@ __device__ __forceinline__ void dma_block_at(const uint8_t* base, uint32_t offse
                : "memory");
 }
 
+// Two e4m3 values as fp16: the low or the high half of a word.
+__device__ __forceinline__ f16x2 e4m3_pair(uint32_t w, bool hi) {
+  return hi ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, true)
+            : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, false);
+}
+
+// acc + x y over 64 k's, of 32 rows each; exact products, and fp32 sums where C
+// is fp32 (OUT 2).
+template <int OUT>
+__device__ __forceinline__ f32x16 mma32(i32x8 x, i32x8 y, f32x16 acc) {
+  if constexpr (OUT != 2) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, acc, 0, 0, 0, 0, 0, 0);
+  } else {
+#pragma unroll
+    for (int t = 0; t < 8; t += 2) {
+      f16x8 a, b;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const f16x2 p = e4m3_pair(x[t + (e >> 1)], e & 1), q = e4m3_pair(y[t + (e >> 1)], e & 1);
+        a[2 * e] = p[0];
+        a[2 * e + 1] = p[1];
+        b[2 * e] = q[0];
+        b[2 * e + 1] = q[1];
+      }
+      acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, acc, 0, 0, 0);
+    }
+    return acc;
+  }
+}
+
 // ---------------------------------------------------------------------------
 // One to four rows of A. A lane keeps 16 k's of every row in registers, as fp16
 // pairs (e4m3 values are fp16 values), and meets them with the same k's of
@@ -46,11 +82,6 @@ __device__ __forceinline__ void dma_block_at(const uint8_t* base, uint32_t offse
 constexpr int kVecRows = 8;
 constexpr int kVecWaves = 8;    // at most, each with slices of K of its own
 constexpr int kVecSlice = 1024;
-
-__device__ __forceinline__ f16x2 e4m3_pair(uint32_t w, bool hi) {
-  return hi ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, true)
-            : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, false);
-}
 
 template <int MM, int LPR, int OUT>
 __global__ void __launch_bounds__(64 * kVecWaves) gemv_fp8_kernel(Fp8Params p) {
@@ -112,9 +143,7 @@ __global__ void __launch_bounds__(64 * kVecWaves) gemv_fp8_kernel(Fp8Params p) {
     } else {
 #pragma unroll
       for (int r = 0; r < kVecRows; ++r) {
-        float v = acc[m][r];
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+        const float v = group_sum<LPR>(acc[m][r]);
         if (lane % LPR == 0) red[wave][m][r * kRowsPer + lane / LPR] = v;
       }
     }
@@ -235,8 +264,7 @@ __global__ void __launch_bounds__(512) gemm_fp8_rows_kernel(Fp8Params p) {
     for (int t = 0; t < kSteps; ++t)
 #pragma unroll
       for (int i = 0; i < FM; ++i)
-        acc[i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b[t], a[t][i], acc[i], 0, 0, 0, 0,
-                                                                 0, 0);
+        acc[i] = mma32<OUT>(b[t], a[t][i], acc[i]);
   };
 
   for (int i = 0; i < Tile::kSlots - 1; ++i) load(i, i);
@@ -469,8 +497,7 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_fp8_tile_kernel(Fp8
 #pragma unroll
     for (int at = 0; at < kBlocks; ++at) {
       const int i = at / FN, j = at % FN;
-      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b[j], a[i], acc[i][j], 0, 0, 0, 0,
-                                                                  0, 0);
+      acc[i][j] = mma32<OUT>(b[j], a[i], acc[i][j]);
 #pragma unroll
       for (int f = at * kReads / kBlocks; f < (at + 1) * kReads / kBlocks; ++f) {
         if (f < FM) na[f] = read(sa + f * 32 * kFp8StageK, t ^ 1);

@@ -487,9 +487,7 @@ __global__ void __launch_bounds__(64 * kVecWaves) gemv_w4_kernel(W4Params p) {
     } else {
 #pragma unroll
       for (int r = 0; r < kVecRows; ++r) {
-        float v = acc[m][r];
-#pragma unroll
-        for (int off = LPR / 2; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+        const float v = group_sum<LPR>(acc[m][r]);
         if (lane % LPR == 0) red[wave][m][r * kRowsPer + lane / LPR] = v;
       }
     }

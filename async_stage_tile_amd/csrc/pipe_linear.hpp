@@ -142,6 +142,21 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   return __builtin_amdgcn_readlane(v, 63);
 }
 
+// Sum over each aligned group of N lanes (8, 16 or 32), in every lane of it.
+template <int N>
+__device__ __forceinline__ float group_sum(float s) {
+  s = dpp_add<0xB1, 0xF>(s);    // quad permutations [1,0,3,2] and [2,3,0,1]
+  s = dpp_add<0x4E, 0xF>(s);
+  s = dpp_add<0x141, 0xF>(s);   // mirror of 8 lanes
+  if constexpr (N >= 16) s = dpp_add<0x140, 0xF>(s);   // mirror of 16
+  if constexpr (N >= 32) {
+    const u32x2 x = __builtin_amdgcn_permlane16_swap(__float_as_uint(s), __float_as_uint(s), false,
+                                                     false);
+    s = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+  }
+  return s;
+}
+
 // Sums over the 64 lanes of eight registers: each swap and addition halves the
 // registers and keeps, in each part of the lanes, another one's sums. Row
 // 4 q + {0, 2, 1, 3}[lane / 16] of the eight ends up in out[q].

@@ -254,7 +254,9 @@ def powers(n, seed):
 FP8_SHAPES = [(1, 8, 16), (1, 4096, 4096), (2, 24, 48), (15, 264, 400), (16, 256, 128), (17, 248, 1040), (24, 512, 2048),
               (33, 40, 4112), (64, 304, 256), (65, 136, 64), (66, 128, 8192), (128, 256, 4096), (129, 520, 1040),
               (200, 1000, 4112), (300, 2056, 272), (257, 264, 80), (130, 8, 16), (500, 504, 5008),
-              (4096, 4104, 192), (4100, 4096, 336), (8192, 2048, 64)]
+              (4096, 4104, 192), (4100, 4096, 336), (8192, 2048, 64), (2048, 3904, 272), (700, 2000, 6000),
+              (4096, 4096, 400), (8192, 4096, 144), (3, 520, 272), (4, 200, 512), (2, 72, 1040), (32, 13000, 1040),
+              (64, 12400, 528), (5, 1000, 16384)]
 
 
 @pytest.mark.parametrize("M,N,K", FP8_SHAPES)
@@ -288,6 +290,18 @@ def test_fp8_random(M, N, K, out):
     close(got, ref, tol, "C")
     got = pt.pipe_gemm_fp8(A, sa, W.t(), sb, out_dtype=out)
     assert torch.equal(got, pt.pipe_gemm_fp8(A, sa, W.t(), sb, out_dtype=out))
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 512, 4096), (24, 512, 4096), (60, 13000, 4096), (150, 512, 4096), (300, 1000, 8192),
+                                   (1000, 5000, 1040), (4096, 4096, 528)])
+def test_fp8_fp32_sums(M, N, K):
+    """fp32 C holds fp32 sums: the errors of K independent roundings add up to sqrt(K) * 2^-24 of the result's
+    norm, which sums of fewer bits pass many times over."""
+    A, W = normal((M, K), F32, 38).mul(30).to(E4), normal((N, K), F32, 39).mul(30).to(E4)
+    one = torch.ones(max(M, N), device=DEV)
+    ref = A.to(D) @ W.to(D).t()
+    got = pt.pipe_gemm_fp8(A, one[:M], W.t(), one[:N], out_dtype=F32).to(D)
+    assert float((got - ref).norm() / ref.norm()) <= K ** 0.5 * U
 
 
 @pytest.mark.parametrize("M,N,K", [(5, 72, 144), (40, 136, 528), (150, 200, 1040), (4096, 4104, 80)])
