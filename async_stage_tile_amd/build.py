@@ -3,6 +3,10 @@
 libpipetile.so -- all kernels + the C ABI of include/pipe_tile.h (the tile stream)
 and include/pipe_linear.h (the quantised linear layer's operators).
 
+_linear.so -- the linear layer's Python marshalling in C++ (csrc/linear_binding.cpp,
+host code against the installed torch's headers; the Python wrappers work
+without it, slower).
+
 Every translation unit compiles to its own object, in parallel; the stream
 kernel source is compiled once per group of stage counts. Then the library
 is linked and moved into place atomically.
@@ -22,6 +26,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpipetile.so")
+BINDING = os.path.join(PKG, "_linear.so")
 ARCH = "gfx950"
 
 # (source, object, extra defines)
@@ -82,13 +87,32 @@ def _link(units: list, out: str, verbose: bool) -> None:
     os.replace(tmp, out)
 
 
+def build_binding(verbose: bool = False) -> None:
+    import sysconfig
+
+    import torch
+    t = os.path.dirname(torch.__file__)
+    cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        raise RuntimeError("no C++ compiler found: one is required to build _linear.so")
+    tmp = BINDING + ".tmp"
+    _run([cxx, "-O2", "-std=c++17", "-fPIC", "-shared",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          "-I", sysconfig.get_paths()["include"], "-I", os.path.join(t, "include"),
+          "-I", os.path.join(t, "include", "torch", "csrc", "api", "include"),
+          "-L", os.path.join(t, "lib"), "-o", tmp, os.path.join(CSRC, "linear_binding.cpp"),
+          "-ltorch_python", "-ltorch_cpu", "-lc10"], verbose)
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = False, jobs: int | None = None) -> str:
     os.makedirs(OBJ, exist_ok=True)
     units = UNITS
-    jobs = jobs or min(len(units), max(1, min(8, os.cpu_count() or 1)))
+    jobs = jobs or min(len(units) + 1, max(1, min(8, os.cpu_count() or 1)))
     with ThreadPoolExecutor(max_workers=jobs) as ex:
         futs = [ex.submit(_run, compile_command(s, os.path.join(OBJ, o), d), verbose)
                 for (s, o, d) in units]
+        futs.append(ex.submit(build_binding, verbose))
         for f in futs:
             f.result()
     _link(UNITS, LIB, verbose)

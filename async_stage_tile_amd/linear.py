@@ -10,6 +10,10 @@ done by the HIP kernels of the shared library, on the given stream or the
 current one. Outputs that are not given are allocated, and so are the
 workspaces that a shape needs. Wrong arguments raise TypeError or ValueError
 here, or PipeError with the library's status, and then nothing is enqueued.
+
+The common case (contiguous operands, outputs made here, the current stream)
+goes through ``_linear.so``, the same marshalling in C++, which the build makes
+next to the library; it hands back what it does not take.
 """
 from __future__ import annotations
 
@@ -41,6 +45,7 @@ _lock = threading.Lock()
 _torch = None
 _codes = {}         # torch dtype -> pipe_dtype_t
 _current_stream = None      # address of a device's current stream
+_fast = None                # the C++ marshalling, or None where it was not built
 
 
 def linear_symbols():
@@ -51,7 +56,7 @@ def linear_symbols():
 def _setup():
     """Loads the library once and binds the functions; torch is imported with
     the first call, as everywhere in this package."""
-    global _fns, _torch, _current_stream
+    global _fns, _torch, _current_stream, _fast
     with _lock:
         if _fns is None:
             L = _pt.lib()
@@ -72,6 +77,14 @@ def _setup():
             _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
                 lambda device: torch.cuda.current_stream(device).cuda_stream)
             _torch = torch
+            try:
+                from . import _linear as fast
+            except ImportError:     # not built, or for another Python
+                fast = None
+            if fast is not None:
+                fast.bind(_current_stream, *(
+                    _c.cast(getattr(fns, n), _V).value for n in _LINEAR_SIGS))
+            _fast = fast
             _fns = fns
     return _fns
 
@@ -153,6 +166,10 @@ def pipe_rmsnorm(x, weight, residual=None, eps=1e-6, out_dtype=None, y=None, y_s
     y, scales; with a residual the new stream h last: (y, h) or (y, scales, h).
     h may be x or residual itself to update the stream in place."""
     fns = _fns or _setup()
+    if _fast and stream is None and y is None and h is None and y_scales is None:
+        out = _fast.rmsnorm(x, weight, residual, eps, out_dtype)
+        if out is not NotImplemented:
+            return out
     dtype = _dtype16(x, "x")
     dev = x.get_device()
     M, N, ld_x = _matrix(x, "x", dtype, dev)
@@ -205,6 +222,10 @@ def pipe_rmsnorm_backward(dy, x, weight, dh=None, eps=1e-6, dx=None, dweight=Non
     that reaches h along the residual stream, added to dx before its rounding;
     dx is then the gradient of both addends."""
     fns = _fns or _setup()
+    if _fast and stream is None and dx is None and dweight is None and workspace is None:
+        out = _fast.rmsnorm_backward(dy, x, weight, dh, eps)
+        if out is not NotImplemented:
+            return out
     dtype = _dtype16(x, "x")
     dev = x.get_device()
     M, N, ld_x = _matrix(x, "x", dtype, dev)
@@ -273,6 +294,10 @@ def pipe_gemm_fp8(A, a_scales, B, b_scales, C=None, out_dtype=None, workspace=No
     stride (the transpose of a row-major (N, K) weight); scales: float32 of M
     and N elements. C: bfloat16 (the default), float16 or float32."""
     fns = _fns or _setup()
+    if _fast and stream is None and C is None and workspace is None:
+        out = _fast.gemm_fp8(A, a_scales, B, b_scales, out_dtype)
+        if out is not NotImplemented:
+            return out
     e4m3 = _torch.float8_e4m3fn
     dev = A.get_device() if isinstance(A, _torch.Tensor) else -1
     M, K, lda = _matrix(A, "A", e4m3, dev)
@@ -318,6 +343,10 @@ def pipe_gemm_w4(A, codes, scales, zeros=None, C=None, workspace=None, stream=No
     zeros: (N, K // group) uint8 of 0..15, None for 8 everywhere. The group
     size is K divided by the scales' columns: a power of two >= 32, or K."""
     fns = _fns or _setup()
+    if _fast and stream is None and C is None and workspace is None:
+        out = _fast.gemm_w4(A, codes, scales, zeros)
+        if out is not NotImplemented:
+            return out
     dtype = _dtype16(A, "A")
     dev = A.get_device()
     M, K, lda = _matrix(A, "A", dtype, dev)

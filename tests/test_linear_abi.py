@@ -168,3 +168,28 @@ def test_wrappers_refuse_host_tensors_and_wrong_types():
         pt.pipe_gemm_w4(x, torch.zeros(8, 32, dtype=torch.uint8), x[:, :1])
     with pytest.raises(TypeError):
         pt.pipe_gemm_w4(x.float(), torch.zeros(8, 32, dtype=torch.uint8), x[:, :1])
+
+
+def test_binding_is_built_and_hands_back_what_it_does_not_take():
+    """The C++ marshalling is in place (the build makes it), and gives host tensors, other types and other
+    arguments back to the Python wrappers, without an error set."""
+    linear._setup()
+    fast = linear._fast
+    assert fast is not None
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    w = torch.ones(64, dtype=torch.bfloat16)
+    e, f = torch.zeros(4, 64, dtype=torch.float8_e4m3fn), torch.ones(4)
+    q = torch.zeros(8, 32, dtype=torch.uint8)
+    for args in ((x, w, None, 1e-6, None), (None, w, None, 1e-6, None), (x, w, x, "eps", "type"), (x[0], w, None, 1e-6, None)):
+        assert fast.rmsnorm(*args) is NotImplemented
+    for args in ((x, x, w, None, 1e-6), (1, 2, 3, 4, 5)):
+        assert fast.rmsnorm_backward(*args) is NotImplemented
+    for args in ((e, f, e.t(), f, None), (x, f, e.t(), f, None), (e, f, e, f, 3)):
+        assert fast.gemm_fp8(*args) is NotImplemented
+    for args in ((x, q, x[:, :1], None), (x, None, None, None)):
+        assert fast.gemm_w4(*args) is NotImplemented
+    assert fast.gemm_w4(x) is NotImplemented and fast.rmsnorm() is NotImplemented
+    with pytest.raises(TypeError):
+        fast.bind(None)
+    with pytest.raises(ValueError):
+        fast.bind(None, 0, 0, 0, 0, 0, 0, 0)
