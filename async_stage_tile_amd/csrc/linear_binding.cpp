@@ -149,11 +149,12 @@ PyObject* grad(PyObject* const* a) {
   size_t bytes = 0;
   if (entry.grad_bytes(M, N, &bytes) != 0) return nullptr;
   const Tensor dx = make(*x, {M, N}, type), dw = make(*x, {N}, ScalarType::Float);
-  const Tensor ws = make(*x, {(int64_t)bytes}, ScalarType::Byte);
+  Tensor ws;
+  if (bytes > 0) ws = make(*x, {(int64_t)bytes}, ScalarType::Byte);
   const int status = enqueue([&] {
     return entry.grad(dy->const_data_ptr(), x->const_data_ptr(), w->const_data_ptr(),
                       dh ? dh->const_data_ptr() : nullptr, dx.data_ptr(), dw.data_ptr<float>(), M, N,
-                      N, N, N, N, (float)eps, code, ws.data_ptr(), bytes, stream);
+                      N, N, N, N, (float)eps, code, bytes > 0 ? ws.data_ptr() : nullptr, bytes, stream);
   });
   return status != 0 ? nullptr : pack({&dx, &dw});
 }

@@ -51,9 +51,8 @@ struct W4Params {
 // Each launcher takes what its entry point has checked. Types: 0 bf16, 1 fp16,
 // 2 fp32, 3 e4m3 (pipe_dtype_t).
 hipError_t launch_rmsnorm(const NormParams& p, int type, bool q8, hipStream_t stream);
-int64_t rmsnorm_grad_partials(int64_t M, int64_t N);
-hipError_t launch_rmsnorm_grad(const NormGradParams& p, float* dweight, int type,
-                               hipStream_t stream);
+int64_t rmsnorm_grad_partials(int64_t M, int64_t N);  // rows of N floats
+hipError_t launch_rmsnorm_grad(NormGradParams p, float* dweight, int type, hipStream_t stream);
 int64_t gemm_fp8_partials(int64_t M, int64_t N, int64_t K);  // floats of workspace
 hipError_t launch_gemm_fp8(Fp8Params p, int out_type, hipStream_t stream);
 int64_t gemm_w4_partials(int64_t M, int64_t N, int64_t K);  // floats of workspace

@@ -121,8 +121,10 @@ pipe_status_t pipe_rmsnorm_backward(const void* dy, const void* x, const void* w
     if (s != PIPE_OK) return s;
     if (weight == nullptr) return PIPE_ERR_NULL;
     if (!aligned(weight, 16)) return PIPE_ERR_ALIGN;
-    if (workspace == nullptr || workspace_bytes < need) return PIPE_ERR_WORKSPACE;
-    if (!aligned(workspace, 16)) return PIPE_ERR_ALIGN;
+    if (need > 0) {
+      if (workspace == nullptr || workspace_bytes < need) return PIPE_ERR_WORKSPACE;
+      if (!aligned(workspace, 16)) return PIPE_ERR_ALIGN;
+    }
   }
   NormGradParams p{};
   p.dy = static_cast<const uint8_t*>(dy);

@@ -366,16 +366,21 @@ __global__ void __launch_bounds__(256) rmsnorm_dweight_kernel(const float* __res
 }
 
 struct GradShape {
-  int rows;      // in flight a workgroup
+  bool tall;     // many rows: one row in flight a workgroup of 256 up to 8192 columns
   int64_t grid;
 };
 
-// Workgroups: two a CU (one of 1024 threads), and no more than there are rows to
-// start on, since each writes a row of partials.
+// Each workgroup writes a row of partials, so few rows want few workgroups with
+// several rows in flight each, of 1024 threads: 1021 x 8192 takes 22.5 us with
+// 256 of those and 26 with 512 of 256 threads, 8192 x 8192 100 and 95. A lone
+// workgroup writes dweight itself (a second turn of rows in it would already
+// cost the second kernel's time).
 GradShape grad_shape(int64_t M, int64_t chunks) {
   GradShape g;
-  g.rows = chunks <= 256 ? 4 : 1;
-  const int64_t need = (M + g.rows - 1) / g.rows, fill = chunks <= 1024 ? 512 : 256;
+  g.tall = chunks <= 256 || M >= 4096;
+  const int rows = chunks <= 256 ? 4 : g.tall ? 1 : chunks <= 512 ? 4 : chunks <= 1024 ? 2 : 1;
+  const int64_t need = (M + rows - 1) / rows;
+  const int64_t fill = g.tall && chunks <= 1024 ? 512 : 256;
   g.grid = need < fill ? need : fill;
   return g;
 }
@@ -389,14 +394,18 @@ hipError_t launch_grad_shape(const NormGradParams& p, int64_t grid, hipStream_t 
 }
 
 template <class T>
-hipError_t launch_grad_type(const NormGradParams& p, int64_t grid, hipStream_t stream) {
-  if (p.chunks <= 64) return launch_grad_shape<T, 64, 256, 1>(p, grid, stream);
-  if (p.chunks <= 128) return launch_grad_shape<T, 64, 256, 2>(p, grid, stream);
-  if (p.chunks <= 256) return launch_grad_shape<T, 64, 256, 4>(p, grid, stream);
-  if (p.chunks <= 512) return launch_grad_shape<T, 256, 256, 2>(p, grid, stream);
-  if (p.chunks <= 1024) return launch_grad_shape<T, 256, 256, 4>(p, grid, stream);
-  if (p.chunks <= 2048) return launch_grad_shape<T, 1024, 1024, 2>(p, grid, stream);
-  return launch_grad_shape<T, 1024, 1024, 4>(p, grid, stream);
+hipError_t launch_grad_type(const NormGradParams& p, const GradShape& g, hipStream_t stream) {
+  if (p.chunks <= 64) return launch_grad_shape<T, 64, 256, 1>(p, g.grid, stream);
+  if (p.chunks <= 128) return launch_grad_shape<T, 64, 256, 2>(p, g.grid, stream);
+  if (p.chunks <= 256) return launch_grad_shape<T, 64, 256, 4>(p, g.grid, stream);
+  if (p.chunks <= 512)
+    return g.tall ? launch_grad_shape<T, 256, 256, 2>(p, g.grid, stream)
+                  : launch_grad_shape<T, 256, 1024, 2>(p, g.grid, stream);
+  if (p.chunks <= 1024)
+    return g.tall ? launch_grad_shape<T, 256, 256, 4>(p, g.grid, stream)
+                  : launch_grad_shape<T, 512, 1024, 2>(p, g.grid, stream);
+  if (p.chunks <= 2048) return launch_grad_shape<T, 1024, 1024, 2>(p, g.grid, stream);
+  return launch_grad_shape<T, 1024, 1024, 4>(p, g.grid, stream);
 }
 
 }  // namespace
@@ -407,17 +416,17 @@ hipError_t launch_rmsnorm(const NormParams& p, int type, bool q8, hipStream_t st
 }
 
 int64_t rmsnorm_grad_partials(int64_t M, int64_t N) {
-  const GradShape g = grad_shape(M, N / 8);
-  return g.grid;
+  const int64_t grid = grad_shape(M, N / 8).grid;
+  return grid > 1 ? grid : 0;
 }
 
-hipError_t launch_rmsnorm_grad(const NormGradParams& p, float* dweight, int type,
-                               hipStream_t stream) {
+hipError_t launch_rmsnorm_grad(NormGradParams p, float* dweight, int type, hipStream_t stream) {
   const GradShape g = grad_shape(p.M, p.chunks);
   if (g.grid > 0) {
-    const hipError_t e = type == 0 ? launch_grad_type<__bf16>(p, g.grid, stream)
-                                   : launch_grad_type<_Float16>(p, g.grid, stream);
-    if (e != hipSuccess) return e;
+    if (g.grid == 1) p.partials = dweight;
+    const hipError_t e = type == 0 ? launch_grad_type<__bf16>(p, g, stream)
+                                   : launch_grad_type<_Float16>(p, g, stream);
+    if (e != hipSuccess || g.grid == 1) return e;
   }
   const int n = p.chunks * 8;
   hipLaunchKernelGGL(rmsnorm_dweight_kernel, dim3((n + 31) / 32), dim3(256), 0, stream, p.partials,

@@ -55,7 +55,8 @@ pipe_status_t pipe_rmsnorm(const void* x, const void* residual, const void* weig
                            int64_t ld_residual, int64_t ld_y, int64_t ld_h, float eps,
                            pipe_dtype_t type, pipe_dtype_t out_type, void* stream);
 
-/* Bytes of workspace pipe_rmsnorm_backward needs: fp32 partials of dweight. */
+/* Bytes of workspace pipe_rmsnorm_backward needs: fp32 partials of dweight,
+ * none for a few rows. */
 pipe_status_t pipe_rmsnorm_backward_workspace_bytes(int64_t M, int64_t N, size_t* bytes);
 
 /* Gradient of y = x * r * weight, r = rsqrt(mean(x^2) + eps), for the input x
@@ -67,7 +68,8 @@ pipe_status_t pipe_rmsnorm_backward_workspace_bytes(int64_t M, int64_t N, size_t
  * then the gradient of both x and residual of the forward call. dx may be dy
  * or dh itself with the same pitch. M == 0 gives dweight = 0; N == 0 is a
  * no-op. Shapes, pitches and alignment as above; dweight and workspace
- * 16-byte aligned. Two kernels are enqueued. */
+ * 16-byte aligned. One or two kernels are
+ * enqueued. */
 pipe_status_t pipe_rmsnorm_backward(const void* dy, const void* x, const void* weight,
                                     const void* dh, void* dx, float* dweight, int64_t M,
                                     int64_t N, int64_t ld_dy, int64_t ld_x, int64_t ld_dh,

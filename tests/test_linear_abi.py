@@ -68,8 +68,8 @@ def grad(dy=P, x=P, w=P, dh=0, dx=P, dw=P, M=4, N=64, lddy=64, ldx=64, lddh=64, 
     (dict(dy=0), pt.PIPE_ERR_NULL), (dict(x=0), pt.PIPE_ERR_NULL), (dict(dx=0), pt.PIPE_ERR_NULL),
     (dict(w=0), pt.PIPE_ERR_NULL), (dict(dw=0), pt.PIPE_ERR_NULL),
     (dict(dw=P + 4), pt.PIPE_ERR_ALIGN), (dict(dh=P + 2), pt.PIPE_ERR_ALIGN),
-    (dict(dh=P, lddh=68), pt.PIPE_ERR_ALIGN), (dict(ws=P + 4), pt.PIPE_ERR_ALIGN),
-    (dict(ws=0), pt.PIPE_ERR_WORKSPACE), (dict(wsb=16), pt.PIPE_ERR_WORKSPACE),
+    (dict(dh=P, lddh=68), pt.PIPE_ERR_ALIGN), (dict(M=100, ws=P + 4), pt.PIPE_ERR_ALIGN),
+    (dict(M=100, ws=0), pt.PIPE_ERR_WORKSPACE), (dict(M=100, wsb=16), pt.PIPE_ERR_WORKSPACE),
     (dict(N=0, dw=0, dy=0), pt.PIPE_OK),
 ])
 def test_rmsnorm_backward_refusals(change, status):
