@@ -1,6 +1,6 @@
 // Products of e4m3 rows with e4m3 weights: C = (A B) * a_scales * b_scales, on
-// the 8-bit MFMAs (v_mfma_f32_16x16x128_f8f6f4 and 32x32x64, twice the rate of
-// the 16-bit and of the older 8-bit forms), fp32 sums.
+// the 8-bit MFMAs (v_mfma_f32_32x32x64_f8f6f4, twice the rate of the 16-bit and
+// of the older 8-bit forms), fp32 sums.
 //
 // The 8-bit MFMAs keep fewer bits than fp32 while they add up their products:
 // sums come out 3e-5 off (of their norm, K 4096; the older 8-bit forms alike).
@@ -77,7 +77,9 @@ __device__ __forceinline__ f32x16 mma32(i32x8 x, i32x8 y, f32x16 acc) {
 // time (LPR lanes make up a row where K is shorter) and all loads of its rows
 // are in flight together. v_dot2 adds up two products at a time in fp32. The
 // MFMAs, which want 16 rows of B side by side and so 64-byte pieces of each,
-// streamed B at 3.6 TB/s where this reads 5.
+// streamed B at 3.6 TB/s where this reads 5 (8192 x 8192 in 12.7 us from HBM).
+// Bound by that read; at 4096 x 4096 (4.9 us, floor 2.6) by the launch and one
+// trip to memory.
 // ---------------------------------------------------------------------------
 constexpr int kVecRows = 8;
 constexpr int kVecWaves = 8;    // at most, each with slices of K of its own
@@ -174,7 +176,10 @@ __global__ void __launch_bounds__(64 * kVecWaves) gemv_fp8_kernel(Fp8Params p) {
 // end. One CU's ring holds about 100 KiB of loads in flight, which at the
 // memory's latency is 35 KB a us: what counts is that every CU has a tile, so
 // tiles are 32 columns wide up to N = 12288, and with fewer than 96 of them K
-// is split over workgroups too.
+// is split over workgroups too. 24 x 8192 x 8192 takes 15 to 20 us (67 MB: 3.3
+// to 4.5 TB/s). B's loads are non-temporal: 53 us for 8 x 16384 x 16384 where
+// cached ones take 60 (they win, 14 us for 17, only for weights that the
+// memory-side cache still holds from the call before).
 // ---------------------------------------------------------------------------
 constexpr int kRowsStageK = 512;
 
@@ -191,6 +196,16 @@ struct Fp8Rows {
   static_assert(kSlots >= 2 && kParts * 32 * FM * kPitch * 4 <= kSlots * kSlot, "LDS");
 };
 
+// Waits for the loads of stage ks of `count` in a ring of S slots, LOADS a stage
+// and wave: those of younger stages may stay under way.
+template <int S, int LOADS>
+__device__ __forceinline__ void wait_stage(int ks, int count) {
+  if (ks + S - 1 <= count)
+    wait_vmcnt<(S - 2) * LOADS>();
+  else
+    wait_vmcnt_mul<LOADS>(count - 1 - ks);
+}
+
 template <int FM, int WN, int OUT>
 __global__ void __launch_bounds__(512) gemm_fp8_rows_kernel(Fp8Params p) {
   using Tile = Fp8Rows<FM, WN>;
@@ -201,10 +216,10 @@ __global__ void __launch_bounds__(512) gemm_fp8_rows_kernel(Fp8Params p) {
   const int li = lane & 31, lh = lane >> 5;
   const int wn = wave % WN, wk = wave / WN;
   const uint32_t base = uniform(lds_addr(&lds[0]));
-  const int64_t wg = long_block();
-  if (wg >= (int64_t)p.tiles_n * p.splits) return;
-  const int split = (int)(wg / p.tiles_n), n0 = (int)(wg % p.tiles_n) * kN;
-  const int per = (p.steps + p.splits - 1) / p.splits;
+  if (long_block() >= p.tiles_n * p.splits) return;   // < 2^26: many splits only for few tiles
+  const int wg = (int)long_block();
+  const int split = p.splits == 1 ? 0 : wg / p.tiles_n, n0 = (wg - split * p.tiles_n) * kN;
+  const int per = p.splits == 1 ? p.steps : (p.steps + p.splits - 1) / p.splits;
   const int first = split * per, count = min(per, p.steps - first);   // >= 1
 
   const uint8_t* src[Tile::kLoads];
@@ -218,9 +233,10 @@ __global__ void __launch_bounds__(512) gemm_fp8_rows_kernel(Fp8Params p) {
                   : p.B + (int64_t)min(n0 + r, p.N - 1) * p.ldb;
     src_k[j] = 16 * ((lane & 31) ^ (r & 15));
   }
-  // Loads past K take the stage's first chunk, past the last stage that one again.
+  // Loads past K take the stage's first chunk.
   auto load = [&](int ks, int slot) {
-    const int k0 = (first + min(ks, count - 1)) * kRowsStageK;
+    if (ks >= count) return;
+    const int k0 = (first + ks) * kRowsStageK;
     const uint32_t to = base + slot * Tile::kSlot;
 #pragma unroll
     for (int j = 0; j < Tile::kLoads; ++j) {
@@ -270,7 +286,7 @@ __global__ void __launch_bounds__(512) gemm_fp8_rows_kernel(Fp8Params p) {
   for (int i = 0; i < Tile::kSlots - 1; ++i) load(i, i);
   int slot = 0;
   auto begin = [&](int ks) {
-    wait_vmcnt<(Tile::kSlots - 2) * Tile::kLoads>();   // those of younger stages
+    wait_stage<Tile::kSlots, Tile::kLoads>(ks, count);
     wait_lgkmcnt0();
     __syncthreads();
     load(ks + Tile::kSlots - 1, slot == 0 ? Tile::kSlots - 1 : slot - 1);
@@ -285,8 +301,7 @@ __global__ void __launch_bounds__(512) gemm_fp8_rows_kernel(Fp8Params p) {
     begin(whole);
     compute(slot, Step<1>{}, p.K - (first + whole) * kRowsStageK - 64 * kSteps * wk);
   }
-  // The last loads have landed and the last reads returned: the sums' place.
-  wait_vmcnt<0>();
+  // The last reads have returned (and the loads before them): the sums' place.
   wait_lgkmcnt0();
   __syncthreads();
   float* sums = reinterpret_cast<float*>(&lds[0]);
@@ -340,6 +355,12 @@ __global__ void __launch_bounds__(512) gemm_fp8_rows_kernel(Fp8Params p) {
 // last stage) load the row's chunk 0 of that stage instead, and A's fragments
 // are zeroed there, so that chunk's finite values add nothing, and a NaN in it
 // is in the row's product anyway.
+//
+// 8192^3 takes 423 us (2.6 PFLOP/s, MFMAs at work half the time at the 1.8 GHz
+// that the card holds under this load), bound by the LDS: its reads and writes
+// take as long as the MFMAs, and a stage 1.4 times as long as either. 1000 x
+// 5000 x 4112 takes 31 us in 240 tiles of 192 x 128, whose loads from L2, at
+// about 60 KB a us and CU, bind it.
 // ---------------------------------------------------------------------------
 constexpr int kFp8StageK = 128;
 constexpr int kFp8Staging = 4096;   // bytes of a wave's part of the epilogue

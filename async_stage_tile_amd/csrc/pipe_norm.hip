@@ -45,7 +45,10 @@ __device__ __forceinline__ void keep_packed(u32x4 (&v)[CH]) {
 }
 
 // One row per TPR threads, WG / TPR rows a workgroup; a thread holds CH chunks
-// of 8 elements, chunk index t + TPR * i.
+// of 8 elements, chunk index t + TPR * i. 8192 x 8192 with residual and e4m3
+// output takes 72 us in the kernel (6.5 TB/s, what a copy reaches); 1021 x 5000
+// 9 us (4.6 TB/s), where a launch and one trip to memory are half; one row of
+// 4096 2.2 us, the two alone.
 template <class T, int TPR, int WG, int CH, bool RES, bool Q8>
 __global__ void __launch_bounds__(WG) rmsnorm_kernel(NormParams p) {
   constexpr int kRows = WG / TPR, kRowWaves = TPR / 64;
@@ -192,7 +195,10 @@ hipError_t launch_norm_type(const NormParams& p, bool q8, hipStream_t stream) {
 }
 
 // ---------------------------------------------------------------------------
-// Gradient.
+// Gradient. A workgroup's rows are its grid stride's; 8192 x 8192 with the
+// residual stream's gradient takes 88 us (6.1 TB/s, bound by memory: a copy
+// reaches 6.5) and 4.9 for the sum of the partials, 1021 x 2048 5.8 and 3.4, of
+// which bytes are 2: launches, one trip to memory and two turns of rows.
 // ---------------------------------------------------------------------------
 template <class T, int TPR, int WG, int CH, bool RES>
 __global__ void __launch_bounds__(WG) rmsnorm_grad_kernel(NormGradParams p) {
@@ -342,7 +348,8 @@ __global__ void __launch_bounds__(WG) rmsnorm_grad_kernel(NormGradParams p) {
 
 // dweight: the partials' sum. A workgroup takes 32 columns (8 threads of four)
 // and 32 interleaved sets of partials, each summed in order, then the 32 sums
-// in order.
+// in order. 3.4 us for 256 partials of 2048 columns, 4.9 for 512 of 8192: a
+// launch, and chains of loads that the caches answer.
 __global__ void __launch_bounds__(256) rmsnorm_dweight_kernel(const float* __restrict__ partials,
                                                               float* __restrict__ dweight,
                                                               int count, int n) {
