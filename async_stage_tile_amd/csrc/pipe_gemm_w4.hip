@@ -93,18 +93,18 @@ __device__ __forceinline__ u32x4 expand_in_order(uint32_t codes) {
 }
 
 // ---------------------------------------------------------------------------
-// Five rows of A and more. A workgroup computes 16 MT rows of A times 128 weight
+// Five rows of A and more. A workgroup computes 16 MT rows of A times TN weight
 // rows; stages of 256 k pass through an LDS ring, filled by direct-to-LDS loads
-// alone, so that one wait count covers a stage: codes (128 rows of 128 bytes,
+// alone, so that one wait count covers a stage: codes (TN rows of 128 bytes,
 // 16-byte chunk c of row r at place c ^ ((r >> 1) & 7)) and A (rows of 512
 // bytes, chunk c of row r at c ^ (r & 15)). The scales and zero points of as
 // many stages as there is room for are copied to a table in LDS between stages,
 // a row's groups at a time: fetched stage by stage, they cost a cache line a row
 // for each few bytes, more requests than the codes themselves. Wave (wn, kh)
-// takes weight rows
-// 32 wn .. + 31 and part kh of the stage's k's; with the codes of 8 k's in one
-// LDS word, an MFMA step of 32 k's reads its operand as it lies: quarter q of
-// the lanes holds k = 8 q .. 8 q + 7. The parts' sums meet in LDS at the end.
+// takes weight rows 32 wn .. + 31 and part kh of the stage's k's; with the codes
+// of 8 k's in one LDS word, an MFMA step of 32 k's reads its operand as it lies:
+// quarter q of the lanes holds k = 8 q .. 8 q + 7. The parts' sums meet in LDS at
+// the end.
 //
 // One barrier a stage: at its top a wave's own loads of the stage have landed
 // and its reads of the stage before have returned. After the barrier that
@@ -119,56 +119,56 @@ __device__ __forceinline__ u32x4 expand_in_order(uint32_t codes) {
 //
 // Bound by turning codes into MFMA operands and by the MFMAs, S's among them,
 // on the way through each stage: 16 rows against 28672 x 8192 take 36 us (the
-// codes alone would take 19), 47 against 6000 x 4096 16.5, 4 of these the join.
+// codes alone would take 19). 47 against 6000 x 4096 take 15.7, of which 12 are
+// left without any of that: two launches, the ring's start, the join.
 // ---------------------------------------------------------------------------
 template <bool B>
 struct W4Flag {
   static constexpr bool value = B;
 };
 
-constexpr int kW4TileN = 128, kW4StageK = 256;
+constexpr int kW4StageK = 256, kW4Waves = 8;
 
-constexpr int kW4Parts = 2;   // waves along K, each with its part of a stage
-
-template <int MT, int F>
+template <int MT, int F, int TN>
 struct W4Tile {
-  static constexpr int kWaves = 4 * kW4Parts;
-  static constexpr int kSpan = kW4StageK / kW4Parts;         // k's of a part
+  static constexpr int kAcross = TN / 32;                  // waves along N, and along K:
+  static constexpr int kParts = kW4Waves / kAcross;
+  static constexpr int kSpan = kW4StageK / kParts;         // k's of a part
   static constexpr int kSum = F < kSpan ? F : kSpan;       // k's between two scalings
   static constexpr int kGroups = kW4StageK / F;            // groups of a stage
-  static constexpr int kCodes = kW4TileN * kW4StageK / 2;  // bytes of a slot's parts
+  static constexpr int kCodes = TN * kW4StageK / 2;  // bytes of a slot's parts
   static constexpr int kA = 16 * MT * kW4StageK * 2;
   static constexpr int kSlot = kCodes + kA;
-  static constexpr int kPitch = kW4TileN + 4;              // floats of a row of sums
+  static constexpr int kPitch = TN + 4;              // floats of a row of sums
   static constexpr int kLds = 163840;
   static constexpr int kFit = (kLds - 8192) / kSlot;
   static constexpr int kSlots = kFit > 5 ? 5 : kFit;
   static constexpr int kTable = kLds - kSlots * kSlot;     // scales (2 bytes), zero points (1)
-  static constexpr int kRoom = kTable / (3 * kW4TileN * kGroups);
+  static constexpr int kRoom = kTable / (3 * TN * kGroups);
   static constexpr int kChunk = kRoom < 32 ? kRoom : 32;   // stages of a table
   static constexpr int kChunkGroups = kChunk * kGroups;
-  static constexpr int kCodeLoads = 16 / kWaves, kALoads = 8 * MT / kWaves;
+  static constexpr int kCodeLoads = TN / 8 / kW4Waves, kALoads = MT;
   static constexpr int kLoads = kCodeLoads + kALoads;      // a wave and stage
   static_assert(kSlots >= 3 && kChunk >= 1 && 16 * MT * kPitch * 4 <= kSlots * kSlot, "LDS");
 };
 
-template <class T, int MT, int F, bool ZEROS>
-__global__ void __launch_bounds__(64 * 4 * kW4Parts) gemm_w4_tile_kernel(W4Params p) {
-  using Tile = W4Tile<MT, F>;
+template <class T, int MT, int F, int TN, bool ZEROS>
+__global__ void __launch_bounds__(64 * kW4Waves) gemm_w4_tile_kernel(W4Params p) {
+  using Tile = W4Tile<MT, F, TN>;
   constexpr int kSteps = Tile::kSpan / 32, kSums = Tile::kSpan / Tile::kSum;
   __shared__ __align__(1024) uint8_t lds[Tile::kLds];
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int lane = lane_id();
   const int li = lane & 15, lq = lane >> 4;
-  const int wn = wave & 3, kh = wave >> 2;
+  const int wn = wave % Tile::kAcross, kh = wave / Tile::kAcross;
   const uint32_t base = uniform(lds_addr(&lds[0]));
   const int64_t wg = long_block();
   // Neighbours share weight rows, then lie along N.
-  const int m_tiles = (p.M + 16 * MT - 1) / (16 * MT), n_tiles = (p.N + kW4TileN - 1) / kW4TileN;
+  const int m_tiles = (p.M + 16 * MT - 1) / (16 * MT), n_tiles = (p.N + TN - 1) / TN;
   if (wg >= (int64_t)m_tiles * n_tiles * p.splits) return;
   const int split = (int)(wg / ((int64_t)m_tiles * n_tiles));
   const int tile = (int)(wg % ((int64_t)m_tiles * n_tiles));
-  const int m0 = tile % m_tiles * (16 * MT), n0 = tile / m_tiles * kW4TileN;
+  const int m0 = tile % m_tiles * (16 * MT), n0 = tile / m_tiles * TN;
   const int stages = (p.K + kW4StageK - 1) / kW4StageK;
   const int per = (stages + p.splits - 1) / p.splits;
   const int first = split * per, count = min(per, stages - first);   // >= 1
@@ -205,17 +205,17 @@ __global__ void __launch_bounds__(64 * 4 * kW4Parts) gemm_w4_tile_kernel(W4Param
       dma_block(a_src[j] + 2 * (int64_t)k, to + Tile::kCodes + (wave * Tile::kALoads + j) * kBlockBytes);
     }
   };
-  // The table of the stages from ks on: this wave takes 128 / kWaves rows, 4 at
-  // a time, 16 groups of each. Group g of the table's n-th row lies at [g][n].
+  // The table of the stages from ks on: this wave takes an eighth of the rows,
+  // 4 at a time, 16 groups of each. Group g of the table's n-th row lies at [g][n].
   uint16_t* table_s = reinterpret_cast<uint16_t*>(&lds[Tile::kSlots * Tile::kSlot]);
-  uint8_t* table_z = reinterpret_cast<uint8_t*>(table_s + Tile::kChunkGroups * kW4TileN);
+  uint8_t* table_z = reinterpret_cast<uint8_t*>(table_s + Tile::kChunkGroups * TN);
   constexpr int kRounds = (Tile::kChunkGroups + 15) / 16;
   auto fill_table = [&](int ks) {
     const int g_end = min(Tile::kChunk, count - ks) * Tile::kGroups;
     for (int h = 0; h < kRounds && 16 * h < g_end; ++h) {
       const int g = 16 * h + li;
       const int at = min((first + ks) * kW4StageK + g * F, p.K - 1) >> p.group_shift;
-      constexpr int kQuads = 32 / Tile::kWaves;
+      constexpr int kQuads = TN / 4 / kW4Waves;
       uint16_t sv[kQuads];
       uint8_t zv[kQuads];
 #pragma unroll
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(64 * 4 * kW4Parts) gemm_w4_tile_kernel(W4Param
 #pragma unroll
       for (int r = 0; r < kQuads; ++r)
         if (g < g_end) {
-          const int to = g * kW4TileN + 4 * (kQuads * wave + r) + lq;
+          const int to = g * TN + 4 * (kQuads * wave + r) + lq;
           table_s[to] = sv[r];
           if constexpr (ZEROS) table_z[to] = zv[r];
         }
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(64 * 4 * kW4Parts) gemm_w4_tile_kernel(W4Param
     for (int f = 0; f < kSums; ++f)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int at = (table + (kh * Tile::kSpan + f * Tile::kSum) / F) * kW4TileN + 32 * wn + 16 * j + li;
+        const int at = (table + (kh * Tile::kSpan + f * Tile::kSum) / F) * TN + 32 * wn + 16 * j + li;
         scale[f][j] = Mma<T>::to_float(table_s[at]);
         zero[f][j] = ZEROS ? (float)table_z[at] : 8.f;
       }
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(64 * 4 * kW4Parts) gemm_w4_tile_kernel(W4Param
     return (16 * i + 4 * lq + e) * Tile::kPitch + 32 * wn + 16 * j + li;
   };
 #pragma unroll
-  for (int part = kW4Parts - 1; part >= 0; --part) {
+  for (int part = Tile::kParts - 1; part >= 0; --part) {
     if (kh == part) {
 #pragma unroll
       for (int i = 0; i < MT; ++i)
@@ -353,12 +353,12 @@ __global__ void __launch_bounds__(64 * 4 * kW4Parts) gemm_w4_tile_kernel(W4Param
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             sums[at(i, j, e)] =
-                part == kW4Parts - 1 ? acc[i][j][e] : acc[i][j][e] + sums[at(i, j, e)];
+                part == Tile::kParts - 1 ? acc[i][j][e] : acc[i][j][e] + sums[at(i, j, e)];
     }
     __syncthreads();
   }
-  for (int u = (int)threadIdx.x; u < 16 * MT * (kW4TileN / 8); u += 64 * Tile::kWaves) {
-    const int r = u / (kW4TileN / 8), c = u % (kW4TileN / 8) * 8;
+  for (int u = (int)threadIdx.x; u < 16 * MT * (TN / 8); u += 64 * kW4Waves) {
+    const int r = u / (TN / 8), c = u % (TN / 8) * 8;
     const int m = m0 + r, n = n0 + c;
     if (m >= p.M || n >= p.N) continue;
     const f32x4 lo = *reinterpret_cast<const f32x4*>(&sums[r * Tile::kPitch + c]);
@@ -537,14 +537,13 @@ hipError_t launch_w4_vec_k(const W4Params& p, hipStream_t stream) {
   return launch_w4_vec<T, MM, 64>(p, stream);
 }
 
-template <class T, int MT, int F>
+template <class T, int MT, int F, int TN>
 hipError_t launch_w4_tile(const W4Params& p, hipStream_t stream) {
-  const int64_t tiles = (((int64_t)p.N + kW4TileN - 1) / kW4TileN) *
-                        (((int64_t)p.M + 16 * MT - 1) / (16 * MT));
-  void (*k)(W4Params) = p.zeros != nullptr ? gemm_w4_tile_kernel<T, MT, F, true>
-                                           : gemm_w4_tile_kernel<T, MT, F, false>;
-  hipLaunchKernelGGL(k, long_grid(tiles * p.splits), dim3(64 * W4Tile<MT, F>::kWaves), 0, stream,
-                     p);
+  const int64_t tiles =
+      (((int64_t)p.N + TN - 1) / TN) * (((int64_t)p.M + 16 * MT - 1) / (16 * MT));
+  void (*k)(W4Params) = p.zeros != nullptr ? gemm_w4_tile_kernel<T, MT, F, TN, true>
+                                           : gemm_w4_tile_kernel<T, MT, F, TN, false>;
+  hipLaunchKernelGGL(k, long_grid(tiles * p.splits), dim3(64 * kW4Waves), 0, stream, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   hipLaunchKernelGGL(gemm_w4_join_kernel<T>, long_grid(((int64_t)p.M * (p.N / 8) + 255) / 256),
@@ -552,22 +551,31 @@ hipError_t launch_w4_tile(const W4Params& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <class T, int MT>
+template <class T, int MT, int TN>
 hipError_t launch_w4_group(const W4Params& p, hipStream_t stream) {
-  if (p.group_shift == 5) return launch_w4_tile<T, MT, 32>(p, stream);
-  if (p.group_shift == 6) return launch_w4_tile<T, MT, 64>(p, stream);
-  return launch_w4_tile<T, MT, 128>(p, stream);
+  if (p.group_shift == 5) return launch_w4_tile<T, MT, 32, TN>(p, stream);
+  if (p.group_shift == 6) return launch_w4_tile<T, MT, 64, TN>(p, stream);
+  return launch_w4_tile<T, MT, 128, TN>(p, stream);
 }
 
 // 16-row tiles of A that a workgroup of the tile kernel takes.
 int w4_m_tiles(int64_t M) { return M <= 16 ? 1 : M <= 32 ? 2 : M <= 48 ? 3 : 4; }
 
+int64_t w4_tiles(int64_t M, int64_t N, int64_t cols) {
+  const int64_t rows = 16 * w4_m_tiles(M);
+  return (N + cols - 1) / cols * ((M + rows - 1) / rows);
+}
+
+// 64 weight rows a tile while the CUs take all tiles at once: fewer splits of K
+// (47 x 6000 x 4096 15.7 us, 128 rows 16.9; 8 x 2048 x 11008 11.7 and 14.1). Else
+// 128, which read A half as often (64 x 28672 x 8192 60 us, 64 rows 72).
+int w4_cols(int64_t M, int64_t N) { return w4_tiles(M, N, 64) <= 256 ? 64 : 128; }
+
 // Workgroups that share a tile's K: as many as fill the CUs, two stages each
 // at least. One to four rows are the other kernel's, which needs none.
 int w4_splits(int64_t M, int64_t N, int64_t K) {
   if (M <= 4) return 1;
-  const int64_t mt = 16 * w4_m_tiles(M);
-  const int64_t tiles = (N + kW4TileN - 1) / kW4TileN * ((M + mt - 1) / mt);
+  const int64_t tiles = w4_tiles(M, N, w4_cols(M, N));
   const int64_t stages = (K + kW4StageK - 1) / kW4StageK;
   int64_t splits = tiles < 256 ? 256 / tiles : 1;
   splits = splits < stages / 2 ? splits : stages / 2;
@@ -581,11 +589,12 @@ hipError_t launch_w4_type(const W4Params& p, hipStream_t stream) {
   if (p.M == 1) return launch_w4_vec_k<T, 1>(p, stream);
   if (p.M == 2) return launch_w4_vec_k<T, 2>(p, stream);
   if (p.M <= 4) return launch_w4_vec_k<T, 4>(p, stream);
+  const bool narrow = w4_cols(p.M, p.N) == 64;
   switch (w4_m_tiles(p.M)) {
-    case 1: return launch_w4_group<T, 1>(p, stream);
-    case 2: return launch_w4_group<T, 2>(p, stream);
-    case 3: return launch_w4_group<T, 3>(p, stream);
-    default: return launch_w4_group<T, 4>(p, stream);
+    case 1: return narrow ? launch_w4_group<T, 1, 64>(p, stream) : launch_w4_group<T, 1, 128>(p, stream);
+    case 2: return narrow ? launch_w4_group<T, 2, 64>(p, stream) : launch_w4_group<T, 2, 128>(p, stream);
+    case 3: return narrow ? launch_w4_group<T, 3, 64>(p, stream) : launch_w4_group<T, 3, 128>(p, stream);
+    default: return narrow ? launch_w4_group<T, 4, 64>(p, stream) : launch_w4_group<T, 4, 128>(p, stream);
   }
 }
 
