@@ -2,8 +2,9 @@
 // a zero point for each group of K.
 //
 // For a few rows the call is bound by reading the weights once: N K / 2 bytes
-// of codes, for a few operations each. One to four rows of A meet them on the
-// vector units (gemv_w4_kernel); more rows on the MFMAs (gemm_w4_tile_kernel).
+// of codes, for a few operations each. One and two rows of A, and four of
+// smaller layers, meet them on the vector units (gemv_w4_kernel); more rows on
+// the MFMAs (gemm_w4_tile_kernel).
 //
 // Integers: a byte 0..15 is, read as e4m3, q * 2^-9 (the subnormals and the
 // first binade are evenly spaced), so one v_cvt_scalef32_pk with scale 2^9
@@ -93,7 +94,7 @@ __device__ __forceinline__ u32x4 expand_in_order(uint32_t codes) {
 }
 
 // ---------------------------------------------------------------------------
-// Five rows of A and more. A workgroup computes 16 MT rows of A times TN weight
+// More rows of A. A workgroup computes 16 MT rows of A times TN weight
 // rows; stages of 256 k pass through an LDS ring, filled by direct-to-LDS loads
 // alone, so that one wait count covers a stage: codes (TN rows of 128 bytes,
 // 16-byte chunk c of row r at place c ^ ((r >> 1) & 7)) and A (rows of 512
@@ -119,7 +120,7 @@ __device__ __forceinline__ u32x4 expand_in_order(uint32_t codes) {
 //
 // Bound by turning codes into MFMA operands and by the MFMAs, S's among them,
 // on the way through each stage: 16 rows against 28672 x 8192 take 36 us (the
-// codes alone would take 19). 47 against 6000 x 4096 take 15.7, of which 12 are
+// codes alone would take 19). 47 against 6000 x 4096 take 15.6, of which 12 are
 // left without any of that: two launches, the ring's start, the join.
 // ---------------------------------------------------------------------------
 template <bool B>
@@ -163,12 +164,14 @@ __global__ void __launch_bounds__(64 * kW4Waves) gemm_w4_tile_kernel(W4Params p)
   const int wn = wave % Tile::kAcross, kh = wave / Tile::kAcross;
   const uint32_t base = uniform(lds_addr(&lds[0]));
   const int64_t wg = long_block();
-  // Neighbours share weight rows, then lie along N.
+  // Neighbours share weight rows, then lie along N. Their number is below 2^31:
+  // the host checks the tiles', and K is split for fewer than 256 tiles only.
   const int m_tiles = (p.M + 16 * MT - 1) / (16 * MT), n_tiles = (p.N + TN - 1) / TN;
   if (wg >= (int64_t)m_tiles * n_tiles * p.splits) return;
-  const int split = (int)(wg / ((int64_t)m_tiles * n_tiles));
-  const int tile = (int)(wg % ((int64_t)m_tiles * n_tiles));
-  const int m0 = tile % m_tiles * (16 * MT), n0 = tile / m_tiles * TN;
+  const int split = p.splits == 1 ? 0 : (int)wg / (m_tiles * n_tiles);
+  const int tile = (int)wg - split * (m_tiles * n_tiles);
+  const int along = m_tiles == 1 ? tile : tile / m_tiles;
+  const int m0 = (tile - along * m_tiles) * (16 * MT), n0 = along * TN;
   const int stages = (p.K + kW4StageK - 1) / kW4StageK;
   const int per = (stages + p.splits - 1) / p.splits;
   const int first = split * per, count = min(per, stages - first);   // >= 1
@@ -567,18 +570,26 @@ int64_t w4_tiles(int64_t M, int64_t N, int64_t cols) {
 }
 
 // 64 weight rows a tile while the CUs take all tiles at once: fewer splits of K
-// (47 x 6000 x 4096 15.7 us, 128 rows 16.9; 8 x 2048 x 11008 11.7 and 14.1). Else
+// (47 x 6000 x 4096 15.6 us, 128 rows 16.9; 8 x 2048 x 11008 11.5 and 14.1). Else
 // 128, which read A half as often (64 x 28672 x 8192 60 us, 64 rows 72).
 int w4_cols(int64_t M, int64_t N) { return w4_tiles(M, N, 64) <= 256 ? 64 : 128; }
 
-// Workgroups that share a tile's K: as many as fill the CUs, two stages each
-// at least. One to four rows are the other kernel's, which needs none.
+// Whether the vector units take it: one or two rows, and three or four against
+// up to 3 * 2^25 weights (4 x 4096 x 4096 8.3 us, on the MFMAs 9.3; 4 x 8192 x
+// 8192 16.0 and 16.2; 4 x 28672 x 8192 43 and 35).
+bool w4_on_vector(int64_t M, int64_t N, int64_t K) {
+  return M <= 2 || (M <= 4 && N * K <= int64_t{3} << 25);
+}
+
+// Workgroups that share a tile's K: as many as fill the CUs, four stages each
+// at least (33 x 1024 x 8192 12.4 us, with two 13.4). The vector units' kernel
+// needs none.
 int w4_splits(int64_t M, int64_t N, int64_t K) {
-  if (M <= 4) return 1;
+  if (w4_on_vector(M, N, K)) return 1;
   const int64_t tiles = w4_tiles(M, N, w4_cols(M, N));
   const int64_t stages = (K + kW4StageK - 1) / kW4StageK;
   int64_t splits = tiles < 256 ? 256 / tiles : 1;
-  splits = splits < stages / 2 ? splits : stages / 2;
+  splits = splits < stages / 4 ? splits : stages / 4;
   if (splits <= 1) return 1;
   const int64_t per = (stages + splits - 1) / splits;
   return (int)((stages + per - 1) / per);   // no empty split
@@ -586,9 +597,11 @@ int w4_splits(int64_t M, int64_t N, int64_t K) {
 
 template <class T>
 hipError_t launch_w4_type(const W4Params& p, hipStream_t stream) {
-  if (p.M == 1) return launch_w4_vec_k<T, 1>(p, stream);
-  if (p.M == 2) return launch_w4_vec_k<T, 2>(p, stream);
-  if (p.M <= 4) return launch_w4_vec_k<T, 4>(p, stream);
+  if (w4_on_vector(p.M, p.N, p.K)) {
+    if (p.M == 1) return launch_w4_vec_k<T, 1>(p, stream);
+    if (p.M == 2) return launch_w4_vec_k<T, 2>(p, stream);
+    return launch_w4_vec_k<T, 4>(p, stream);
+  }
   const bool narrow = w4_cols(p.M, p.N) == 64;
   switch (w4_m_tiles(p.M)) {
     case 1: return narrow ? launch_w4_group<T, 1, 64>(p, stream) : launch_w4_group<T, 1, 128>(p, stream);

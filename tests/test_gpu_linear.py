@@ -387,6 +387,17 @@ def test_w4_exact_integers(M, N, K, G, dtype, zeros):
     assert torch.equal(pt.pipe_gemm_w4(A, codes, s, zeros=z), ref.to(dtype))
 
 
+# Wide layers, whose tiles are of 128 weight rows, also for three and four rows of many weights.
+W4_WIDE = [(5, 16520, 288, 32), (20, 16648, 256, 128), (33, 16456, 640, 64), (40, 16648, 512, 128), (64, 16400, 1056, 32),
+           (200, 5000, 320, 64), (3, 12312, 8192, 128), (4, 49160, 2080, 32)]
+
+
+@pytest.mark.parametrize("M,N,K,G", W4_WIDE)
+@pytest.mark.parametrize("dtype,zeros", [(BF, True), (HF, False)])
+def test_w4_wide_exact_integers(M, N, K, G, dtype, zeros):
+    test_w4_exact_integers(M, N, K, G, dtype, zeros)
+
+
 @pytest.mark.parametrize("M,N,K,G", [(1, 512, 4096, 128), (13, 264, 2048, 32), (30, 136, 1024, 64), (60, 264, 4096, 128)])
 @pytest.mark.parametrize("dtype", [BF, HF])
 def test_w4_random(M, N, K, G, dtype):
