@@ -171,15 +171,16 @@ __global__ void __launch_bounds__(64 * kVecWaves) gemv_fp8_kernel(Fp8Params p) {
 // Five to 64 rows: bound by reading B once, through few CUs' worth of tiles. A
 // workgroup of 8 waves computes 32 FM rows of A times 32 WN rows of B. Stages
 // of 512 k pass through an LDS ring (rows of 512 bytes, 16-byte chunk c of row
-// r at place c ^ (r & 15), 2 rows a direct-to-LDS block); wave (wn, wk) takes 32
-// rows of B and part wk of the stage's k's. The parts' sums meet in LDS at the
-// end. One CU's ring holds about 100 KiB of loads in flight, which at the
+// r at place c ^ (r & 15), 2 rows a direct-to-LDS block); wave (wn, wk) takes
+// 32 rows of B and part wk of the stage's k's. The parts' sums meet in LDS at
+// the end. One CU's ring holds about 100 KiB of loads in flight, which at the
 // memory's latency is 35 KB a us: what counts is that every CU has a tile, so
 // tiles are 32 columns wide up to N = 12288, and with fewer than 96 of them K
-// is split over workgroups too. 24 x 8192 x 8192 takes 15 to 20 us (67 MB: 3.3
-// to 4.5 TB/s). B's loads are non-temporal: 53 us for 8 x 16384 x 16384 where
-// cached ones take 60 (they win, 14 us for 17, only for weights that the
-// memory-side cache still holds from the call before).
+// is split over workgroups too. 24 x 8192 x 8192 takes 16 to 19 us (67 MB: 3.5
+// to 4.2 TB/s), and 15.5 without A's loads or the MFMAs: the read of B is all.
+// B's loads are non-temporal: 53 us for 8 x 16384 x 16384 where cached ones
+// take 60 (they win, 14 us for 17, only for weights that the memory-side cache
+// still holds from the call before).
 // ---------------------------------------------------------------------------
 constexpr int kRowsStageK = 512;
 
@@ -356,11 +357,11 @@ __global__ void __launch_bounds__(512) gemm_fp8_rows_kernel(Fp8Params p) {
 // are zeroed there, so that chunk's finite values add nothing, and a NaN in it
 // is in the row's product anyway.
 //
-// 8192^3 takes 423 us (2.6 PFLOP/s, MFMAs at work half the time at the 1.8 GHz
-// that the card holds under this load), bound by the LDS: its reads and writes
-// take as long as the MFMAs, and a stage 1.4 times as long as either. 1000 x
-// 5000 x 4112 takes 31 us in 240 tiles of 192 x 128, whose loads from L2, at
-// about 60 KB a us and CU, bind it.
+// 8192^3 takes 413 to 423 us (2.6 PFLOP/s): the MFMAs are at work 69 % of the
+// cycles, at the 1.7 GHz that the card holds under this load; the LDS's reads and
+// writes take about as many, and the two do not overlap wholly. 1000 x 5000 x
+// 4112 takes 31 us in 240 tiles of 192 x 128, whose loads from L2, at about 60 KB
+// a us and CU, bind it.
 // ---------------------------------------------------------------------------
 constexpr int kFp8StageK = 128;
 constexpr int kFp8Staging = 4096;   // bytes of a wave's part of the epilogue

@@ -68,8 +68,7 @@ pipe_status_t pipe_rmsnorm_backward_workspace_bytes(int64_t M, int64_t N, size_t
  * then the gradient of both x and residual of the forward call. dx may be dy
  * or dh itself with the same pitch. M == 0 gives dweight = 0; N == 0 is a
  * no-op. Shapes, pitches and alignment as above; dweight and workspace
- * 16-byte aligned. One or two kernels are
- * enqueued. */
+ * 16-byte aligned. One or two kernels are enqueued. */
 pipe_status_t pipe_rmsnorm_backward(const void* dy, const void* x, const void* weight,
                                     const void* dh, void* dx, float* dweight, int64_t M,
                                     int64_t N, int64_t ld_dy, int64_t ld_x, int64_t ld_dh,
@@ -88,7 +87,8 @@ pipe_status_t pipe_gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K, siz
  *   N % 8 == 0, K % 16 == 0, M arbitrary (else PIPE_ERR_SHAPE); M == 0 or
  *   N == 0 is a no-op, K == 0 gives C = 0 (scales unread). A, B, C bases
  *   16-byte aligned, lda and ldb multiples of 16 and below 2^24 (else
- *   PIPE_ERR_SHAPE), ldc a multiple of 8, scales 4-byte and the workspace 16-byte aligned (else PIPE_ERR_ALIGN). */
+ *   PIPE_ERR_SHAPE), ldc a multiple of 8, scales 4-byte and the workspace
+ *   16-byte aligned (else PIPE_ERR_ALIGN). */
 pipe_status_t pipe_gemm_fp8(const void* A, const float* a_scales, const void* B,
                             const float* b_scales, void* C, int64_t M, int64_t N, int64_t K,
                             int64_t lda, int64_t ldb, int64_t ldc, pipe_dtype_t out_type,
