@@ -2,9 +2,10 @@
 // a zero point for each group of K.
 //
 // For a few rows the call is bound by reading the weights once: N K / 2 bytes
-// of codes, for a few operations each. One and two rows of A, and four of
-// smaller layers, meet them on the vector units (gemv_w4_kernel); more rows on
-// the MFMAs (gemm_w4_tile_kernel).
+// of codes, for a few operations each. One row of A, or two, meets them on the
+// vector units (gemv_w4_kernel), up to eight on the small MFMAs
+// (gemm_w4_quad_kernel), more rows or weights on the large ones
+// (gemm_w4_tile_kernel).
 //
 // Integers: a byte 0..15 is, read as e4m3, q * 2^-9 (the subnormals and the
 // first binade are evenly spaced), so one v_cvt_scalef32_pk with scale 2^9
@@ -21,6 +22,9 @@
 namespace pipe {
 
 namespace {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
 template <class T>
 struct Mma;
@@ -40,6 +44,11 @@ struct Mma<__bf16> {
   static __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {
     return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a),
                                            __builtin_bit_cast(bf16x2, b), c, false);
+  }
+  static __device__ __forceinline__ f32x4 mfma4(uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1,
+                                                f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(__builtin_bit_cast(s16x4, u32x2{a0, a1}),
+                                                  __builtin_bit_cast(s16x4, u32x2{b0, b1}), c, 0, 0, 0);
   }
   static __device__ __forceinline__ float to_float(uint16_t v) { return Pair<__bf16>::lo(v); }
   static __device__ __forceinline__ uint32_t pack(float a, float b) { return Pair<__bf16>::pack(a, b); }
@@ -61,6 +70,11 @@ struct Mma<_Float16> {
     return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, a), __builtin_bit_cast(f16x2, b), c,
                                   false);
   }
+  static __device__ __forceinline__ f32x4 mfma4(uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1,
+                                                f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(f16x4, u32x2{a0, a1}),
+                                              __builtin_bit_cast(f16x4, u32x2{b0, b1}), c, 0, 0, 0);
+  }
   static __device__ __forceinline__ float to_float(uint16_t v) { return Pair<_Float16>::lo(v); }
   static __device__ __forceinline__ uint32_t pack(float a, float b) {
     return Pair<_Float16>::pack(a, b);
@@ -73,6 +87,13 @@ __device__ __forceinline__ u32x4 expand(uint32_t codes) {
   const uint32_t even = codes & 0x0F0F0F0Fu, odd = (codes >> 4) & 0x0F0F0F0Fu;
   return u32x4{Mma<T>::codes_lo(even), Mma<T>::codes_hi(even), Mma<T>::codes_lo(odd),
                Mma<T>::codes_hi(odd)};
+}
+
+// The value of the lane N places on among its 16, around.
+template <int N>
+__device__ __forceinline__ float rotate16(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v),
+                                                               0x120 + N, 0xf, 0xf, false));
 }
 
 // A's 8 values in the order of expand().
@@ -397,7 +418,7 @@ __global__ void __launch_bounds__(256) gemm_w4_join_kernel(W4Params p) {
 }
 
 // ---------------------------------------------------------------------------
-// One to four rows of A. A lane keeps the values of 32 k's of every row in
+// One or two rows of A. A lane keeps the values of 32 k's of every row in
 // registers (LPR lanes make up a row of weights, a wave's slice of K) and meets
 // them with the codes of kVecRows weight rows, one 16-byte load each: a wave
 // reads 1 KiB of a row at a time, and all loads of its rows are in flight
@@ -540,6 +561,149 @@ hipError_t launch_w4_vec_k(const W4Params& p, hipStream_t stream) {
   return launch_w4_vec<T, MM, 64>(p, stream);
 }
 
+// ---------------------------------------------------------------------------
+// Two to eight rows of A against smaller layers. v_mfma_f32_4x4x4 multiplies 16
+// blocks apart, four rows by four columns by four k's each: lane 4 b + j holds
+// values of A's row j and of weight row j, at the 32 k's of block b, that one
+// 16-byte load of codes brings. KB blocks lie along K, 64 / KB weight rows make
+// up a load, and a lane's 32 k's lie in one group, so scale and zero point are
+// applied to the block's product in the lane, sum_k a times the zero point by one
+// more product, against ones. No LDS on the way in, and the vector units only
+// expand the codes, where v_dot2 would take 8 cycles for every 128 products too:
+// 4 x 4096 x 4096 5.8 us (on v_dot2 7.7), 4 x 3544 x 22464 16.6 (25.2).
+// Bound by a launch and a trip to memory there, and by the reads, in pieces of
+// 256 bytes a row, on larger layers.
+// ---------------------------------------------------------------------------
+template <class T, int MM, int KB, int LOADS, bool ZEROS>
+__global__ void __launch_bounds__(64 * kVecWaves) gemm_w4_quad_kernel(W4Params p) {
+  constexpr int kRowsPer = 64 / KB;                  // weight rows a load
+  constexpr int kRows = LOADS * kRowsPer;       // of a workgroup
+  constexpr int kSlice = 32 * KB;                    // k's of a wave and turn
+  constexpr int kFours = (MM + 3) / 4;
+  __shared__ float red[kVecWaves][MM][LOADS][16];
+  const int lane = (int)(threadIdx.x & 63);
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int waves = (int)(blockDim.x >> 6);
+  const int j = lane & 3, block = lane >> 2;
+  const int64_t row0 = long_block() * kRows;
+  if (row0 >= p.N) return;
+  const int row = block / KB * 4 + j;                // of a load's rows
+  float acc[LOADS][MM];
+#pragma unroll
+  for (int r = 0; r < LOADS; ++r)
+#pragma unroll
+    for (int m = 0; m < MM; ++m) acc[r][m] = 0.f;
+  const uint8_t* a_row[kFours];
+#pragma unroll
+  for (int f = 0; f < kFours; ++f) a_row[f] = p.A + min(4 * f + j, p.M - 1) * p.lda;
+  const int slices = (p.K + kSlice - 1) / kSlice;
+  for (int slice = wave; slice < slices; slice += waves) {
+    const int k = slice * kSlice + block % KB * 32;
+    const bool in = k < p.K;
+    const int kk = in ? k : 0;        // past K: values of the row's start times zeros
+    const int g = kk >> p.group_shift;
+    u32x4 a[kFours][4], w[LOADS];
+    uint16_t s[LOADS];
+    uint8_t z[LOADS];
+#pragma unroll
+    for (int r = 0; r < LOADS; ++r) {
+      int64_t n = row0 + r * kRowsPer + row;
+      if (n > p.N - 1) n = p.N - 1;
+      w[r] = __builtin_nontemporal_load(
+          reinterpret_cast<const u32x4*>(p.codes + n * p.ld_codes + (kk >> 1)));
+      s[r] = p.scales[n * p.ld_scales + g];
+      if constexpr (ZEROS) z[r] = p.zeros[n * p.ld_zeros + g];
+    }
+#pragma unroll
+    for (int f = 0; f < kFours; ++f)
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        a[f][t] = *reinterpret_cast<const u32x4*>(a_row[f] + 2 * (int64_t)kk + 16 * t);
+    const f32x4 none = {0.f, 0.f, 0.f, 0.f};
+    f32x4 total[kFours];              // sums of the A values
+#pragma unroll
+    for (int f = 0; f < kFours; ++f) {
+      total[f] = none;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        a[f][t] = in ? even_odd(a[f][t]) : u32x4{0, 0, 0, 0};
+        total[f] = Mma<T>::mfma4(a[f][t][0], a[f][t][1], Mma<T>::kOnes, Mma<T>::kOnes, total[f]);
+        total[f] = Mma<T>::mfma4(a[f][t][2], a[f][t][3], Mma<T>::kOnes, Mma<T>::kOnes, total[f]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < LOADS; ++r) {
+      f32x4 part[kFours];
+#pragma unroll
+      for (int f = 0; f < kFours; ++f) part[f] = none;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const u32x4 q = expand<T>(w[r][t]);
+#pragma unroll
+        for (int f = 0; f < kFours; ++f) {
+          part[f] = Mma<T>::mfma4(a[f][t][0], a[f][t][1], q[0], q[1], part[f]);
+          part[f] = Mma<T>::mfma4(a[f][t][2], a[f][t][3], q[2], q[3], part[f]);
+        }
+      }
+      const float zp = ZEROS ? (float)z[r] : 8.f;
+      const float sc = in ? Mma<T>::to_float(s[r]) : 0.f;
+#pragma unroll
+      for (int m = 0; m < MM; ++m) acc[r][m] += sc * (part[m / 4][m % 4] - zp * total[m / 4][m % 4]);
+    }
+  }
+  // The sums of four blocks' lanes are added up here, those of 16-lane rows and
+  // waves below.
+#pragma unroll
+  for (int r = 0; r < LOADS; ++r)
+#pragma unroll
+    for (int m = 0; m < MM; ++m) {
+      float v = acc[r][m];
+      v += rotate16<4>(v);
+      v += rotate16<8>(v);
+      if ((block & 3) == 0) red[wave][m][r][(lane >> 4) * 4 + j] = v;
+    }
+  __syncthreads();
+  constexpr int kPairs = MM * kRows / 2;
+  uint32_t* C = reinterpret_cast<uint32_t*>(p.C);
+  for (int u = (int)threadIdx.x; u < kPairs; u += (int)blockDim.x) {
+    const int m = u / (kPairs / MM), at = u % (kPairs / MM) * 2;
+    const int64_t n = row0 + at;
+    if (m >= p.M || n >= p.N) continue;
+    const int r = at / kRowsPer, i = at % kRowsPer;
+    float lo = 0.f, hi = 0.f;
+    for (int v = 0; v < waves; ++v)
+#pragma unroll
+      for (int b = 0; b < KB / 4; ++b) {
+        const float* sum = &red[v][m][r][(i / 4 * (KB / 4) + b) * 4 + i % 4];
+        lo += sum[0];
+        hi += sum[1];
+      }
+    C[(m * p.ldc + n) >> 1] = Mma<T>::pack(lo, hi);
+  }
+}
+
+template <class T, int MM, int KB, int LOADS>
+hipError_t launch_w4_quad(const W4Params& p, hipStream_t stream) {
+  constexpr int kRows = LOADS * (64 / KB);
+  const int slices = (p.K + 32 * KB - 1) / (32 * KB);
+  const int turns = (slices + kVecWaves - 1) / kVecWaves;
+  const int waves = (slices + turns - 1) / turns;
+  void (*k)(W4Params) = p.zeros != nullptr ? gemm_w4_quad_kernel<T, MM, KB, LOADS, true>
+                                           : gemm_w4_quad_kernel<T, MM, KB, LOADS, false>;
+  hipLaunchKernelGGL(k, long_grid(((int64_t)p.N + kRows - 1) / kRows), dim3(64 * waves), 0, stream, p);
+  return hipGetLastError();
+}
+
+// Blocks along K: up to all 16. Four loads of codes for each of A's where that
+// leaves more than 128 workgroups, else two (8 x 1024 x 8192 10.5 us with four,
+// 8.5 with two; 8 x 4096 x 4096 7.1 and 8.2).
+template <class T, int MM>
+hipError_t launch_w4_quad_k(const W4Params& p, hipStream_t stream) {
+  if (p.K <= 8 * 32)
+    return p.N > 4096 ? launch_w4_quad<T, MM, 8, 4>(p, stream) : launch_w4_quad<T, MM, 8, 2>(p, stream);
+  return p.N > 2048 ? launch_w4_quad<T, MM, 16, 4>(p, stream) : launch_w4_quad<T, MM, 16, 2>(p, stream);
+}
+
 template <class T, int MT, int F, int TN>
 hipError_t launch_w4_tile(const W4Params& p, hipStream_t stream) {
   const int64_t tiles =
@@ -574,18 +738,24 @@ int64_t w4_tiles(int64_t M, int64_t N, int64_t cols) {
 // 128, which read A half as often (64 x 28672 x 8192 60 us, 64 rows 72).
 int w4_cols(int64_t M, int64_t N) { return w4_tiles(M, N, 64) <= 256 ? 64 : 128; }
 
-// Whether the vector units take it: one or two rows, and three or four against
-// up to 3 * 2^25 weights (4 x 4096 x 4096 8.3 us, on the MFMAs 9.3; 4 x 8192 x
-// 8192 16.0 and 16.2; 4 x 28672 x 8192 43 and 35).
-bool w4_on_vector(int64_t M, int64_t N, int64_t K) {
-  return M <= 2 || (M <= 4 && N * K <= int64_t{3} << 25);
+enum W4Kind { kW4Vec, kW4Quad, kW4Tile };
+
+// The vector units take one row, and two of more than 2^25 weights (2 x 28672 x
+// 8192 30 us, the small MFMAs 34; 2 x 4096 x 4096 5.7 and 4.9). The small MFMAs
+// take up to four rows of up to 3 * 2^25 weights (4 x 8192 x 8192 13.0 us, the
+// tiles 16.1; 4 x 28672 x 8192 38 and 35) and up to eight of 3 * 2^23 (8 x 4096 x
+// 4096 7.1 and 9.3; 8 x 8192 x 8192 21 and 17).
+W4Kind w4_kind(int64_t M, int64_t N, int64_t K) {
+  const int64_t weights = N * K;
+  if (M == 1 || (M == 2 && weights > int64_t{1} << 25)) return kW4Vec;
+  return weights <= int64_t{3} << (M <= 4 ? 25 : 23) && M <= 8 ? kW4Quad : kW4Tile;
 }
 
 // Workgroups that share a tile's K: as many as fill the CUs, four stages each
-// at least (33 x 1024 x 8192 12.4 us, with two 13.4). The vector units' kernel
-// needs none.
+// at least (33 x 1024 x 8192 12.4 us, with two 13.4). The other kernels need
+// none.
 int w4_splits(int64_t M, int64_t N, int64_t K) {
-  if (w4_on_vector(M, N, K)) return 1;
+  if (w4_kind(M, N, K) != kW4Tile) return 1;
   const int64_t tiles = w4_tiles(M, N, w4_cols(M, N));
   const int64_t stages = (K + kW4StageK - 1) / kW4StageK;
   int64_t splits = tiles < 256 ? 256 / tiles : 1;
@@ -597,10 +767,12 @@ int w4_splits(int64_t M, int64_t N, int64_t K) {
 
 template <class T>
 hipError_t launch_w4_type(const W4Params& p, hipStream_t stream) {
-  if (w4_on_vector(p.M, p.N, p.K)) {
-    if (p.M == 1) return launch_w4_vec_k<T, 1>(p, stream);
-    if (p.M == 2) return launch_w4_vec_k<T, 2>(p, stream);
-    return launch_w4_vec_k<T, 4>(p, stream);
+  const W4Kind kind = w4_kind(p.M, p.N, p.K);
+  if (kind == kW4Vec)
+    return p.M == 1 ? launch_w4_vec_k<T, 1>(p, stream) : launch_w4_vec_k<T, 2>(p, stream);
+  if (kind == kW4Quad) {
+    if (p.M == 2) return launch_w4_quad_k<T, 2>(p, stream);
+    return p.M <= 4 ? launch_w4_quad_k<T, 4>(p, stream) : launch_w4_quad_k<T, 8>(p, stream);
   }
   const bool narrow = w4_cols(p.M, p.N) == 64;
   switch (w4_m_tiles(p.M)) {

@@ -389,10 +389,16 @@ def test_w4_exact_integers(M, N, K, G, dtype, zeros):
 
 # Wide layers, whose tiles are of 128 weight rows, also for three and four rows of many weights.
 W4_WIDE = [(5, 16520, 288, 32), (20, 16648, 256, 128), (33, 16456, 640, 64), (40, 16648, 512, 128), (64, 16400, 1056, 32),
-           (200, 5000, 320, 64), (3, 12312, 8192, 128), (4, 49160, 2080, 32)]
+           (200, 5000, 320, 64), (3, 12312, 8192, 128), (4, 49160, 2080, 32), (5, 16520, 1600, 32),
+           (2, 4120, 8224, 32)]
 
 
-@pytest.mark.parametrize("M,N,K,G", W4_WIDE)
+# Two to eight rows: one or two turns through K, blocks that K leaves empty, both numbers of loads, ends of N.
+W4_FEW = [(2, 2056, 4096, 64), (3, 2072, 4608, 128), (4, 4104, 96, 32), (5, 2064, 160, 32), (6, 72, 8256, 64),
+          (7, 4112, 256, 256), (8, 1000, 5120, 128), (8, 3000, 8192, 1024), (4, 8, 32, 32), (2, 40, 64, 64)]
+
+
+@pytest.mark.parametrize("M,N,K,G", W4_WIDE + W4_FEW)
 @pytest.mark.parametrize("dtype,zeros", [(BF, True), (HF, False)])
 def test_w4_wide_exact_integers(M, N, K, G, dtype, zeros):
     test_w4_exact_integers(M, N, K, G, dtype, zeros)
