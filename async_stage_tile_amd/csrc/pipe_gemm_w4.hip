@@ -419,13 +419,11 @@ __global__ void __launch_bounds__(256) gemm_w4_join_kernel(W4Params p) {
 
 // ---------------------------------------------------------------------------
 // One or two rows of A. A lane keeps the values of 32 k's of every row in
-// registers (LPR lanes make up a row of weights, a wave's slice of K) and meets
-// them with the codes of kVecRows weight rows, one 16-byte load each: a wave
-// reads 1 KiB of a row at a time, and all loads of its rows are in flight
-// together. 1 x 28672 x 8192 takes 22 us (5.4 TB/s), bound by reading the codes
+// registers (a wave takes a slice of 2048) and meets them with the codes of
+// kVecRows weight rows, one 16-byte load each: a wave reads 1 KiB of a row at a
+// time, and all loads of its rows are in flight together. 1 x 28672 x 8192 takes 22 us (5.4 TB/s), bound by reading the codes
 // and then by turning them into floats (codes masked into the mantissa of a
-// large float instead: 27 us); 1 x 4096 x 4096 4.9 us, a launch and one trip to
-// memory. A lane's 32 k's lie in one group, whatever its size, so the scale
+// large float instead: 27 us). A lane's 32 k's lie in one group, whatever its size, so the scale
 // and the zero point are applied to the lane's own sum. v_dot2 adds up two
 // products at a time in fp32.
 // ---------------------------------------------------------------------------
@@ -433,24 +431,23 @@ constexpr int kVecRows = 8;
 constexpr int kVecWaves = 8;    // at most, each with slices of K of its own
 constexpr int kVecSlice = 2048;
 
-template <class T, int MM, int LPR, bool ZEROS>
+template <class T, int MM, bool ZEROS>
 __global__ void __launch_bounds__(64 * kVecWaves) gemv_w4_kernel(W4Params p) {
-  constexpr int kRowsPer = 64 / LPR;   // weight rows a load
-  __shared__ float red[kVecWaves][MM][kVecRows * kRowsPer];
+  __shared__ float red[kVecWaves][MM][kVecRows];
   const int lane = (int)(threadIdx.x & 63);
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int waves = (int)(blockDim.x >> 6);
   const int64_t wg = long_block();
-  const int64_t row0 = wg * (kVecRows * kRowsPer);
+  const int64_t row0 = wg * kVecRows;
   if (row0 >= p.N) return;
   float acc[MM][kVecRows];
 #pragma unroll
   for (int m = 0; m < MM; ++m)
 #pragma unroll
     for (int r = 0; r < kVecRows; ++r) acc[m][r] = 0.f;
-  const int slices = LPR < 64 ? 1 : (p.K + kVecSlice - 1) / kVecSlice;
+  const int slices = (p.K + kVecSlice - 1) / kVecSlice;
   for (int slice = wave; slice < slices; slice += waves) {
-    const int k = slice * kVecSlice + (lane % LPR) * 32;
+    const int k = slice * kVecSlice + lane * 32;
     const bool in = k < p.K;
     const int kk = in ? k : 0;      // lanes past K: values of the row's start times zeros
     u32x4 a[MM][4];
@@ -466,8 +463,7 @@ __global__ void __launch_bounds__(64 * kVecWaves) gemv_w4_kernel(W4Params p) {
     const int g = kk >> p.group_shift;
 #pragma unroll
     for (int r = 0; r < kVecRows; ++r) {
-      int64_t n = row0 + r * kRowsPer;
-      if constexpr (LPR < 64) n += lane / LPR;
+      int64_t n = row0 + r;
       if (n > p.N - 1) n = p.N - 1;
       w[r] = __builtin_nontemporal_load(
           reinterpret_cast<const u32x4*>(p.codes + n * p.ld_codes + (kk >> 1)));
@@ -508,24 +504,16 @@ __global__ void __launch_bounds__(64 * kVecWaves) gemv_w4_kernel(W4Params p) {
   }
 #pragma unroll
   for (int m = 0; m < MM; ++m) {
-    if constexpr (LPR == 64) {
-      float out[2];
-      sum_rows(acc[m], out);
-      if ((lane & 15) == 0) {
-        const int part = (lane >> 4), at = ((part & 1) << 1) | (part >> 1);
-        red[wave][m][at] = out[0];
-        red[wave][m][4 + at] = out[1];
-      }
-    } else {
-#pragma unroll
-      for (int r = 0; r < kVecRows; ++r) {
-        const float v = group_sum<LPR>(acc[m][r]);
-        if (lane % LPR == 0) red[wave][m][r * kRowsPer + lane / LPR] = v;
-      }
+    float out[2];
+    sum_rows(acc[m], out);
+    if ((lane & 15) == 0) {
+      const int part = (lane >> 4), at = ((part & 1) << 1) | (part >> 1);
+      red[wave][m][at] = out[0];
+      red[wave][m][4 + at] = out[1];
     }
   }
   __syncthreads();
-  constexpr int kPairs = MM * kVecRows * kRowsPer / 2;
+  constexpr int kPairs = MM * kVecRows / 2;
   uint32_t* C = reinterpret_cast<uint32_t*>(p.C);
   for (int u = (int)threadIdx.x; u < kPairs; u += (int)blockDim.x) {
     const int m = u / (kPairs / MM), r = u % (kPairs / MM) * 2;
@@ -540,29 +528,20 @@ __global__ void __launch_bounds__(64 * kVecWaves) gemv_w4_kernel(W4Params p) {
   }
 }
 
-template <class T, int MM, int LPR>
+template <class T, int MM>
 hipError_t launch_w4_vec(const W4Params& p, hipStream_t stream) {
-  constexpr int kRows = kVecRows * (64 / LPR);
-  const int slices = LPR < 64 ? 1 : (p.K + kVecSlice - 1) / kVecSlice;
+  const int slices = (p.K + kVecSlice - 1) / kVecSlice;
   const int turns = (slices + kVecWaves - 1) / kVecWaves;
   const int waves = (slices + turns - 1) / turns;
-  void (*k)(W4Params) = p.zeros != nullptr ? gemv_w4_kernel<T, MM, LPR, true>
-                                           : gemv_w4_kernel<T, MM, LPR, false>;
-  hipLaunchKernelGGL(k, long_grid(((int64_t)p.N + kRows - 1) / kRows), dim3(64 * waves), 0, stream, p);
+  void (*k)(W4Params) = p.zeros != nullptr ? gemv_w4_kernel<T, MM, true>
+                                           : gemv_w4_kernel<T, MM, false>;
+  hipLaunchKernelGGL(k, long_grid(((int64_t)p.N + kVecRows - 1) / kVecRows), dim3(64 * waves), 0,
+                     stream, p);
   return hipGetLastError();
 }
 
-// A row of weights takes 32 k's a lane: as many lanes as K has, up to a wave.
-template <class T, int MM>
-hipError_t launch_w4_vec_k(const W4Params& p, hipStream_t stream) {
-  if (p.K <= 8 * 32) return launch_w4_vec<T, MM, 8>(p, stream);
-  if (p.K <= 16 * 32) return launch_w4_vec<T, MM, 16>(p, stream);
-  if (p.K <= 32 * 32) return launch_w4_vec<T, MM, 32>(p, stream);
-  return launch_w4_vec<T, MM, 64>(p, stream);
-}
-
 // ---------------------------------------------------------------------------
-// Two to eight rows of A against smaller layers. v_mfma_f32_4x4x4 multiplies 16
+// One to eight rows of A against smaller layers. v_mfma_f32_4x4x4 multiplies 16
 // blocks apart, four rows by four columns by four k's each: lane 4 b + j holds
 // values of A's row j and of weight row j, at the 32 k's of block b, that one
 // 16-byte load of codes brings. KB blocks lie along K, 64 / KB weight rows make
@@ -570,7 +549,8 @@ hipError_t launch_w4_vec_k(const W4Params& p, hipStream_t stream) {
 // applied to the block's product in the lane, sum_k a times the zero point by one
 // more product, against ones. No LDS on the way in, and the vector units only
 // expand the codes, where v_dot2 would take 8 cycles for every 128 products too:
-// 4 x 4096 x 4096 5.8 us (on v_dot2 7.7), 4 x 3544 x 22464 16.6 (25.2).
+// 4 x 4096 x 4096 5.8 us (on v_dot2 7.7), 4 x 3544 x 22464 16.6 (25.2), 1 x 4096
+// x 4096 4.7 (4.8).
 // Bound by a launch and a trip to memory there, and by the reads, in pieces of
 // 256 bytes a row, on larger layers.
 // ---------------------------------------------------------------------------
@@ -740,14 +720,19 @@ int w4_cols(int64_t M, int64_t N) { return w4_tiles(M, N, 64) <= 256 ? 64 : 128;
 
 enum W4Kind { kW4Vec, kW4Quad, kW4Tile };
 
-// The vector units take one row, and two of more than 2^25 weights (2 x 28672 x
-// 8192 30 us, the small MFMAs 34; 2 x 4096 x 4096 5.7 and 4.9). The small MFMAs
-// take up to four rows of up to 3 * 2^25 weights (4 x 8192 x 8192 13.0 us, the
-// tiles 16.1; 4 x 28672 x 8192 38 and 35) and up to eight of 3 * 2^23 (8 x 4096 x
-// 4096 7.1 and 9.3; 8 x 8192 x 8192 21 and 17).
+// The vector units take one row of more than 2^24 weights (1 x 28672 x 8192 22 us,
+// the small MFMAs 32; 1 x 2048 x 1024 3.9 and 3.3) or of a long K (1 x 1024 x 8192
+// 4.1 and 4.9), and two of more than 2^25 (2 x 28672 x 8192 30 and 34; 2 x 4096 x
+// 4096 5.7 and 4.9). The small MFMAs take the rest, up to four rows of up to
+// 3 * 2^25 weights (4 x 8192 x 8192 13.0 us, the tiles 16.1; 4 x 28672 x 8192 38
+// and 35) and up to eight of 3 * 2^23 (8 x 4096 x 4096 7.1 and 9.3; 8 x 8192 x
+// 8192 21 and 17).
 W4Kind w4_kind(int64_t M, int64_t N, int64_t K) {
   const int64_t weights = N * K;
-  if (M == 1 || (M == 2 && weights > int64_t{1} << 25)) return kW4Vec;
+  if (M <= 2) {
+    const bool vec = K > 1024 && (weights > int64_t{1} << (M == 1 ? 24 : 25) || (M == 1 && K > 4096));
+    return vec ? kW4Vec : kW4Quad;
+  }
   return weights <= int64_t{3} << (M <= 4 ? 25 : 23) && M <= 8 ? kW4Quad : kW4Tile;
 }
 
@@ -769,8 +754,9 @@ template <class T>
 hipError_t launch_w4_type(const W4Params& p, hipStream_t stream) {
   const W4Kind kind = w4_kind(p.M, p.N, p.K);
   if (kind == kW4Vec)
-    return p.M == 1 ? launch_w4_vec_k<T, 1>(p, stream) : launch_w4_vec_k<T, 2>(p, stream);
+    return p.M == 1 ? launch_w4_vec<T, 1>(p, stream) : launch_w4_vec<T, 2>(p, stream);
   if (kind == kW4Quad) {
+    if (p.M == 1) return launch_w4_quad_k<T, 1>(p, stream);
     if (p.M == 2) return launch_w4_quad_k<T, 2>(p, stream);
     return p.M <= 4 ? launch_w4_quad_k<T, 4>(p, stream) : launch_w4_quad_k<T, 8>(p, stream);
   }

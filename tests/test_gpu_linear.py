@@ -395,7 +395,8 @@ W4_WIDE = [(5, 16520, 288, 32), (20, 16648, 256, 128), (33, 16456, 640, 64), (40
 
 # Two to eight rows: one or two turns through K, blocks that K leaves empty, both numbers of loads, ends of N.
 W4_FEW = [(2, 2056, 4096, 64), (3, 2072, 4608, 128), (4, 4104, 96, 32), (5, 2064, 160, 32), (6, 72, 8256, 64),
-          (7, 4112, 256, 256), (8, 1000, 5120, 128), (8, 3000, 8192, 1024), (4, 8, 32, 32), (2, 40, 64, 64)]
+          (7, 4112, 256, 256), (8, 1000, 5120, 128), (8, 3000, 8192, 1024), (4, 8, 32, 32), (2, 40, 64, 64), (1, 2056, 1024, 64), (1, 4104, 256, 32),
+          (1, 24, 4128, 32), (1, 4104, 4096, 128), (2, 33000, 1024, 128), (1, 5000, 18432, 256)]
 
 
 @pytest.mark.parametrize("M,N,K,G", W4_WIDE + W4_FEW)
