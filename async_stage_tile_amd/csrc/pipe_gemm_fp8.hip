@@ -15,7 +15,8 @@
 //
 // Few rows: the call is bound by reading B once, from memory straight into
 // registers for up to four (gemv_fp8_kernel), through a deep LDS ring for up to
-// 64 (gemm_fp8_rows_kernel). Many rows: gemm_fp8_tile_kernel.
+// 64 and for more of small layers (gemm_fp8_rows_kernel). Many rows:
+// gemm_fp8_tile_kernel.
 #include "pipe_device.hpp"
 #include "pipe_linear.hpp"
 
@@ -168,19 +169,19 @@ __global__ void __launch_bounds__(64 * kVecWaves) gemv_fp8_kernel(Fp8Params p) {
 }
 
 // ---------------------------------------------------------------------------
-// Five to 64 rows: bound by reading B once, through few CUs' worth of tiles. A
-// workgroup of 8 waves computes 32 FM rows of A times 32 WN rows of B. Stages
-// of 512 k pass through an LDS ring (rows of 512 bytes, 16-byte chunk c of row
-// r at place c ^ (r & 15), 2 rows a direct-to-LDS block); wave (wn, wk) takes
-// 32 rows of B and part wk of the stage's k's. The parts' sums meet in LDS at
-// the end. One CU's ring holds about 100 KiB of loads in flight, which at the
-// memory's latency is 35 KB a us: what counts is that every CU has a tile, so
-// tiles are 32 columns wide up to N = 12288, and with fewer than 96 of them K
-// is split over workgroups too. 24 x 8192 x 8192 takes 16 to 19 us (67 MB: 3.5
-// to 4.2 TB/s), and 15.5 without A's loads or the MFMAs: the read of B is all.
-// B's loads are non-temporal: 53 us for 8 x 16384 x 16384 where cached ones
-// take 60 (they win, 14 us for 17, only for weights that the memory-side cache
-// still holds from the call before).
+// Five to 64 rows, and more of small layers: bound by reading B once, through
+// few CUs' worth of tiles. A workgroup of 8 waves computes 32 FM rows of A
+// times 32 WN rows of B. Stages of 512 k pass through an LDS ring (rows of 512
+// bytes, 16-byte chunk c of row r at place c ^ (r & 15), 2 rows a direct-to-LDS
+// block); wave (wn, wk) takes 32 rows of B and part wk of the stage's k's. The
+// parts' sums meet in LDS at the end. One CU's ring holds about 100 KiB of
+// loads in flight, which at the memory's latency is 35 KB a us: what counts is
+// that every CU has a tile, so tiles are 32 columns wide up to N = 12288, and
+// with fewer than 96 of them K is split over workgroups too. 24 x 8192 x 8192
+// takes 16 to 19 us (67 MB: 3.5 to 4.2 TB/s), and 15.5 without A's loads or the
+// MFMAs: the read of B is all. B's loads are non-temporal: 53 us for 8 x 16384
+// x 16384 where cached ones take 60 (they win, 14 us for 17, only for weights
+// that the memory-side cache still holds from the call before).
 // ---------------------------------------------------------------------------
 constexpr int kRowsStageK = 512;
 
@@ -217,9 +218,17 @@ __global__ void __launch_bounds__(512) gemm_fp8_rows_kernel(Fp8Params p) {
   const int li = lane & 31, lh = lane >> 5;
   const int wn = wave % WN, wk = wave / WN;
   const uint32_t base = uniform(lds_addr(&lds[0]));
-  if (long_block() >= p.tiles_n * p.splits) return;   // < 2^26: many splits only for few tiles
+  const int tiles = p.tiles_m * p.tiles_n;
+  if (long_block() >= tiles * p.splits) return;   // < 2^28: splits only for few tiles
   const int wg = (int)long_block();
-  const int split = p.splits == 1 ? 0 : wg / p.tiles_n, n0 = (wg - split * p.tiles_n) * kN;
+  const int split = p.splits == 1 ? 0 : wg / tiles, tile = wg - split * tiles;
+  // The longer side's tiles go round the XCDs, so that its operand, read by all
+  // workgroups along the shorter side, comes into few L2s (8192 x 64 x 8192 17.9
+  // us, the other way round 29.5).
+  const bool tall = p.tiles_m > p.tiles_n;
+  const int shorter = p.tiles_m == 1 ? 0 : tile / (tall ? p.tiles_m : p.tiles_n);
+  const int longer = tile - shorter * (tall ? p.tiles_m : p.tiles_n);
+  const int m0 = (tall ? longer : shorter) * 32 * FM, n0 = (tall ? shorter : longer) * kN;
   const int per = p.splits == 1 ? p.steps : (p.steps + p.splits - 1) / p.splits;
   const int first = split * per, count = min(per, p.steps - first);   // >= 1
 
@@ -230,7 +239,7 @@ __global__ void __launch_bounds__(512) gemm_fp8_rows_kernel(Fp8Params p) {
     const bool of_a = j < Tile::kLoadsA;
     const int block = of_a ? wave * Tile::kLoadsA + j : wave * Tile::kLoadsB + j - Tile::kLoadsA;
     const int r = block * 2 + (lane >> 5);
-    src[j] = of_a ? p.A + (int64_t)min(r, p.M - 1) * p.lda
+    src[j] = of_a ? p.A + (int64_t)min(m0 + r, p.M - 1) * p.lda
                   : p.B + (int64_t)min(n0 + r, p.N - 1) * p.ldb;
     src_k[j] = 16 * ((lane & 31) ^ (r & 15));
   }
@@ -316,12 +325,12 @@ __global__ void __launch_bounds__(512) gemm_fp8_rows_kernel(Fp8Params p) {
           f32x4{acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]};
   __syncthreads();
   for (int u = (int)threadIdx.x; u < 32 * FM * (kN / 4); u += 512) {
-    const int m = u / (kN / 4), c = u % (kN / 4) * 4, n = n0 + c;
+    const int at = u / (kN / 4), c = u % (kN / 4) * 4, m = m0 + at, n = n0 + c;
     if (m >= p.M || n >= p.N) continue;
-    f32x4 v = *reinterpret_cast<const f32x4*>(sums + m * Tile::kPitch + c);
+    f32x4 v = *reinterpret_cast<const f32x4*>(sums + at * Tile::kPitch + c);
 #pragma unroll
     for (int s = 1; s < Tile::kParts; ++s)
-      v += *reinterpret_cast<const f32x4*>(sums + (s * 32 * FM + m) * Tile::kPitch + c);
+      v += *reinterpret_cast<const f32x4*>(sums + (s * 32 * FM + at) * Tile::kPitch + c);
     if (p.splits > 1) {
       *reinterpret_cast<f32x4*>(p.partials + ((int64_t)split * p.M + m) * p.N + n) = v;
     } else {
@@ -700,13 +709,20 @@ int shares(int steps, int64_t most, int least) {
 Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K) {
   Fp8Plan c{kVec, 0, 0, 1, 0, false};
   if (M <= 4) return c;
-  if (M <= 64) {
+  // The few-row kernel, also for more rows while its tiles of 64 x 32 all run at
+  // once and K is not long: 128 x 4096 x 4096 takes 9.7 us and in the large tiles
+  // 18.7, 256 x 1024 x 4096 8.8 and 15.0; 128 x 4096 x 14336 24.8 and 22.1, and
+  // with two rounds of them 192 x 4096 x 4096 17.5 and 18.5, 128 x 8192 x 8192 35
+  // and 23.
+  const int64_t few = (M + 63) / 64 * ((N + 31) / 32);
+  if (M <= 64 || (few <= 256 && K <= 8192)) {
     c.kind = kRows;
-    c.tiles_m = 1;
-    c.wide = N > 192 * 64;
+    c.tiles_m = ceil_div(M, 64);
+    c.wide = M <= 64 && N > 192 * 64;
     c.tiles_n = ceil_div(N, c.wide ? 64 : 32);
     c.steps = ceil_div(K, kRowsStageK);
-    c.splits = c.tiles_n < 96 ? shares(c.steps, 192 / c.tiles_n, 2) : 1;
+    const int tiles = c.tiles_m * c.tiles_n;
+    c.splits = tiles < 96 ? shares(c.steps, 192 / tiles, 2) : 1;
     return c;
   }
   // The tile kernels: of all tile shapes and splits of K, the least estimate of

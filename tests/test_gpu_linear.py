@@ -261,7 +261,12 @@ FP8_SHAPES = [(1, 8, 16), (1, 4096, 4096), (2, 24, 48), (15, 264, 400), (16, 256
               (64, 12400, 528), (5, 1000, 16384)]
 
 
-@pytest.mark.parametrize("M,N,K", FP8_SHAPES)
+# Large tiles of every shape at their edges, and the few-row kernel's second and later rows of tiles.
+FP8_MORE = [(65, 136, 8256), (129, 520, 9232), (257, 264, 8208), (130, 8, 8224), (500, 504, 13200), (66, 4104, 336),
+            (1000, 1000, 400), (600, 2056, 2064), (65, 4088, 8192), (128, 4096, 1040), (1000, 504, 1552), (4100, 40, 80)]
+
+
+@pytest.mark.parametrize("M,N,K", FP8_SHAPES + FP8_MORE)
 def test_fp8_exact_integers(M, N, K):
     A, W = small_e4m3((M, K), 30), small_e4m3((N, K), 31)
     sa, sb = powers(M, 32), powers(N, 33)
