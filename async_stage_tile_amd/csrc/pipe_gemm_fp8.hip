@@ -712,13 +712,16 @@ Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K) {
   // The few-row kernel, also for more rows while its tiles of 64 x 32 all run at
   // once and K is not long: 128 x 4096 x 4096 takes 9.7 us and in the large tiles
   // 18.7, 256 x 1024 x 4096 8.8 and 15.0; 128 x 4096 x 14336 24.8 and 22.1, and
-  // with two rounds of them 192 x 4096 x 4096 17.5 and 18.5, 128 x 8192 x 8192 35
-  // and 23.
-  const int64_t few = (M + 63) / 64 * ((N + 31) / 32);
-  if (M <= 64 || (few <= 256 && K <= 8192)) {
+  // with two rounds of them 128 x 8192 x 8192 35 and 23. Its tiles of 64 x 64
+  // likewise up to half that K: 256 x 4096 x 4096 15.1 and 18.6, 300 x 3000 x 2000
+  // 11.8 and 16.8; 1024 x 1024 x 8192 27.2 and 21.7.
+  const int64_t tall = (M + 63) / 64;
+  const bool few32 = tall * ((N + 31) / 32) <= 256 && K <= 8192;
+  const bool few64 = tall * ((N + 63) / 64) <= 256 && K <= 4096;
+  if (M <= 64 || few32 || few64) {
     c.kind = kRows;
     c.tiles_m = ceil_div(M, 64);
-    c.wide = M <= 64 && N > 192 * 64;
+    c.wide = M <= 64 ? N > 192 * 64 : !few32;
     c.tiles_n = ceil_div(N, c.wide ? 64 : 32);
     c.steps = ceil_div(K, kRowsStageK);
     const int tiles = c.tiles_m * c.tiles_n;

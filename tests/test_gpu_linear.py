@@ -263,7 +263,8 @@ FP8_SHAPES = [(1, 8, 16), (1, 4096, 4096), (2, 24, 48), (15, 264, 400), (16, 256
 
 # Large tiles of every shape at their edges, and the few-row kernel's second and later rows of tiles.
 FP8_MORE = [(65, 136, 8256), (129, 520, 9232), (257, 264, 8208), (130, 8, 8224), (500, 504, 13200), (66, 4104, 336),
-            (1000, 1000, 400), (600, 2056, 2064), (65, 4088, 8192), (128, 4096, 1040), (1000, 504, 1552), (4100, 40, 80)]
+            (1000, 1000, 400), (600, 2056, 2064), (65, 4088, 8192), (128, 4096, 1040), (1000, 504, 1552), (4100, 40, 80),
+            (200, 4096, 1552), (1500, 520, 528), (1300, 2000, 2064), (2000, 4120, 400)]
 
 
 @pytest.mark.parametrize("M,N,K", FP8_SHAPES + FP8_MORE)
