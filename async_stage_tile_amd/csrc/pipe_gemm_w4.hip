@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(256) gemm_w4_join_kernel(W4Params p) {
 // One or two rows of A. A lane keeps the values of 32 k's of every row in
 // registers (a wave takes a slice of 2048) and meets them with the codes of
 // kVecRows weight rows, one 16-byte load each: a wave reads 1 KiB of a row at a
-// time, and all loads of its rows are in flight together. 1 x 28672 x 8192 takes 22 us (5.4 TB/s), bound by reading the codes
+// time, and all loads of its rows are in flight together. 1 x 28672 x 8192 takes 23 us (5.3 TB/s), bound by reading the codes
 // and then by turning them into floats (codes masked into the mantissa of a
 // large float instead: 27 us). A lane's 32 k's lie in one group, whatever its size, so the scale
 // and the zero point are applied to the lane's own sum. v_dot2 adds up two
@@ -720,7 +720,7 @@ int w4_cols(int64_t M, int64_t N) { return w4_tiles(M, N, 64) <= 256 ? 64 : 128;
 
 enum W4Kind { kW4Vec, kW4Quad, kW4Tile };
 
-// The vector units take one row of more than 2^24 weights (1 x 28672 x 8192 22 us,
+// The vector units take one row of more than 2^24 weights (1 x 28672 x 8192 23 us,
 // the small MFMAs 32; 1 x 2048 x 1024 3.9 and 3.3) or of a long K (1 x 1024 x 8192
 // 4.1 and 4.9), and two of more than 2^25 (2 x 28672 x 8192 30 and 34; 2 x 4096 x
 // 4096 5.7 and 4.9). The small MFMAs take the rest, up to four rows of up to
