@@ -668,7 +668,8 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_fp8_tile_kernel(Fp8
 }
 
 // Sum of the splits' partial products in split order, scaled and rounded: four
-// columns a thread.
+// columns a thread. Bound by a launch and trips to memory, so four splits' loads
+// go out together (30 x 512 x 16384 8.2 us in all, one at a time 9.5).
 template <int OUT>
 __global__ void __launch_bounds__(256) gemm_fp8_join_kernel(Fp8Params p) {
   const int quads = p.N >> 2;
@@ -678,6 +679,7 @@ __global__ void __launch_bounds__(256) gemm_fp8_join_kernel(Fp8Params p) {
   const int64_t plane = (int64_t)p.M * p.N;
   const float* src = p.partials + (int64_t)m * p.N + n;
   f32x4 v = *reinterpret_cast<const f32x4*>(src);
+#pragma unroll 4
   for (int s = 1; s < p.splits; ++s) v += *reinterpret_cast<const f32x4*>(src + s * plane);
   const float sa = p.a_scales[m];
 #pragma unroll
