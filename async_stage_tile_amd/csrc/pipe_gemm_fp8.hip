@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(64 * kVecWaves) gemv_fp8_kernel(Fp8Params p) {
 // parts' sums meet in LDS at the end. One CU's ring holds about 100 KiB of
 // loads in flight, which at the memory's latency is 35 KB a us: what counts is
 // that every CU has a tile, so tiles are 32 columns wide up to N = 12288, and
-// with fewer than 96 of them K is split over workgroups too. 24 x 8192 x 8192
+// with few of them a long K is split over workgroups too. 24 x 8192 x 8192
 // takes 16 to 19 us (67 MB: 3.5 to 4.2 TB/s), and 15.5 without A's loads or the
 // MFMAs: the read of B is all. B's loads are non-temporal: 53 us for 8 x 16384
 // x 16384 where cached ones take 60 (they win, 14 us for 17, only for weights
@@ -727,7 +727,12 @@ Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K) {
     c.tiles_n = ceil_div(N, c.wide ? 64 : 32);
     c.steps = ceil_div(K, kRowsStageK);
     const int tiles = c.tiles_m * c.tiles_n;
-    c.splits = tiles < 96 ? shares(c.steps, 192 / tiles, 2) : 1;
+    // K is split where that gives idle CUs enough stages to pay for the join: 16 x
+    // 1024 x 3008 takes 5.0 us whole and 6.1 split, 33 x 1000 x 8192 7.9 in 6
+    // parts; 24 x 4096 x 14336 14.5 in two and 18.2 whole, 8 x 4096 x 4096 7.3 and
+    // 6.5.
+    const int most = tiles < 96 ? 192 / tiles : tiles <= 128 && c.steps >= 16 ? 2 : 1;
+    c.splits = c.steps >= 8 ? shares(c.steps, most, 2) : 1;
     return c;
   }
   // The tile kernels: of all tile shapes and splits of K, the least estimate of
