@@ -739,15 +739,14 @@ W4Kind w4_kind(int64_t M, int64_t N, int64_t K) {
   return weights <= int64_t{3} << (M <= 4 ? 25 : 23) && M <= 8 ? kW4Quad : kW4Tile;
 }
 
-// Workgroups that share a tile's K: as many as fill the CUs, four stages each
-// at least (33 x 1024 x 8192 12.4 us, with two 13.4). The other kernels need
-// none.
+// Workgroups that share a tile's K: as many as fill the CUs, two stages each at
+// least (40 x 2048 x 2048 8.7 us, with four 10.0). The other kernels need none.
 int w4_splits(int64_t M, int64_t N, int64_t K) {
   if (w4_kind(M, N, K) != kW4Tile) return 1;
   const int64_t tiles = w4_tiles(M, N, w4_cols(M, N));
   const int64_t stages = (K + kW4StageK - 1) / kW4StageK;
   int64_t splits = tiles < 256 ? 256 / tiles : 1;
-  splits = splits < stages / 4 ? splits : stages / 4;
+  splits = splits < stages / 2 ? splits : stages / 2;
   if (splits <= 1) return 1;
   const int64_t per = (stages + splits - 1) / splits;
   return (int)((stages + per - 1) / per);   // no empty split
