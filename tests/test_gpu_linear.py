@@ -491,7 +491,7 @@ def test_w4_empty_and_refusals():
 # ---------------------------------------------------------------------------
 # Streams, graphs, long extents
 # ---------------------------------------------------------------------------
-def _layer_inputs(M=100, N=512, K=2048, seed=70):
+def _layer_inputs(M=100, N=512, K=4096, seed=70):
     x, res, dy = (normal((M, K), BF, seed + i) for i in range(3))
     w = normal((K,), BF, seed + 3)
     W, sb = small_e4m3((N, K), seed + 4), powers(N, seed + 5)
@@ -512,7 +512,7 @@ def _layer(x, res, dy, w, W, sb, codes, s, stream=None):
 def test_operators_on_a_side_stream():
     ins = _layer_inputs()
     want = _layer(*ins)
-    assert pt.pipe_gemm_fp8_workspace_bytes(100, 512, 2048) > 0    # the workspace too is held for the side stream
+    assert pt.pipe_gemm_fp8_workspace_bytes(100, 512, 4096) > 0    # the workspace too is held for the side stream
     torch.cuda.synchronize()
     side = torch.cuda.Stream(device=DEV)
     side.wait_stream(torch.cuda.current_stream())
