@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(512) gemm_fp8_rows_kernel(Fp8Params p) {
 // are zeroed there, so that chunk's finite values add nothing, and a NaN in it
 // is in the row's product anyway.
 //
-// 8192^3 takes 413 to 423 us (2.6 PFLOP/s): the MFMAs are at work 69 % of the
+// 8192^3 takes 413 to 431 us (2.6 PFLOP/s): the MFMAs are at work 69 % of the
 // cycles, at the 1.7 GHz that the card holds under this load; the LDS's reads and
 // writes take about as many, and the two do not overlap wholly. 1000 x 5000 x
 // 4112 takes 31 us in 240 tiles of 192 x 128, whose loads from L2, at about 60 KB
