@@ -1,12 +1,19 @@
-// Products of e4m3 rows with e4m3 weights: C = (A B) * a_scales * b_scales, on
-// the 8-bit MFMAs (v_mfma_f32_32x32x64_f8f6f4, twice the rate of the 16-bit and
-// of the older 8-bit forms), fp32 sums.
+// Products of e4m3 rows with e4m3 weights: C = (A B) * a_scales * b_scales.
 //
-// The 8-bit MFMAs keep fewer bits than fp32 while they add up their products:
-// sums come out 3e-5 off (of their norm, K 4096; the older 8-bit forms alike).
-// That is a sixteenth of fp16's rounding and less of bf16's, so 16-bit C takes
-// it. For fp32 C the same bytes are turned into fp16 values, exactly, and go
-// through the fp16 MFMAs, at half the rate: 7e-8 off.
+// The 8-bit MFMAs (v_mfma_f32_32x32x64_f8f6f4, twice the rate of the 16-bit and
+// of the older 8-bit forms) keep fewer bits than fp32 while they add up their
+// products: of each eight neighbouring k's, products are cut off 13 bits below
+// the largest one's leading bit, toward zero; from there on the sums are fp32
+// (measured with single products, the older forms' sums are as far off). Sums
+// come out 1.5e-5 of their norm off for normal inputs, 3e-5 where one channel in
+// a hundred is 11 times louder, 8e-5 where one in 500 is 300 times louder, 2e-4
+// where they cancel to a fortieth, K 64 to 16384 alike. Beside bf16's rounding
+// (1.6e-3 of the norm) that is nothing to see, so bf16 C takes it for five rows
+// of A and more; beside fp16's (2e-4) it is. For fp16 and fp32 C the same bytes
+// are turned into fp16 values, exactly, and go through the fp16 MFMAs, whose
+// sums are fp32 sums (4e-8 to 9e-8 off), at half the rate: 8192^3 with
+// fp16 C takes 735 us for 422, 1000 x 5000 x 4112 46 for 32, 24 x 8192 x 8192
+// 16.6 for 16.1.
 //
 // An MFMA multiplies the bytes that the two operands hold at the same place of
 // a lane, so any assignment of k's to places gives the same product as long as
@@ -47,11 +54,11 @@ __device__ __forceinline__ f16x2 e4m3_pair(uint32_t w, bool hi) {
             : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, false);
 }
 
-// acc + x y over 64 k's, of 32 rows each; exact products, and fp32 sums where C
-// is fp32 (OUT 2).
+// acc + x y over 64 k's, of 32 rows each; exact products and fp32 sums, but for
+// bf16 C (OUT 0) those of the 8-bit MFMAs.
 template <int OUT>
 __device__ __forceinline__ f32x16 mma32(i32x8 x, i32x8 y, f32x16 acc) {
-  if constexpr (OUT != 2) {
+  if constexpr (OUT == 0) {
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, acc, 0, 0, 0, 0, 0, 0);
   } else {
 #pragma unroll

@@ -81,9 +81,12 @@ pipe_status_t pipe_gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K, siz
 
 /* C[m][n] = (sum_k A[m][k] * B[n][k]) * a_scales[m] * b_scales[n], A (M x K)
  * and B (N x K, the transpose of the K x N right operand: lda, ldb >= K) in
- * e4m3, C in PIPE_BF16, PIPE_FP16 or PIPE_FP32. For fp32 C the sum is an fp32
- * sum. For 16-bit C and five rows of A or more it is that of the 8-bit matrix
- * instructions, which keep fewer bits (3e-5 of the result's norm, measured).
+ * e4m3, C in PIPE_BF16, PIPE_FP16 or PIPE_FP32. For fp16 and fp32 C the sum is
+ * an fp32 sum. For bf16 C and five rows of A or more it is that of the 8-bit
+ * matrix instructions, at twice the rate: of each eight neighbouring k's
+ * products are cut off 13 bits below the largest one's leading bit, and added
+ * up in fp32 from there on (1.5e-5 to 2e-4 of the result's norm, measured on
+ * normal inputs and on sums that cancel; bf16's own rounding is 1.6e-3).
  *   N % 8 == 0, K % 16 == 0, M arbitrary (else PIPE_ERR_SHAPE); M == 0 or
  *   N == 0 is a no-op, K == 0 gives C = 0 (scales unread). A, B, C bases
  *   16-byte aligned, lda and ldb multiples of 16 and below 2^24 (else
