@@ -39,7 +39,13 @@ PyObject* current_stream = nullptr;   // device -> address of its current stream
 
 PyObject* not_here() { Py_RETURN_NOTIMPLEMENTED; }
 
-const Tensor* tensor(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
+// A plain tensor or parameter; subclasses are the Python wrapper's.
+const Tensor* tensor(PyObject* o) { return THPVariable_CheckExact(o) ? &THPVariable_Unpack(o) : nullptr; }
+
+// The address of an operand that may be missing. It throws for a tensor without
+// storage (a function transform's), so it is read while the interpreter's lock
+// is held, as every address here.
+const void* address(const Tensor* t) { return t != nullptr ? t->const_data_ptr() : nullptr; }
 
 int code16(ScalarType t) { return t == ScalarType::BFloat16 ? 0 : t == ScalarType::Half ? 1 : -1; }
 
@@ -79,13 +85,17 @@ Tensor make(const Tensor& like, c10::IntArrayRef size, ScalarType type) {
                                    std::nullopt);
 }
 
-template <class F>
-int enqueue(F f) {
-  int status;
-  Py_BEGIN_ALLOW_THREADS
-  status = f();
-  Py_END_ALLOW_THREADS
-  return status;
+// The C call without the interpreter's lock, which is taken again however the
+// call is left.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
+template <class... P, class... A>
+int enqueue(int (*f)(P...), A... args) {
+  const Unlocked unlocked;
+  return f(args...);
 }
 
 PyObject* pack(std::initializer_list<const Tensor*> list) {
@@ -124,12 +134,9 @@ PyObject* rmsnorm(PyObject* const* a) {
   Tensor s, h;
   if (q8) s = make(*x, {M}, ScalarType::Float);
   if (res != nullptr) h = make(*x, {M, N}, type);
-  const int status = enqueue([&] {
-    return entry.rmsnorm(x->const_data_ptr(), res ? res->const_data_ptr() : nullptr, w->const_data_ptr(),
-                         y.data_ptr(), q8 ? s.data_ptr<float>() : nullptr,
-                         res ? h.data_ptr() : nullptr, M, N, N, N, N, N, (float)eps, code,
-                         q8 ? 3 : code, stream);
-  });
+  const int status = enqueue(entry.rmsnorm, address(x), address(res), address(w), y.data_ptr(),
+                             q8 ? s.data_ptr<float>() : nullptr, res ? h.data_ptr() : nullptr, M, N, N,
+                             N, N, N, (float)eps, code, q8 ? 3 : code, stream);
   if (status != 0) return nullptr;
   if (q8) return res ? pack({&y, &s, &h}) : pack({&y, &s});
   return res ? pack({&y, &h}) : THPVariable_Wrap(y);
@@ -157,11 +164,9 @@ PyObject* grad(PyObject* const* a) {
   const Tensor dx = make(*x, {M, N}, type), dw = make(*x, {N}, ScalarType::Float);
   Tensor ws;
   if (bytes > 0) ws = make(*x, {(int64_t)bytes}, ScalarType::Byte);
-  const int status = enqueue([&] {
-    return entry.grad(dy->const_data_ptr(), x->const_data_ptr(), w->const_data_ptr(),
-                      dh ? dh->const_data_ptr() : nullptr, dx.data_ptr(), dw.data_ptr<float>(), M, N,
-                      N, N, N, N, (float)eps, code, bytes > 0 ? ws.data_ptr() : nullptr, bytes, stream);
-  });
+  const int status = enqueue(entry.grad, address(dy), address(x), address(w), address(dh), dx.data_ptr(),
+                             dw.data_ptr<float>(), M, N, N, N, N, N, (float)eps, code,
+                             bytes > 0 ? ws.data_ptr() : nullptr, bytes, stream);
   return status != 0 ? nullptr : pack({&dx, &dw});
 }
 
@@ -191,11 +196,9 @@ PyObject* gemm_fp8(PyObject* const* a) {
   const Tensor C = make(*A, {M, N}, out);
   Tensor ws;
   if (bytes > 0) ws = make(*A, {(int64_t)bytes}, ScalarType::Byte);
-  const int status = enqueue([&] {
-    return entry.fp8(A->const_data_ptr(), sa->const_data_ptr<float>(), B->const_data_ptr(),
-                     sb->const_data_ptr<float>(), C.data_ptr(), M, N, K, K, K, N, code,
-                     bytes > 0 ? ws.data_ptr() : nullptr, bytes, stream);
-  });
+  const int status = enqueue(entry.fp8, address(A), static_cast<const float*>(address(sa)), address(B),
+                             static_cast<const float*>(address(sb)), C.data_ptr(), M, N, K, K, K, N, code,
+                             bytes > 0 ? ws.data_ptr() : nullptr, bytes, stream);
   return status != 0 ? nullptr : THPVariable_Wrap(C);
 }
 
@@ -222,11 +225,9 @@ PyObject* gemm_w4(PyObject* const* a) {
   const Tensor C = make(*A, {M, N}, type);
   Tensor ws;
   if (bytes > 0) ws = make(*A, {(int64_t)bytes}, ScalarType::Byte);
-  const int status = enqueue([&] {
-    return entry.w4(A->const_data_ptr(), q->const_data_ptr(), s->const_data_ptr(),
-                    z ? z->const_data_ptr() : nullptr, C.data_ptr(), M, N, K, K / groups, K, K / 2,
-                    groups, groups, N, code, bytes > 0 ? ws.data_ptr() : nullptr, bytes, stream);
-  });
+  const int status = enqueue(entry.w4, address(A), address(q), address(s), address(z), C.data_ptr(), M, N, K,
+                             K / groups, K, K / 2, groups, groups, N, code,
+                             bytes > 0 ? ws.data_ptr() : nullptr, bytes, stream);
   return status != 0 ? nullptr : THPVariable_Wrap(C);
 }
 
