@@ -22,6 +22,7 @@ there is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -249,16 +250,28 @@ def _stream(stream=None, device=None):
     return ctypes.c_void_p(int(s.cuda_stream))
 
 
-def _hold_for(stream, device, *tensors):
-    """Tensors this wrapper allocated, used by work enqueued on `stream`: when
-    that is not the device's current stream, tell the caching allocator, so that
-    their memory is not handed out again before that stream's work is done."""
+def _allocating_for(stream):
+    """The context of a wrapper's own allocations: memory that work on `stream`
+    uses comes from that stream's pool. A block that the current stream has just
+    freed may still have its kernels ahead, which `stream` does not wait for."""
     import torch
-    if stream is None or stream == torch.cuda.current_stream(device):
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _hold_for(stream, device, *tensors):
+    """Tensors this wrapper allocated from the pool of `stream`: when that is not
+    the device's current stream, where the caller will use them, tell the caching
+    allocator, so that their memory is not handed out again on `stream` before
+    the current stream's work is done."""
+    import torch
+    if stream is None:
+        return
+    current = torch.cuda.current_stream(device)
+    if stream == current:
         return
     for t in tensors:
         if t is not None:
-            t.record_stream(stream)
+            t.record_stream(current)
 
 
 def matrix_geometry(shape, strides, name="matrix"):
@@ -298,7 +311,8 @@ def pipe_tile_copy(src, dst=None, checksums=False, stream=None, **cfg):
     M, N, ld_src = _check_matrix(src, "src", (torch.float16, torch.bfloat16, torch.int16))
     made = []
     if dst is None:
-        dst = torch.empty_like(src, memory_format=torch.contiguous_format)
+        with _allocating_for(stream):
+            dst = torch.empty_like(src, memory_format=torch.contiguous_format)
         made.append(dst)
     Md, Nd, ld_dst = _check_matrix(dst, "dst", (src.dtype,))
     if (Md, Nd) != (M, N):
@@ -308,8 +322,9 @@ def pipe_tile_copy(src, dst=None, checksums=False, stream=None, **cfg):
     chk = None
     if checksums:   # one word per tile of the configured shape
         tm, tn = max(1, c.tile_m), max(1, c.tile_n)
-        chk = torch.empty(((M + tm - 1) // tm) * ((N + tn - 1) // tn), dtype=torch.int32,
-                          device=dev)
+        with _allocating_for(stream):
+            chk = torch.empty(((M + tm - 1) // tm) * ((N + tn - 1) // tn), dtype=torch.int32,
+                              device=dev)
         made.append(chk)
     with torch.cuda.device(dev):
         st = lib().pipe_tile_copy(_ptr(src), _ptr(dst), M, N, ld_src, ld_dst, ctypes.byref(c),
@@ -333,11 +348,13 @@ def pipe_rowsum(A, out=None, workspace=None, stream=None, **cfg):
     M, N, lda = _check_matrix(A, "A", (torch.float16,))
     made = []
     if out is None:
-        out = torch.empty(M, dtype=torch.float32, device=A.device)
+        with _allocating_for(stream):
+            out = torch.empty(M, dtype=torch.float32, device=A.device)
         made.append(out)
     need = pipe_rowsum_workspace_bytes(M, N, **cfg)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=A.device)
+        with _allocating_for(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=A.device)
         made.append(workspace)
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     c = make_config(PIPE_OP_ROWSUM, **cfg)
@@ -426,7 +443,8 @@ def pipe_gemm_mainloop(A, B, C=None, stream=None, out_dtype=None, **cfg):
         raise ValueError("inner dimensions differ")
     made = None
     if C is None:
-        C = made = torch.empty((M, N), dtype=out_dtype or torch.float32, device=A.device)
+        with _allocating_for(stream):
+            C = made = torch.empty((M, N), dtype=out_dtype or torch.float32, device=A.device)
     Mc, Nc, ldc = _check_matrix(C, "C", (torch.float32, torch.bfloat16))
     if (Mc, Nc) != (M, N):
         raise ValueError("C shape mismatch")

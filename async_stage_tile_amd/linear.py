@@ -8,8 +8,9 @@
 Argument marshalling only, as in the package's other functions: the work is
 done by the HIP kernels of the shared library, on the given stream or the
 current one. Outputs that are not given are allocated, and so are the
-workspaces that a shape needs. Wrong arguments raise TypeError or ValueError
-here, or PipeError with the library's status, and then nothing is enqueued.
+workspaces that a shape needs, from the memory pool of the stream that the work
+goes to. Wrong arguments raise TypeError or ValueError here, or PipeError with
+the library's status, and then nothing is enqueued.
 
 The common case (contiguous operands, outputs made here, the current stream)
 goes through ``_linear.so``, the same marshalling in C++, which the build makes
@@ -135,6 +136,17 @@ def _dtype16(t, name):
     return dtype
 
 
+def _make(made, stream, like, shape, dtype):
+    """A tensor for work on `stream`, noted in `made`."""
+    if stream is None:
+        t = like.new_empty(shape, dtype=dtype)
+    else:
+        with _pt._allocating_for(stream):
+            t = like.new_empty(shape, dtype=dtype)
+    made.append(t)
+    return t
+
+
 def _call(fn, name, device, stream, made, *args):
     """The C call with the tensors' device current, on the given stream or the
     device's current one, which goes last; `made`: the tensors allocated here."""
@@ -179,8 +191,7 @@ def pipe_rmsnorm(x, weight, residual=None, eps=1e-6, out_dtype=None, y=None, y_s
     w = _vector(weight, "weight", dtype, dev, N)
     made = []
     if y is None:
-        y = _torch.empty_like(x, dtype=out_dtype, memory_format=_torch.contiguous_format)
-        made.append(y)
+        y = _make(made, stream, x, (M, N), out_dtype)
         ld_y = N
     else:
         ld_y = _matrix(y, "y", out_dtype, dev, (M, N))[2]
@@ -188,8 +199,7 @@ def pipe_rmsnorm(x, weight, residual=None, eps=1e-6, out_dtype=None, y=None, y_s
     scales = 0
     if q8:
         if y_scales is None:
-            y_scales = x.new_empty(M, dtype=_torch.float32)
-            made.append(y_scales)
+            y_scales = _make(made, stream, x, (M,), _torch.float32)
             scales = y_scales.data_ptr()
         else:
             scales = _vector(y_scales, "y_scales", _torch.float32, dev, M)
@@ -200,8 +210,7 @@ def pipe_rmsnorm(x, weight, residual=None, eps=1e-6, out_dtype=None, y=None, y_s
         ld_r = _matrix(residual, "residual", dtype, dev, (M, N))[2]
         r_ptr = residual.data_ptr()
         if h is None:
-            h = _torch.empty_like(x, memory_format=_torch.contiguous_format)
-            made.append(h)
+            h = _make(made, stream, x, (M, N), dtype)
             ld_h = N
         else:
             ld_h = _matrix(h, "h", dtype, dev, (M, N))[2]
@@ -237,25 +246,23 @@ def pipe_rmsnorm_backward(dy, x, weight, dh=None, eps=1e-6, dx=None, dweight=Non
         dh_ptr = dh.data_ptr()
     made = []
     if dx is None:
-        dx = _torch.empty_like(x, memory_format=_torch.contiguous_format)
-        made.append(dx)
+        dx = _make(made, stream, x, (M, N), dtype)
         ld_dx = N
     else:
         ld_dx = _matrix(dx, "dx", dtype, dev, (M, N))[2]
     if dweight is None:
-        dweight = x.new_empty(N, dtype=_torch.float32)
-        made.append(dweight)
+        dweight = _make(made, stream, x, (N,), _torch.float32)
     else:
         _vector(dweight, "dweight", _torch.float32, dev, N)
     ws, ws_bytes = _workspace(fns.pipe_rmsnorm_backward_workspace_bytes,
-                              "pipe_rmsnorm_backward_workspace_bytes", (M, N), workspace, x, made)
+                              "pipe_rmsnorm_backward_workspace_bytes", (M, N), workspace, x, made, stream)
     _call(fns.pipe_rmsnorm_backward, "pipe_rmsnorm_backward", dev, stream, made, dy.data_ptr(),
           x.data_ptr(), w, dh_ptr, dx.data_ptr(), dweight.data_ptr(), M, N, ld_dy, ld_x, ld_dh,
           ld_dx, eps, _codes[dtype], ws, ws_bytes)
     return dx, dweight
 
 
-def _workspace(fn, name, shape, given, like, made):
+def _workspace(fn, name, shape, given, like, made, stream):
     """(address, bytes) of a call's workspace: the given tensor, or one made here."""
     if given is not None:
         if not given.is_contiguous() or given.get_device() != like.get_device():
@@ -268,9 +275,7 @@ def _workspace(fn, name, shape, given, like, made):
     size = need.value
     if size == 0:
         return 0, 0
-    ws = like.new_empty(size, dtype=_torch.uint8)
-    made.append(ws)
-    return ws.data_ptr(), size
+    return _make(made, stream, like, (size,), _torch.uint8).data_ptr(), size
 
 
 def pipe_rmsnorm_backward_workspace_bytes(M, N) -> int:
@@ -316,8 +321,7 @@ def pipe_gemm_fp8(A, a_scales, B, b_scales, C=None, out_dtype=None, workspace=No
         out_dtype = out_dtype or _torch.bfloat16
         if out_dtype == e4m3 or out_dtype not in _codes:
             raise TypeError(f"out_dtype must be bfloat16, float16 or float32, not {out_dtype}")
-        C = A.new_empty((M, N), dtype=out_dtype)
-        made.append(C)
+        C = _make(made, stream, A, (M, N), out_dtype)
         ldc = N
     else:
         out_dtype = out_dtype or C.dtype
@@ -325,7 +329,7 @@ def pipe_gemm_fp8(A, a_scales, B, b_scales, C=None, out_dtype=None, workspace=No
             raise TypeError(f"C must be bfloat16, float16 or float32, not {out_dtype}")
         ldc = _matrix(C, "C", out_dtype, dev, (M, N))[2]
     ws, ws_bytes = _workspace(fns.pipe_gemm_fp8_workspace_bytes, "pipe_gemm_fp8_workspace_bytes",
-                              (M, N, K), workspace, A, made)
+                              (M, N, K), workspace, A, made, stream)
     _call(fns.pipe_gemm_fp8, "pipe_gemm_fp8", dev, stream, made, A.data_ptr(), sa, B.data_ptr(), sb,
           C.data_ptr(), M, N, K, lda, ldb, ldc, _codes[out_dtype], ws, ws_bytes)
     return C
@@ -365,13 +369,12 @@ def pipe_gemm_w4(A, codes, scales, zeros=None, C=None, workspace=None, stream=No
         z_ptr = zeros.data_ptr()
     made = []
     if C is None:
-        C = A.new_empty((M, N))
-        made.append(C)
+        C = _make(made, stream, A, (M, N), dtype)
         ldc = N
     else:
         ldc = _matrix(C, "C", dtype, dev, (M, N))[2]
     ws, ws_bytes = _workspace(fns.pipe_gemm_w4_workspace_bytes, "pipe_gemm_w4_workspace_bytes",
-                              (M, N, K), workspace, A, made)
+                              (M, N, K), workspace, A, made, stream)
     _call(fns.pipe_gemm_w4, "pipe_gemm_w4", dev, stream, made, A.data_ptr(), codes.data_ptr(),
           scales.data_ptr(), z_ptr, C.data_ptr(), M, N, K, K // groups if groups else 0, lda,
           ld_codes, ld_scales, ld_zeros, ldc, _codes[dtype], ws, ws_bytes)

@@ -1,0 +1,104 @@
+"""Calls with a stream of their own, whose outputs and workspaces the wrappers allocate, next to work on the current
+stream that still waits for its turn. Memory that was just freed on the current stream, with a kernel ahead that writes
+to it, must not become such an output; nor may an output's memory be handed out on the given stream while the
+current stream still has to read it."""
+import pytest
+import torch
+
+import async_stage_tile_amd as pt
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, E4 = torch.bfloat16, torch.float8_e4m3fn
+LONG = 20_000_000       # clock ticks that the current stream is kept busy, about 10 ms
+
+
+@pytest.fixture(autouse=True)
+def _name(request):
+    print(f"[stream memory] {request.node.name}", flush=True)
+    yield
+    torch.cuda.synchronize()
+
+
+def ints(shape, low, high, dtype, seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return torch.randint(low, high + 1, shape, device=DEV, generator=g).to(torch.float32).to(dtype)
+
+
+def calls():
+    x, w = ints((512, 1024), -4, 4, BF, 1), ints((1024,), -4, 4, BF, 2)
+    a8, w8 = ints((128, 8192), -4, 4, E4, 3), ints((256, 8192), -4, 4, E4, 4)
+    one = torch.ones(256, device=DEV)
+    a4, s4 = ints((40, 4096), -4, 4, BF, 5), torch.ones(256, 32, device=DEV, dtype=BF)
+    q4 = ints((256, 2048), 0, 255, torch.uint8, 6)
+    half, gb = ints((1024, 1024), -4, 4, torch.float16, 7), ints((1024, 512), -2, 2, BF, 8)
+    assert pt.pipe_gemm_fp8_workspace_bytes(128, 256, 8192) > 0 and pt.pipe_gemm_w4_workspace_bytes(40, 256, 4096) > 0
+    assert pt.pipe_rmsnorm_backward_workspace_bytes(512, 1024) > 0
+    return {
+        "rmsnorm": lambda s: pt.pipe_rmsnorm(x, w, residual=x, out_dtype=E4, stream=s),
+        "rmsnorm_backward": lambda s: pt.pipe_rmsnorm_backward(x, x, w, dh=x, stream=s),
+        "gemm_fp8": lambda s: pt.pipe_gemm_fp8(a8, one[:128], w8.t(), one, stream=s),
+        "gemm_w4": lambda s: pt.pipe_gemm_w4(a4, q4, s4, stream=s),
+        "tile_copy": lambda s: pt.pipe_tile_copy(half, checksums=True, stream=s),
+        "rowsum": lambda s: pt.pipe_rowsum(half, stream=s, split=4),
+        "gemm_mainloop": lambda s: pt.pipe_gemm_mainloop(x, gb, stream=s),
+    }
+
+
+def tensors(out):
+    return [t.view(torch.uint8).clone() for t in (out if isinstance(out, tuple) else (out,))]
+
+
+def sizes(want):
+    """Every size up to the largest output's, in steps of the allocator: workspaces are among them."""
+    top = max(t.numel() for t in want)
+    return sorted({n for n in (512, 1024, 2048, 65536, 1 << 20, 1 << 21, 1 << 22)} | {t.numel() for t in want if t.numel()}) + [top]
+
+
+@pytest.mark.parametrize("name", ["rmsnorm", "rmsnorm_backward", "gemm_fp8", "gemm_w4", "tile_copy", "rowsum", "gemm_mainloop"])
+def test_no_output_in_memory_that_the_current_stream_still_writes(name):
+    call = calls()[name]
+    want = tensors(call(None))
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    side = torch.cuda.Stream(device=DEV)
+    blocks = [torch.empty(n, dtype=torch.uint8, device=DEV) for n in sizes(want) for _ in range(2)]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(LONG)
+    for b in blocks:
+        b.fill_(0x55)           # behind the sleep
+    blocks.clear()
+    del b
+    out = call(side)
+    side.synchronize()
+    early = torch.cuda.current_stream().query()
+    torch.cuda.synchronize()
+    if early:                   # the fills were over before the call
+        pytest.skip("the streams share a queue")
+    for got, ref in zip(tensors(out), want):
+        assert torch.equal(got, ref)
+
+
+@pytest.mark.parametrize("name", ["rmsnorm", "rmsnorm_backward", "gemm_fp8", "gemm_w4", "tile_copy", "rowsum", "gemm_mainloop"])
+def test_no_output_reused_before_the_current_stream_has_read_it(name):
+    call = calls()[name]
+    want = tensors(call(None))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream(device=DEV)
+    out = call(side)
+    torch.cuda.current_stream().wait_stream(side)
+    side.synchronize()
+    torch.cuda._sleep(LONG)
+    got = tensors(out)          # copies, behind the sleep
+    del out
+    with torch.cuda.stream(side):
+        for n in sizes(want):
+            for _ in range(4):
+                torch.full((n,), 0x55, dtype=torch.uint8, device=DEV)
+    side.synchronize()
+    early = torch.cuda.current_stream().query()
+    torch.cuda.synchronize()
+    if early:
+        pytest.skip("the streams share a queue")
+    for g, ref in zip(got, want):
+        assert torch.equal(g, ref)
