@@ -609,14 +609,16 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_fp8_tile_kernel(Fp8
     asm volatile("" : "+v"(el));
     const int eli = el & 31, elh = el >> 5;
     uint8_t* mid = &staging[wave][0];
-    const int row0 = tm * Tile::kRowsA + wm * FM * 32, col0 = tn * Tile::kRowsB + wn * FN * 32;
+    // Unsigned: the last tile of 192 rows may end past 2^31.
+    const uint32_t row0 = (uint32_t)tm * Tile::kRowsA + wm * FM * 32;
+    const int col0 = tn * Tile::kRowsB + wn * FN * 32;
     const int wrow = eli * 128, wswz = (eli >> 1) & 7;
-    auto flush = [&](uint8_t* out, int64_t pitch, int row, int col, int per_chunk) {
+    auto flush = [&](uint8_t* out, int64_t pitch, uint32_t row, int col, int per_chunk) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int r = 8 * k + (el >> 3), c = (el & 7) ^ ((r >> 1) & 7);
         const u32x4 v = *reinterpret_cast<const u32x4*>(mid + r * 128 + (el & 7) * 16);
-        if (row + r < p.M && col + c * per_chunk < p.N)
+        if (row + r < (uint32_t)p.M && col + c * per_chunk < p.N)
           *reinterpret_cast<u32x4*>(out + (row + r) * pitch + (int64_t)col * (16 / per_chunk) + c * 16) = v;
       }
     };
@@ -650,7 +652,7 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_fp8_tile_kernel(Fp8
     uint8_t* out = static_cast<uint8_t*>(p.C);
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-      const float sa = p.a_scales[min(row0 + 32 * i + eli, p.M - 1)];
+      const float sa = p.a_scales[min(row0 + 32 * i + eli, (uint32_t)p.M - 1)];
       if constexpr (OUT == 2) {
 #pragma unroll
         for (int j = 0; j < FN; ++j) block32(i, j, sa, sb[j], out, p.ldc * 4);
