@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(64 * kW4Waves) gemm_w4_tile_kernel(W4Params p)
   const int64_t wg = long_block();
   // Neighbours share weight rows, then lie along N. Their number is below 2^31:
   // the host checks the tiles', and K is split for fewer than 256 tiles only.
-  const int m_tiles = (p.M + 16 * MT - 1) / (16 * MT), n_tiles = (p.N + TN - 1) / TN;
+  const int m_tiles = (p.M - 1) / (16 * MT) + 1, n_tiles = (p.N + TN - 1) / TN;
   if (wg >= (int64_t)m_tiles * n_tiles * p.splits) return;
   const int split = p.splits == 1 ? 0 : (int)wg / (m_tiles * n_tiles);
   const int tile = (int)wg - split * (m_tiles * n_tiles);

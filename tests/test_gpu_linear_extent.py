@@ -38,3 +38,13 @@ def test_fp8_rows_to_the_end_of_32_bits(M):
     C = pt.pipe_gemm_fp8(A, scales, w.to(torch.float8_e4m3fn).t(), torch.ones(N, device=DEV))
     assert torch.equal(C[-tail:], ((a @ w.t()) * scales[-tail:, None]).to(torch.bfloat16))
     assert not bool(C[:tail].any())
+
+
+def test_w4_rows_to_the_end_of_32_bits():
+    M, N, K, tail = END, 8, 32, 400
+    A = torch.zeros((M, K), dtype=torch.bfloat16, device=DEV)
+    A[-tail:] = small((tail, K), 3).to(torch.bfloat16)
+    q = small((N, K), 4).add(8).to(torch.uint8)
+    C = pt.pipe_gemm_w4(A, q[:, 0::2] | (q[:, 1::2] << 4), torch.ones((N, 1), dtype=torch.bfloat16, device=DEV))
+    assert torch.equal(C[-tail:], (A[-tail:].float() @ (q.float() - 8).t()).to(torch.bfloat16))
+    assert not bool(C[:tail].any())
