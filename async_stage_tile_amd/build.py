@@ -5,7 +5,8 @@ and include/pipe_linear.h (the quantised linear layer's operators).
 
 _linear.so -- the linear layer's Python marshalling in C++ (csrc/linear_binding.cpp,
 host code against the installed torch's headers; the Python wrappers work
-without it, slower).
+without it, slower). Where it cannot be built (no torch, no headers, no C++
+compiler) the build says so and goes on without it.
 
 Every translation unit compiles to its own object, in parallel; the stream
 kernel source is compiled once per group of stage counts. Then the library
@@ -77,7 +78,8 @@ def _run(cmd: list, verbose: bool) -> None:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError(f"hipcc failed with exit code {res.returncode}: {cmd[-3]}")
+        what = next((a for a in cmd if a.endswith((".hip", ".cpp"))), cmd[-1])
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed with exit code {res.returncode}: {what}")
 
 
 def _link(units: list, out: str, verbose: bool) -> None:
@@ -112,10 +114,16 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
     with ThreadPoolExecutor(max_workers=jobs) as ex:
         futs = [ex.submit(_run, compile_command(s, os.path.join(OBJ, o), d), verbose)
                 for (s, o, d) in units]
-        futs.append(ex.submit(build_binding, verbose))
+        binding = ex.submit(build_binding, verbose)
         for f in futs:
             f.result()
     _link(UNITS, LIB, verbose)
+    if binding.exception() is not None:
+        # One of an earlier build may not fit this library.
+        if os.path.exists(BINDING):
+            os.remove(BINDING)
+        sys.stderr.write(f"warning: _linear.so was not built ({binding.exception()}); "
+                         "the linear layer's calls take the Python wrappers\n")
     return LIB
 
 
