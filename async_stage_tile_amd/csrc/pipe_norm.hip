@@ -220,7 +220,11 @@ __global__ void __launch_bounds__(WG) rmsnorm_grad_kernel(NormGradParams p) {
   }
   // A row's loads go out before the row ahead of it is reduced. Past the last
   // row they take the last one again: a branch around them would make the
-  // compiler wait for them with the row in use.
+  // compiler wait for them with the row in use. Not so with four chunks for each
+  // of 1024 threads, rows wider than 16384: a thread has 128 registers there, and
+  // two rows' worth spilled up to 115 of them (2048 x 32768 took 359 us so, and
+  // takes 109; 8 x 32768 35 and 10).
+  constexpr bool kAhead = WG < 1024 || CH < 4;
   u32x4 h[CH], d[CH], s[RES ? CH : 1], nh[CH], nd[CH], ns[RES ? CH : 1];
   const auto load = [&](int64_t row) {
     const int64_t at = row < p.M ? row : p.M - 1;
@@ -247,17 +251,18 @@ __global__ void __launch_bounds__(WG) rmsnorm_grad_kernel(NormGradParams p) {
   };
   int turn = 0;
   const int64_t step = (int64_t)gridDim.x * kRows;
-  load((int64_t)blockIdx.x * kRows + sub);
+  if constexpr (kAhead) load((int64_t)blockIdx.x * kRows + sub);
   for (int64_t base = (int64_t)blockIdx.x * kRows; base < p.M; base += step, turn ^= 1) {
     const int64_t row = base + sub;
     const bool live = row < p.M;
+    if constexpr (!kAhead) load(row);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       h[i] = nh[i];
       d[i] = nd[i];
       if constexpr (RES) s[i] = ns[i];
     }
-    load(row + step);
+    if constexpr (kAhead) load(row + step);
     float hh = 0.f, gh = 0.f;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -319,9 +324,13 @@ __global__ void __launch_bounds__(WG) rmsnorm_grad_kernel(NormGradParams p) {
   }
   f32x4* out = reinterpret_cast<f32x4*>(p.partials + (int64_t)blockIdx.x * ((int64_t)p.chunks * 8));
   if constexpr (kRows == 1) {
+    // The thread's place is made anew for the compiler, which would else keep
+    // the columns through the loop, in scratch memory where registers are short.
+    int at = t;
+    asm volatile("" : "+v"(at));
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int c = t + TPR * i;
+      const int c = at + TPR * i;
       if (c < p.chunks) {
         out[2 * c] = f32x4{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
         out[2 * c + 1] = f32x4{dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
