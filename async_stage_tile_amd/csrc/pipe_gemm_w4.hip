@@ -15,7 +15,9 @@
 // Scales and zero points: over one group (q - z) s = s q - s z, so with
 // P = sum_k a q and S = sum_k a of the group, acc += s (P - z S). On the MFMAs S
 // is one more product, against ones. Everything is exact or fp32; no weight is
-// rounded to 16 bits.
+// rounded to 16 bits. P and z S may be larger than their difference, and their
+// fp32 errors with them: on loud channels, activations of one sign and sums that
+// cancel they stay within sqrt(K) 2^-24 of the two sums.
 #include "pipe_device.hpp"
 #include "pipe_linear.hpp"
 

@@ -106,8 +106,11 @@ pipe_status_t pipe_gemm_w4_workspace_bytes(int64_t M, int64_t N, int64_t K, size
  * ld_codes bytes) and zero points z (one uint8 of 0..15 each; NULL: 8
  * everywhere). Codes and zero points enter the products as the integers they
  * are, the scale is applied to the fp32 sum of each group, and C is rounded
- * once. An infinite A gives NaN where IEEE arithmetic on the single weights
- * may give an infinity.
+ * once. A group's product is s (sum a q - z sum a): the fp32 errors are those
+ * of these two sums, which may be larger than their difference. Where one of
+ * them passes fp32's range (an infinite A, or bf16 values near the end of the
+ * range) C is NaN, though the single weights' products may add up to a number
+ * or an infinity.
  *   group: a power of two >= 32 that divides K, or K itself if K % 32 == 0
  *   (else PIPE_ERR_SHAPE). N % 8 == 0, M arbitrary (the kernels are laid out
  *   for up to 64 rows; more run in passes of 64). M == 0 or N == 0 is a no-op,

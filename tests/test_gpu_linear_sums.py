@@ -25,12 +25,12 @@ def _name(request):
     torch.cuda.synchronize()
 
 
-def values(kind, M, N, K, seed):
+def values(kind, M, N, K, seed, device=DEV):
     """Rows of activations and of weights."""
-    g = torch.Generator(device=DEV).manual_seed(seed)
+    g = torch.Generator(device=device).manual_seed(seed)
 
     def normal(*shape):
-        return torch.randn(*shape, device=DEV, generator=g)
+        return torch.randn(*shape, device=device, generator=g)
 
     a, w = normal(M, K), normal(N, K)
     if kind == "positive":
@@ -117,3 +117,52 @@ def test_fp8_bf16_output_holds_13_bits_of_each_eight_products(M, N, K, kind):
     if kind == "positive":
         mean = mean + linear * (7 * 2.0 ** -14)
     check_mean(got, ref, mean * scale + mag * (4 * U), "C")
+
+
+def four_bits(w, G, dtype):
+    """Codes, scales and zero points of weights in groups of G, and the weights that they stand for."""
+    N, K = w.shape
+    g = w.view(N, K // G, G)
+    low, high = g.amin(dim=2).clamp_max(0), g.amax(dim=2).clamp_min(0)
+    s = ((high - low) / 15).to(dtype)
+    z = (-low / s.float()).round().clamp(0, 15)
+    q = ((g / s.float()[:, :, None]).round() + z[:, :, None]).clamp(0, 15)
+    return q, s, z
+
+
+def w4_reference(A, q, s, z, chunk=256):
+    """The product in 64 bits, and the size of what its sums pass through: for each group the terms a q and z a and their
+    sums, whichever is larger, scaled; the groups' as independent errors."""
+    M, (N, groups, G) = A.shape[0], q.shape
+    a = A.to(D).view(M, groups, G)
+    total, squares = a.sum(dim=2), (a * a).sum(dim=2)
+    ref, size = [], []
+    for n in range(0, N, chunk):
+        Q, S, Z = (t[n:n + chunk].to(D) for t in (q, s, z))
+        P = torch.matmul(a.transpose(0, 1).contiguous(), Q.permute(1, 2, 0).contiguous())       # groups, M, N
+        terms = torch.matmul((a * a).transpose(0, 1).contiguous(), (Q * Q).permute(1, 2, 0).contiguous())
+        S, Z, T = S.t()[:, None, :], Z.t()[:, None, :], total.t()[:, :, None]
+        ref.append((S * (P - Z * T)).sum(dim=0))
+        part = torch.maximum(terms, P * P) + Z * Z * torch.maximum(squares.t()[:, :, None], T * T)
+        size.append((S * S * part).sum(dim=0).sqrt())
+    return torch.cat(ref, dim=1), torch.cat(size, dim=1)
+
+
+# The vector units, the small matrix instructions with both numbers of loads, the tiles of both widths.
+W4_SUM_SHAPES = [(1, 4096, 8192, 128), (2, 8200, 4096, 64), (1, 4096, 2048, 32), (4, 2048, 4096, 128), (8, 2056, 4096, 64),
+                 (16, 2048, 1024, 32), (40, 2000, 4096, 128), (64, 18432, 512, 64), (200, 1000, 2048, 2048)]
+
+
+@pytest.mark.parametrize("M,N,K,G", W4_SUM_SHAPES)
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_w4_holds_fp32_sums_of_unrounded_weights(M, N, K, G, kind, dtype):
+    """K roundings of 2^-24 of the sums that codes and zero points enter apart."""
+    a, w = values(kind, M, N, K, 220)
+    A = a.to(dtype)
+    q, s, z = four_bits(w / K ** 0.5, G, dtype)
+    codes = q.to(torch.uint8).view(N, K)
+    codes = codes[:, 0::2] | (codes[:, 1::2] << 4)
+    ref, size = w4_reference(A, q, s, z)
+    got = pt.pipe_gemm_w4(A, codes, s, zeros=z.to(torch.uint8))
+    check_mean(got, ref, size * ((K ** 0.5 + 4) * U), "C")
