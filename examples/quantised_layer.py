@@ -29,8 +29,9 @@ class QuantisedLayer:
         self.row_scales = w.abs().amax(dim=1).clamp_min(2.0 ** -100) / 448
         self.e4m3 = (w / self.row_scales[:, None]).to(torch.float8_e4m3fn)
         g = w.view(w.shape[0], -1, GROUP)
-        low, high = g.amin(dim=2), g.amax(dim=2)
-        self.scales = ((high - low) / 15).to(weight.dtype)
+        # From zero or below to zero or above: the zero point is one of the 16 codes also where a group has one sign.
+        low, high = g.amin(dim=2).clamp_max(0), g.amax(dim=2).clamp_min(0)
+        self.scales = ((high - low) / 15).clamp_min(torch.finfo(weight.dtype).tiny).to(weight.dtype)
         self.zeros = (-low / self.scales.float()).round().clamp(0, 15).to(torch.uint8)
         q = (g / self.scales.float()[:, :, None]).round() + self.zeros[:, :, None]
         q = q.clamp(0, 15).to(torch.uint8).view(w.shape)
