@@ -594,10 +594,6 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_fp8_tile_kernel(Fp8
       slot = next;
     }
 
-    // As in the 16-bit GEMM's epilogue: the wave sleeps once before the first
-    // accumulator is read, which was seen to come too early there.
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_sleep(1);
     __builtin_amdgcn_sched_barrier(0);
     // Lane l holds row l % 32 and columns 8 (e / 4) + 4 (l / 32) + e % 4 of a
     // block. Rows of 128 bytes go through the wave's own staging buffer, its
