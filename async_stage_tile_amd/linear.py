@@ -101,8 +101,7 @@ def _matrix(t, name, dtype, device, shape=None):
             return rows, cols, cols
     except (AttributeError, ValueError):    # no tensor, or not two axes
         pass
-    if not isinstance(t, _torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
+    _tensor(t, name)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if device < 0:
@@ -116,8 +115,7 @@ def _matrix(t, name, dtype, device, shape=None):
 
 def _vector(t, name, dtype, device, n):
     """Address of a contiguous vector of n elements."""
-    if not isinstance(t, _torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
+    _tensor(t, name)
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if t.get_device() != device:
@@ -128,12 +126,24 @@ def _vector(t, name, dtype, device, n):
 
 
 def _dtype16(t, name):
-    if not isinstance(t, _torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    dtype = t.dtype
+    dtype = _tensor(t, name).dtype
     if _codes.get(dtype, PIPE_FP32) > PIPE_FP16:
         raise TypeError(f"{name} must be bfloat16 or float16, not {dtype}")
     return dtype
+
+
+def _tensor(t, name):
+    if not isinstance(t, _torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return t
+
+
+def _check_given(stream, workspace=None):
+    """The types of arguments whose attributes are used further on."""
+    if stream is not None and not isinstance(stream, _torch.cuda.Stream):
+        raise TypeError("stream must be a torch.cuda.Stream")
+    if workspace is not None:
+        _tensor(workspace, "workspace")
 
 
 def _make(made, stream, like, shape, dtype):
@@ -182,10 +192,12 @@ def pipe_rmsnorm(x, weight, residual=None, eps=1e-6, out_dtype=None, y=None, y_s
         out = _fast.rmsnorm(x, weight, residual, eps, out_dtype)
         if out is not NotImplemented:
             return out
+    _check_given(stream)
+    eps = float(eps)
     dtype = _dtype16(x, "x")
     dev = x.get_device()
     M, N, ld_x = _matrix(x, "x", dtype, dev)
-    out_dtype = out_dtype or (dtype if y is None else y.dtype)
+    out_dtype = out_dtype or (dtype if y is None else _tensor(y, "y").dtype)
     if out_dtype is not dtype and out_dtype is not _torch.float8_e4m3fn:
         raise TypeError(f"out_dtype must be {dtype} or float8_e4m3fn, not {out_dtype}")
     w = _vector(weight, "weight", dtype, dev, N)
@@ -235,6 +247,8 @@ def pipe_rmsnorm_backward(dy, x, weight, dh=None, eps=1e-6, dx=None, dweight=Non
         out = _fast.rmsnorm_backward(dy, x, weight, dh, eps)
         if out is not NotImplemented:
             return out
+    _check_given(stream, workspace)
+    eps = float(eps)
     dtype = _dtype16(x, "x")
     dev = x.get_device()
     M, N, ld_x = _matrix(x, "x", dtype, dev)
@@ -306,6 +320,7 @@ def pipe_gemm_fp8(A, a_scales, B, b_scales, C=None, out_dtype=None, workspace=No
         out = _fast.gemm_fp8(A, a_scales, B, b_scales, out_dtype)
         if out is not NotImplemented:
             return out
+    _check_given(stream, workspace)
     e4m3 = _torch.float8_e4m3fn
     dev = A.get_device() if isinstance(A, _torch.Tensor) else -1
     M, K, lda = _matrix(A, "A", e4m3, dev)
@@ -324,7 +339,7 @@ def pipe_gemm_fp8(A, a_scales, B, b_scales, C=None, out_dtype=None, workspace=No
         C = _make(made, stream, A, (M, N), out_dtype)
         ldc = N
     else:
-        out_dtype = out_dtype or C.dtype
+        out_dtype = out_dtype or _tensor(C, "C").dtype
         if out_dtype == e4m3 or out_dtype not in _codes:
             raise TypeError(f"C must be bfloat16, float16 or float32, not {out_dtype}")
         ldc = _matrix(C, "C", out_dtype, dev, (M, N))[2]
@@ -354,6 +369,7 @@ def pipe_gemm_w4(A, codes, scales, zeros=None, C=None, workspace=None, stream=No
         out = _fast.gemm_w4(A, codes, scales, zeros)
         if out is not NotImplemented:
             return out
+    _check_given(stream, workspace)
     dtype = _dtype16(A, "A")
     dev = A.get_device()
     M, K, lda = _matrix(A, "A", dtype, dev)
