@@ -3,6 +3,7 @@ spilled registers would take. Needs hipcc, no GPU."""
 import os
 import re
 import subprocess
+from concurrent.futures import ThreadPoolExecutor
 
 import pytest
 
@@ -23,7 +24,16 @@ def remarks(source, out):
     return dict(zip(names, scratch))
 
 
-@pytest.mark.parametrize("source", ["pipe_norm.hip", "pipe_gemm_fp8.hip", "pipe_gemm_w4.hip"])
-def test_no_scratch_memory(source, tmp_path):
-    found = remarks(source, os.path.join(tmp_path, "out.s"))
-    assert {k: v for k, v in found.items() if v} == {}
+SOURCES = ["pipe_norm.hip", "pipe_gemm_fp8.hip", "pipe_gemm_w4.hip"]
+
+
+@pytest.fixture(scope="module")
+def found(tmp_path_factory):
+    where = tmp_path_factory.mktemp("remarks")
+    with ThreadPoolExecutor(len(SOURCES)) as ex:
+        return dict(zip(SOURCES, ex.map(lambda s: remarks(s, os.path.join(where, s + ".s")), SOURCES)))
+
+
+@pytest.mark.parametrize("source", SOURCES)
+def test_no_scratch_memory(source, found):
+    assert {k: v for k, v in found[source].items() if v} == {}
