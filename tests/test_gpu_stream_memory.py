@@ -102,3 +102,30 @@ def test_no_output_reused_before_the_current_stream_has_read_it(name):
         pytest.skip("the streams share a queue")
     for g, ref in zip(got, want):
         assert torch.equal(g, ref)
+
+
+@pytest.mark.parametrize("name", ["rmsnorm", "rmsnorm_backward", "gemm_fp8", "gemm_w4", "tile_copy", "rowsum", "gemm_mainloop"])
+def test_captured_on_a_stream_that_joins_the_capture(name):
+    """The given stream is forked from the captured one: outputs and workspaces come from the graph's own pool, and every
+    replay writes them again."""
+    call = calls()[name]
+    want = tensors(call(None))
+    torch.cuda.synchronize()
+    main, side = torch.cuda.Stream(device=DEV), torch.cuda.Stream(device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        side.wait_stream(main)
+        out = call(side)
+        main.wait_stream(side)
+    out = out if isinstance(out, tuple) else (out,)
+    for _ in range(4):
+        for t in out:
+            t.view(torch.uint8).fill_(0x55)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        call(None)
+        torch.full((1 << 20,), 7.0, device=DEV).add_(1.0)
+        torch.cuda.synchronize()
+        for got, ref in zip(tensors(out), want):
+            assert torch.equal(got, ref)
