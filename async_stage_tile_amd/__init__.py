@@ -274,6 +274,16 @@ def _hold_for(stream, device, *tensors):
             t.record_stream(current)
 
 
+def _use_on(stream, *tensors):
+    """The caller's tensors (None skipped) in work on `stream`: their memory is not
+    handed out again before that work is done, however soon the caller drops them."""
+    if stream is None:
+        return
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 def matrix_geometry(shape, strides, name="matrix"):
     """(rows, cols, row pitch in elements) of a 2-D row-major view, or
     ValueError. Columns must be adjacent (unit stride) and rows must not
@@ -331,6 +341,7 @@ def pipe_tile_copy(src, dst=None, checksums=False, stream=None, **cfg):
                                   _ptr(chk), _stream(stream, dev))
     _check(st, "pipe_tile_copy")
     _hold_for(stream, dev, *made)
+    _use_on(stream, src, dst, *c.buffers)
     return (dst, chk) if checksums else dst
 
 
@@ -367,6 +378,7 @@ def pipe_rowsum(A, out=None, workspace=None, stream=None, **cfg):
                                wbytes, _stream(stream, dev))
     _check(st, "pipe_rowsum")
     _hold_for(stream, dev, *made)
+    _use_on(stream, A, out, workspace, *c.buffers)
     return out
 
 
@@ -386,6 +398,7 @@ def pipe_rowsum_noalloc(A, out, stream=None, **cfg):
         st = lib().pipe_rowsum_noalloc(_ptr(A), _ptr(out), M, N, lda, ctypes.byref(c),
                                        _stream(stream, dev))
     _check(st, "pipe_rowsum_noalloc")
+    _use_on(stream, A, out, *c.buffers)
     return out
 
 
@@ -455,6 +468,7 @@ def pipe_gemm_mainloop(A, B, C=None, stream=None, out_dtype=None, **cfg):
                                       ctypes.byref(c), _stream(stream, dev))
     _check(st, "pipe_gemm_mainloop")
     _hold_for(stream, dev, made)
+    _use_on(stream, A, B, C, *c.buffers)
     return C
 
 

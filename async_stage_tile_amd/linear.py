@@ -231,6 +231,7 @@ def pipe_rmsnorm(x, weight, residual=None, eps=1e-6, out_dtype=None, y=None, y_s
         raise ValueError("h goes with a residual")
     _call(fns.pipe_rmsnorm, "pipe_rmsnorm", dev, stream, made, x.data_ptr(), r_ptr, w, y.data_ptr(),
           scales, h_ptr, M, N, ld_x, ld_r, ld_y, ld_h, eps, _codes[dtype], _codes[out_dtype])
+    _pt._use_on(stream, x, weight, residual, y, y_scales, h)
     if residual is None:
         return (y, y_scales) if q8 else y
     return (y, y_scales, h) if q8 else (y, h)
@@ -273,6 +274,7 @@ def pipe_rmsnorm_backward(dy, x, weight, dh=None, eps=1e-6, dx=None, dweight=Non
     _call(fns.pipe_rmsnorm_backward, "pipe_rmsnorm_backward", dev, stream, made, dy.data_ptr(),
           x.data_ptr(), w, dh_ptr, dx.data_ptr(), dweight.data_ptr(), M, N, ld_dy, ld_x, ld_dh,
           ld_dx, eps, _codes[dtype], ws, ws_bytes)
+    _pt._use_on(stream, dy, x, weight, dh, dx, dweight, workspace)
     return dx, dweight
 
 
@@ -347,6 +349,7 @@ def pipe_gemm_fp8(A, a_scales, B, b_scales, C=None, out_dtype=None, workspace=No
                               (M, N, K), workspace, A, made, stream)
     _call(fns.pipe_gemm_fp8, "pipe_gemm_fp8", dev, stream, made, A.data_ptr(), sa, B.data_ptr(), sb,
           C.data_ptr(), M, N, K, lda, ldb, ldc, _codes[out_dtype], ws, ws_bytes)
+    _pt._use_on(stream, A, a_scales, B, b_scales, C, workspace)
     return C
 
 
@@ -394,4 +397,5 @@ def pipe_gemm_w4(A, codes, scales, zeros=None, C=None, workspace=None, stream=No
     _call(fns.pipe_gemm_w4, "pipe_gemm_w4", dev, stream, made, A.data_ptr(), codes.data_ptr(),
           scales.data_ptr(), z_ptr, C.data_ptr(), M, N, K, K // groups if groups else 0, lda,
           ld_codes, ld_scales, ld_zeros, ldc, _codes[dtype], ws, ws_bytes)
+    _pt._use_on(stream, A, codes, scales, zeros, C, workspace)
     return C

@@ -129,3 +129,47 @@ def test_captured_on_a_stream_that_joins_the_capture(name):
         torch.cuda.synchronize()
         for got, ref in zip(tensors(out), want):
             assert torch.equal(got, ref)
+
+
+def inputs_and_calls():
+    """As calls(), with the operands apart: (operands, what to do with them)."""
+    one = torch.ones(256, device=DEV)
+    rows = lambda: ints((512, 1024), -4, 4, BF, 1)
+    return {
+        "rmsnorm": ((rows(), ints((1024,), -4, 4, BF, 2), ints((512, 1024), -4, 4, BF, 9)),
+                    lambda t, s: pt.pipe_rmsnorm(t[0], t[1], residual=t[2], stream=s)),
+        "rmsnorm_backward": ((rows(), ints((512, 1024), -4, 4, BF, 9), ints((1024,), -4, 4, BF, 2), ints((512, 1024), -4, 4, BF, 10)),
+                             lambda t, s: pt.pipe_rmsnorm_backward(t[0], t[1], t[2], dh=t[3], stream=s)),
+        "gemm_fp8": ((ints((128, 8192), -4, 4, E4, 3), one[:128].clone(), ints((256, 8192), -4, 4, E4, 4), one),
+                     lambda t, s: pt.pipe_gemm_fp8(t[0], t[1], t[2].t(), t[3], stream=s)),
+        "gemm_w4": ((ints((40, 4096), -4, 4, BF, 5), ints((256, 2048), 0, 255, torch.uint8, 6),
+                     torch.ones(256, 32, device=DEV, dtype=BF), ints((256, 32), 0, 15, torch.uint8, 7)),
+                    lambda t, s: pt.pipe_gemm_w4(t[0], t[1], t[2], zeros=t[3], stream=s)),
+        "tile_copy": ((ints((1024, 1024), -4, 4, torch.float16, 7),), lambda t, s: pt.pipe_tile_copy(t[0], stream=s)),
+        "rowsum": ((ints((1024, 1024), -4, 4, torch.float16, 7),), lambda t, s: pt.pipe_rowsum(t[0], stream=s, split=4)),
+        "gemm_mainloop": ((rows(), ints((1024, 512), -2, 2, BF, 8)),
+                          lambda t, s: pt.pipe_gemm_mainloop(t[0], t[1], stream=s)),
+    }
+
+
+@pytest.mark.parametrize("name", ["rmsnorm", "rmsnorm_backward", "gemm_fp8", "gemm_w4", "tile_copy", "rowsum", "gemm_mainloop"])
+def test_no_operand_reused_before_the_given_stream_has_read_it(name):
+    """Operands that the caller drops right after the call, while the given stream has not begun it."""
+    operands, call = inputs_and_calls()[name]
+    want = tensors(call(operands, None))
+    sizes_in = [t.numel() * t.element_size() for t in operands]
+    side = torch.cuda.Stream(device=DEV)
+    call(operands, side)            # first calls of a stream may allocate
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(LONG)
+    out = call(operands, side)
+    del operands
+    fills = [torch.full((n,), 0x55, dtype=torch.uint8, device=DEV) for n in sizes_in for _ in range(24)]
+    torch.cuda.current_stream().synchronize()
+    early = side.query()
+    torch.cuda.synchronize()
+    if early:
+        pytest.skip("the streams share a queue")
+    for got, ref in zip(tensors(out), want):
+        assert torch.equal(got, ref)
