@@ -100,6 +100,11 @@ def work(case):
 # ---------------------------------------------------------------------------
 # The 4-bit form in plain operations
 # ---------------------------------------------------------------------------
+def _powers(exponent, dtype):
+    """Powers of two, exactly: pow() on the GPU rounds some of them."""
+    return torch.exp2(exponent.double()).to(dtype)[:, :, None]
+
+
 def _to_mx(x):
     """The rows' values in the 4-bit form, as (values of e2m1, exponents). A block's power of two is the largest one
     not above its largest magnitude, divided by 4: that magnitude becomes 4 to 8, and 6 is the most there is. Rounding
@@ -109,7 +114,7 @@ def _to_mx(x):
     v = x.view(M, K // BLOCK, BLOCK)
     top = v.abs().amax(dim=2)
     exponent = torch.where(top > 0, torch.frexp(top).exponent.to(torch.int32) - 3, -127).clamp(-127, 127)
-    q = torch.ldexp(v, -exponent[:, :, None])
+    q = v * _powers(-exponent, x.dtype)
     a = q.abs()
     step = 0.5 + 0.5 * (a >= 2) + (a >= 4)
     return (torch.round(a / step) * step).clamp(max=6.0).copysign(q), exponent
@@ -117,7 +122,7 @@ def _to_mx(x):
 
 def _mx_values(values, exponent):
     """What the 4-bit form stands for."""
-    return torch.ldexp(values, exponent[:, :, None]).flatten(1)
+    return (values * _powers(exponent, values.dtype)).flatten(1)
 
 
 def _mx_pack(values, exponent):
@@ -296,7 +301,7 @@ def _meaning(codes, scales):
     out = torch.empty(codes.shape[0], 2 * codes.shape[1], dtype=d, device=codes.device)
     out[:, 0::2] = table[(codes % 16).int()]
     out[:, 1::2] = table[torch.div(codes, 16, rounding_mode="floor").int()]
-    return out * torch.repeat_interleave(torch.pow(2.0, scales.to(d) - 127), BLOCK, dim=1)
+    return out * torch.repeat_interleave(torch.exp2(scales.to(d) - 127), BLOCK, dim=1)
 
 
 def _normed(s, N):
