@@ -580,7 +580,10 @@ device_status = pipe_device_status
 
 # The operators of a quantised linear layer (pipe_linear.h).
 from .linear import (  # noqa: E402
-    PIPE_BF16, PIPE_E4M3, PIPE_FP16, PIPE_FP32, PIPE_RMSNORM_MAX_N, linear_symbols, pipe_gemm_fp8,
-    pipe_gemm_fp8_workspace_bytes, pipe_gemm_w4, pipe_gemm_w4_workspace_bytes, pipe_rmsnorm,
-    pipe_rmsnorm_backward,
+    PIPE_BF16, PIPE_E4M3, PIPE_FP16, PIPE_FP32, PIPE_LAYERNORM_MAX_N, PIPE_MXFP4, PIPE_RMSNORM_MAX_N,
+    linear_symbols, pipe_gemm_fp8, pipe_gemm_fp8_workspace_bytes, pipe_gemm_w4,
+    pipe_gemm_w4_workspace_bytes, pipe_layernorm, pipe_layernorm_backward,
+    pipe_layernorm_backward_workspace_bytes, pipe_rmsnorm, pipe_rmsnorm_backward,
     pipe_rmsnorm_backward_workspace_bytes)
+from .mxfp4 import (  # noqa: E402
+    pipe_dequantize_mxfp4, pipe_gemm_mxfp4, pipe_gemm_mxfp4_workspace_bytes, pipe_quantize_mxfp4)

@@ -45,6 +45,9 @@ UNITS = [
     ("pipe_norm.hip", "pipe_norm.o", []),
     ("pipe_gemm_fp8.hip", "pipe_gemm_fp8.o", []),
     ("pipe_gemm_w4.hip", "pipe_gemm_w4.o", []),
+    ("pipe_layernorm.hip", "pipe_layernorm.o", []),
+    ("pipe_mx_quant.hip", "pipe_mx_quant.o", []),
+    ("pipe_gemm_mx.hip", "pipe_gemm_mx.o", []),
 ]
 # Kept for callers that list the tile-stream sources.
 SOURCES = sorted({u[0] for u in UNITS})

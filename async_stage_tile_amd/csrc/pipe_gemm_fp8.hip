@@ -24,28 +24,14 @@
 // registers for up to four (gemv_fp8_kernel), through a deep LDS ring for up to
 // 64 and for more of small layers (gemm_fp8_rows_kernel). Many rows:
 // gemm_fp8_tile_kernel.
-#include "pipe_device.hpp"
-#include "pipe_linear.hpp"
+#include "pipe_gemm_tiles.hpp"
 
 namespace pipe {
 
 namespace {
 
-template <int T>
-struct Step {
-  static constexpr int value = T;
-};
-
 __device__ __forceinline__ i32x8 join(u32x4 a, u32x4 b) {
   return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
-}
-
-__device__ __forceinline__ void dma_block_at(const uint8_t* base, uint32_t offset,
-                                             uint32_t lds_base) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-               :
-               : "v"(offset), "s"(base), "{m0}"(lds_base)
-               : "memory");
 }
 
 // Two e4m3 values as fp16: the low or the high half of a word.
@@ -205,16 +191,6 @@ struct Fp8Rows {
   static constexpr int kPitch = kN + 4;                // floats of a row of sums
   static_assert(kSlots >= 2 && kParts * 32 * FM * kPitch * 4 <= kSlots * kSlot, "LDS");
 };
-
-// Waits for the loads of stage ks of `count` in a ring of S slots, LOADS a stage
-// and wave: those of younger stages may stay under way.
-template <int S, int LOADS>
-__device__ __forceinline__ void wait_stage(int ks, int count) {
-  if (ks + S - 1 <= count)
-    wait_vmcnt<(S - 2) * LOADS>();
-  else
-    wait_vmcnt_mul<LOADS>(count - 1 - ks);
-}
 
 template <int FM, int WN, int OUT>
 __global__ void __launch_bounds__(512) gemm_fp8_rows_kernel(Fp8Params p) {
@@ -384,16 +360,6 @@ __global__ void __launch_bounds__(512) gemm_fp8_rows_kernel(Fp8Params p) {
 constexpr int kFp8StageK = 128;
 constexpr int kFp8Staging = 4096;   // bytes of a wave's part of the epilogue
 
-template <int OUT>
-struct Out16;
-template <>
-struct Out16<0> {
-  using type = __bf16;
-};
-template <>
-struct Out16<1> {
-  using type = _Float16;
-};
 // Four floats at any 4-byte boundary.
 typedef float f32x4_by4 __attribute__((ext_vector_type(4), aligned(4)));
 
@@ -408,25 +374,6 @@ struct Fp8Tile {
                 "a wave loads an even number of blocks of each operand");
   static_assert(S * kStage + kWaves * kFp8Staging <= 163840, "the ring and the staging fit");
 };
-
-// Output tile and K range of a work item. Workgroups go to the 8 XCDs in turn:
-// the items are dealt so that each XCD walks one contiguous run of the order,
-// and the order runs down bands of 4 tile rows, column by column, so that the
-// tiles an XCD holds at once share few A and B rows.
-__device__ __forceinline__ void fp8_item(const Fp8Params& p, int item, int items, int& tm, int& tn,
-                                         int& split) {
-  constexpr int kBand = 4;
-  const int per = items >> 3, odd = items & 7, xcd = item & 7;
-  int q = xcd * per + min(xcd, odd) + (item >> 3);
-  split = q % p.splits;
-  q /= p.splits;
-  const int band = kBand * p.tiles_n;
-  const int first = q / band * kBand;
-  const int rows = min(p.tiles_m - first, kBand);
-  const int local = q % band;
-  tm = first + local % rows;
-  tn = local / rows;
-}
 
 template <int FM, int FN, int WM, int WN, int S, int PER_CU, int OUT>
 __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_fp8_tile_kernel(Fp8Params p) {
@@ -461,7 +408,7 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_fp8_tile_kernel(Fp8
   int f_k = 0;
   auto open = [&]() {
     int tm, tn, split;
-    fp8_item(p, f_item, items, tm, tn, split);
+    tile_item(p, f_item, items, tm, tn, split);
     const int row_a = tm * Tile::kRowsA, row_b = tn * Tile::kRowsB;
 #pragma unroll
     for (int j = 0; j < Tile::kLoads; ++j) {
@@ -562,7 +509,7 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_fp8_tile_kernel(Fp8
   int slot = 0;
   for (int item = (int)blockIdx.x; item < items; item += (int)gridDim.x) {
     int tm, tn, split;
-    fp8_item(p, item, items, tm, tn, split);
+    tile_item(p, item, items, tm, tn, split);
     const int first = split * per, count = min(per, p.steps - first);
     const int tail = p.K - (first + count - 1) * kFp8StageK;   // bytes of K in the last stage, and more
 #pragma unroll
@@ -704,16 +651,6 @@ struct Fp8Plan {
   int tiles_m, tiles_n, splits, steps;
   bool wide;   // kRows: 64 columns
 };
-
-int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
-
-// Equal shares of `steps` stages for at most `most` workgroups a tile, `least`
-// stages each; no share is empty.
-int shares(int steps, int64_t most, int least) {
-  int64_t n = most < steps / least ? most : steps / least;
-  if (n <= 1) return 1;
-  return ceil_div(steps, ceil_div(steps, n));
-}
 
 Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K) {
   Fp8Plan c{kVec, 0, 0, 1, 0, false};

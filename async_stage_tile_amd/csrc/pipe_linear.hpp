@@ -27,6 +27,26 @@ struct NormGradParams {
   float inv_n, eps;
 };
 
+struct LayerNormParams {
+  const uint8_t *x, *residual, *weight, *bias;
+  uint8_t *y, *h, *scales;  // scales: fp32, one a row, or e8m0
+  int64_t ld_x, ld_residual, ld_y, ld_h, ld_scales;  // bytes
+  int64_t M;
+  int32_t chunks;  // 8-element chunks in a row
+  float inv_n, eps;
+};
+
+struct LayerNormGradParams {
+  const uint8_t *dy, *x, *weight, *dh;
+  uint8_t* dx;
+  float *sum_weight, *sum_bias;  // a workgroup's are sum_stride floats further each
+  int64_t sum_stride;
+  int64_t ld_dy, ld_x, ld_dh, ld_dx;  // bytes
+  int64_t M;
+  int32_t chunks;
+  float inv_n, eps;
+};
+
 struct Fp8Params {
   const uint8_t *A, *B;
   const float *a_scales, *b_scales;
@@ -53,6 +73,10 @@ struct W4Params {
 hipError_t launch_rmsnorm(const NormParams& p, int type, bool q8, hipStream_t stream);
 int64_t rmsnorm_grad_partials(int64_t M, int64_t N);  // rows of N floats
 hipError_t launch_rmsnorm_grad(NormGradParams p, float* dweight, int type, hipStream_t stream);
+hipError_t launch_layernorm(const LayerNormParams& p, int type, int out, hipStream_t stream);  // out: 0 type, 1 e4m3, 2 4-bit
+int64_t layernorm_grad_partials(int64_t M, int64_t N);  // rows of N floats
+hipError_t launch_layernorm_grad(LayerNormGradParams p, float* partials, float* dweight, float* dbias,
+                                 int type, hipStream_t stream);
 int64_t gemm_fp8_partials(int64_t M, int64_t N, int64_t K);  // floats of workspace
 hipError_t launch_gemm_fp8(Fp8Params p, int out_type, hipStream_t stream);
 int64_t gemm_w4_partials(int64_t M, int64_t N, int64_t K);  // floats of workspace

@@ -17,14 +17,11 @@
 // workgroups meet in a second small kernel, in a fixed order.
 //
 // Both are bound by memory: a few fp32 operations for every byte moved.
-#include "pipe_linear.hpp"
+#include "pipe_norm.hpp"
 
 namespace pipe {
 
 namespace {
-
-constexpr float kE4m3Max = 448.f;
-constexpr float kAmaxMin = 0x1p-100f;  // keeps the scale and its reciprocal normal numbers
 
 // The sums of the waves of one row: TPR threads a row, in a workgroup of WG.
 template <int TPR, int WG, bool MAX>
@@ -33,16 +30,6 @@ struct RowExchange {
   float sum[2][kWaves];
   uint32_t top[MAX ? kWaves : 1];
 };
-
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-
-// Keeps the 16-bit pairs as what stays in registers across a reduction: without
-// it the compiler keeps their fp32 values, twice the registers.
-template <int CH>
-__device__ __forceinline__ void keep_packed(u32x4 (&v)[CH]) {
-#pragma unroll
-  for (int i = 0; i < CH; ++i) asm("" : "+v"(v[i]));
-}
 
 // One row per TPR threads, WG / TPR rows a workgroup; a thread holds CH chunks
 // of 8 elements, chunk index t + TPR * i. 8192 x 8192 with residual and e4m3

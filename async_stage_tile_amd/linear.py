@@ -4,6 +4,10 @@
     pipe_rmsnorm_backward(dy, x, weight, dh=None, ...) -> dx, dweight
     pipe_gemm_fp8(A, a_scales, B, b_scales, ...)       -> C
     pipe_gemm_w4(A, codes, scales, zeros=None, ...)    -> C
+    pipe_layernorm(x, weight, bias=None, residual=None, ...)  -> y [, scales] [, h]
+    pipe_layernorm_backward(dy, x, weight, dh=None, ...)      -> dx, dweight, dbias
+
+and, in ``mxfp4.py``, those of the microscaled 4-bit form.
 
 Argument marshalling only, as in the package's other functions: the work is
 done by the HIP kernels of the shared library, on the given stream or the
@@ -27,7 +31,9 @@ PIPE_BF16 = 0
 PIPE_FP16 = 1
 PIPE_FP32 = 2
 PIPE_E4M3 = 3
+PIPE_MXFP4 = 4
 PIPE_RMSNORM_MAX_N = 32768
+PIPE_LAYERNORM_MAX_N = 32768
 
 _c = ctypes
 _V, _L, _F, _I, _Z = _c.c_void_p, _c.c_int64, _c.c_float, _c.c_int, _c.c_size_t
@@ -39,7 +45,15 @@ _LINEAR_SIGS = {
     "pipe_gemm_fp8": [_V] * 5 + [_L] * 6 + [_I, _V, _Z, _V],
     "pipe_gemm_w4_workspace_bytes": [_L, _L, _L, _c.POINTER(_Z)],
     "pipe_gemm_w4": [_V] * 5 + [_L] * 9 + [_I, _V, _Z, _V],
+    "pipe_layernorm": [_V] * 7 + [_L] * 7 + [_F, _I, _I, _V],
+    "pipe_layernorm_backward_workspace_bytes": [_L, _L, _c.POINTER(_Z)],
+    "pipe_layernorm_backward": [_V] * 7 + [_L] * 6 + [_F, _I, _V, _Z, _V],
+    "pipe_quantize_mxfp4": [_V] * 3 + [_L] * 5 + [_I, _V],
+    "pipe_dequantize_mxfp4": [_V] * 3 + [_L] * 5 + [_I, _V],
+    "pipe_gemm_mxfp4_workspace_bytes": [_L, _L, _L, _c.POINTER(_Z)],
+    "pipe_gemm_mxfp4": [_V] * 5 + [_L] * 8 + [_I, _V, _Z, _V],
 }
+_FIRST = 7      # the signatures that the C++ marshalling's bind() takes
 
 _fns = None
 _lock = threading.Lock()
@@ -73,7 +87,8 @@ def _setup():
                 setattr(fns, name, fn)
             import torch
             _codes.update({torch.bfloat16: PIPE_BF16, torch.float16: PIPE_FP16,
-                           torch.float32: PIPE_FP32, torch.float8_e4m3fn: PIPE_E4M3})
+                           torch.float32: PIPE_FP32, torch.float8_e4m3fn: PIPE_E4M3,
+                           torch.float4_e2m1fn_x2: PIPE_MXFP4})
             # The address alone, without the Stream object around it (1 us a call).
             _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
                 lambda device: torch.cuda.current_stream(device).cuda_stream)
@@ -84,7 +99,7 @@ def _setup():
                 fast = None
             if fast is not None:
                 fast.bind(_current_stream, *(
-                    _c.cast(getattr(fns, n), _V).value for n in _LINEAR_SIGS))
+                    _c.cast(getattr(fns, n), _V).value for n in list(_LINEAR_SIGS)[:_FIRST]))
             _fast = fast
             _fns = fns
     return _fns
@@ -336,13 +351,13 @@ def pipe_gemm_fp8(A, a_scales, B, b_scales, C=None, out_dtype=None, workspace=No
     made = []
     if C is None:
         out_dtype = out_dtype or _torch.bfloat16
-        if out_dtype == e4m3 or out_dtype not in _codes:
+        if _codes.get(out_dtype, PIPE_E4M3) > PIPE_FP32:
             raise TypeError(f"out_dtype must be bfloat16, float16 or float32, not {out_dtype}")
         C = _make(made, stream, A, (M, N), out_dtype)
         ldc = N
     else:
         out_dtype = out_dtype or _tensor(C, "C").dtype
-        if out_dtype == e4m3 or out_dtype not in _codes:
+        if _codes.get(out_dtype, PIPE_E4M3) > PIPE_FP32:
             raise TypeError(f"C must be bfloat16, float16 or float32, not {out_dtype}")
         ldc = _matrix(C, "C", out_dtype, dev, (M, N))[2]
     ws, ws_bytes = _workspace(fns.pipe_gemm_fp8_workspace_bytes, "pipe_gemm_fp8_workspace_bytes",
@@ -399,3 +414,141 @@ def pipe_gemm_w4(A, codes, scales, zeros=None, C=None, workspace=None, stream=No
           ld_codes, ld_scales, ld_zeros, ldc, _codes[dtype], ws, ws_bytes)
     _pt._use_on(stream, A, codes, scales, zeros, C, workspace)
     return C
+
+
+def _padded(n):
+    """The pitch of n bytes' rows that start at multiples of 16 bytes."""
+    return -(-n // 16) * 16
+
+
+def _make_scales(made, stream, like, rows, blocks):
+    """e8m0 scales of rows that start at multiples of 16 bytes."""
+    return _make(made, stream, like, (rows, _padded(blocks)), _torch.float8_e8m0fnu)[:, :blocks]
+
+
+def _scales(t, name, device, rows, blocks):
+    """Pitch of a matrix of e8m0 scales. The kernels read its rows in groups of
+    16 bytes, so the last row's group has to lie in the tensor's memory."""
+    pitch = _matrix(t, name, _torch.float8_e8m0fnu, device, (rows, blocks))[2]
+    if rows <= 1:
+        pitch = _padded(blocks)
+    if rows and t.storage_offset() + (rows - 1) * pitch + _padded(blocks) > t.untyped_storage().nbytes():
+        raise ValueError(f"{name}: the memory of the last row must reach a multiple of 16 bytes "
+                         "(rows of scales are read in groups of 16)")
+    return pitch
+
+
+def pipe_layernorm(x, weight, bias=None, residual=None, eps=1e-5, out_dtype=None, y=None, y_scales=None,
+                   h=None, stream=None):
+    """Layer norm of each row, the residual added first where one is given:
+    h = x + residual (rounded to x's type), m = mean(h),
+    y = (h - m) * rsqrt(mean((h - m)^2) + eps) * weight + bias.
+
+    x, residual: (M, N) bfloat16 or float16; weight, bias: (N). out_dtype: x's
+    type (the default); torch.float8_e4m3fn, whose rows are scaled by scales[m] =
+    max|y[m]| / 448; or torch.float4_e2m1fn_x2, the microscaled 4-bit form of
+    pipe_quantize_mxfp4 (N a multiple of 32). Returns y; with e4m3 or 4 bits y,
+    scales; with a residual the new stream h last: (y, h) or (y, scales, h).
+    h may be x or residual itself to update the stream in place."""
+    fns = _fns or _setup()
+    _check_given(stream)
+    eps = float(eps)
+    dtype = _dtype16(x, "x")
+    dev = x.get_device()
+    M, N, ld_x = _matrix(x, "x", dtype, dev)
+    out_dtype = out_dtype or (dtype if y is None else _tensor(y, "y").dtype)
+    q8, mx = out_dtype is _torch.float8_e4m3fn, out_dtype is _torch.float4_e2m1fn_x2
+    if out_dtype is not dtype and not q8 and not mx:
+        raise TypeError(f"out_dtype must be {dtype}, float8_e4m3fn or float4_e2m1fn_x2, not {out_dtype}")
+    if mx and N % 32:
+        raise ValueError(f"rows of {N} columns have no 4-bit form: blocks are of 32")
+    w = _vector(weight, "weight", dtype, dev, N)
+    b = 0 if bias is None else _vector(bias, "bias", dtype, dev, N)
+    made = []
+    shape = (M, N // 2) if mx else (M, N)
+    if y is None:
+        y = _make(made, stream, x, shape, out_dtype)
+        ld_y = shape[1]
+    else:
+        ld_y = _matrix(y, "y", out_dtype, dev, shape)[2]
+    scales = ld_s = 0
+    if mx:
+        if y_scales is None:
+            y_scales = _make_scales(made, stream, x, M, N // 32)
+        ld_s = _scales(y_scales, "y_scales", dev, M, N // 32)
+        scales = y_scales.data_ptr()
+    elif q8:
+        if y_scales is None:
+            y_scales = _make(made, stream, x, (M,), _torch.float32)
+            scales = y_scales.data_ptr()
+        else:
+            scales = _vector(y_scales, "y_scales", _torch.float32, dev, M)
+    elif y_scales is not None:
+        raise ValueError("y_scales go with an e4m3 or a 4-bit output")
+    r_ptr = h_ptr = ld_r = ld_h = 0
+    if residual is not None:
+        ld_r = _matrix(residual, "residual", dtype, dev, (M, N))[2]
+        r_ptr = residual.data_ptr()
+        if h is None:
+            h = _make(made, stream, x, (M, N), dtype)
+            ld_h = N
+        else:
+            ld_h = _matrix(h, "h", dtype, dev, (M, N))[2]
+        h_ptr = h.data_ptr()
+    elif h is not None:
+        raise ValueError("h goes with a residual")
+    _call(fns.pipe_layernorm, "pipe_layernorm", dev, stream, made, x.data_ptr(), r_ptr, w, b, y.data_ptr(),
+          scales, h_ptr, M, N, ld_x, ld_r, ld_y, ld_s, ld_h, eps, _codes[dtype], _codes[out_dtype])
+    _pt._use_on(stream, x, weight, bias, residual, y, y_scales, h)
+    out = (y, y_scales) if q8 or mx else (y,)
+    if residual is not None:
+        out += (h,)
+    return out if len(out) > 1 else y
+
+
+def pipe_layernorm_backward_workspace_bytes(M, N) -> int:
+    need = _Z(0)
+    st = (_fns or _setup()).pipe_layernorm_backward_workspace_bytes(M, N, ctypes.byref(need))
+    _pt._check(st, "pipe_layernorm_backward_workspace_bytes")
+    return need.value
+
+
+def pipe_layernorm_backward(dy, x, weight, dh=None, eps=1e-5, dx=None, dweight=None, dbias=None,
+                            workspace=None, stream=None):
+    """Gradient of pipe_layernorm's y for its normalised input x (its h where a
+    residual was added): dx (x's type), dweight and dbias (float32). dh: the
+    gradient that reaches h along the residual stream, added to dx before its
+    rounding; dx is then the gradient of both addends."""
+    fns = _fns or _setup()
+    _check_given(stream, workspace)
+    eps = float(eps)
+    dtype = _dtype16(x, "x")
+    dev = x.get_device()
+    M, N, ld_x = _matrix(x, "x", dtype, dev)
+    ld_dy = _matrix(dy, "dy", dtype, dev, (M, N))[2]
+    w = _vector(weight, "weight", dtype, dev, N)
+    dh_ptr = ld_dh = 0
+    if dh is not None:
+        ld_dh = _matrix(dh, "dh", dtype, dev, (M, N))[2]
+        dh_ptr = dh.data_ptr()
+    made = []
+    if dx is None:
+        dx = _make(made, stream, x, (M, N), dtype)
+        ld_dx = N
+    else:
+        ld_dx = _matrix(dx, "dx", dtype, dev, (M, N))[2]
+    sums = []
+    for t, name in ((dweight, "dweight"), (dbias, "dbias")):
+        if t is None:
+            t = _make(made, stream, x, (N,), _torch.float32)
+        else:
+            _vector(t, name, _torch.float32, dev, N)
+        sums.append(t)
+    dweight, dbias = sums
+    ws, ws_bytes = _workspace(fns.pipe_layernorm_backward_workspace_bytes,
+                              "pipe_layernorm_backward_workspace_bytes", (M, N), workspace, x, made, stream)
+    _call(fns.pipe_layernorm_backward, "pipe_layernorm_backward", dev, stream, made, dy.data_ptr(),
+          x.data_ptr(), w, dh_ptr, dx.data_ptr(), dweight.data_ptr(), dbias.data_ptr(), M, N, ld_dy, ld_x,
+          ld_dh, ld_dx, eps, _codes[dtype], ws, ws_bytes)
+    _pt._use_on(stream, dy, x, weight, dh, dx, dweight, dbias, workspace)
+    return dx, dweight, dbias
