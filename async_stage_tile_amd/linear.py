@@ -53,7 +53,7 @@ _LINEAR_SIGS = {
     "pipe_gemm_mxfp4_workspace_bytes": [_L, _L, _L, _c.POINTER(_Z)],
     "pipe_gemm_mxfp4": [_V] * 5 + [_L] * 8 + [_I, _V, _Z, _V],
 }
-_FIRST = 7      # the signatures that the C++ marshalling's bind() takes
+_FIRST = 7      # the C++ marshalling's bind() takes so many, bind_layer() the rest
 
 _fns = None
 _lock = threading.Lock()
@@ -98,8 +98,9 @@ def _setup():
             except ImportError:     # not built, or for another Python
                 fast = None
             if fast is not None:
-                fast.bind(_current_stream, *(
-                    _c.cast(getattr(fns, n), _V).value for n in list(_LINEAR_SIGS)[:_FIRST]))
+                at = [_c.cast(getattr(fns, n), _V).value for n in _LINEAR_SIGS]
+                fast.bind(_current_stream, *at[:_FIRST])
+                fast.bind_layer(*at[_FIRST:])
             _fast = fast
             _fns = fns
     return _fns
@@ -451,6 +452,10 @@ def pipe_layernorm(x, weight, bias=None, residual=None, eps=1e-5, out_dtype=None
     scales; with a residual the new stream h last: (y, h) or (y, scales, h).
     h may be x or residual itself to update the stream in place."""
     fns = _fns or _setup()
+    if _fast and stream is None and y is None and h is None and y_scales is None:
+        out = _fast.layernorm(x, weight, bias, residual, eps, out_dtype)
+        if out is not NotImplemented:
+            return out
     _check_given(stream)
     eps = float(eps)
     dtype = _dtype16(x, "x")
@@ -520,6 +525,10 @@ def pipe_layernorm_backward(dy, x, weight, dh=None, eps=1e-5, dx=None, dweight=N
     gradient that reaches h along the residual stream, added to dx before its
     rounding; dx is then the gradient of both addends."""
     fns = _fns or _setup()
+    if _fast and stream is None and dx is None and dweight is None and dbias is None and workspace is None:
+        out = _fast.layernorm_backward(dy, x, weight, dh, eps)
+        if out is not NotImplemented:
+            return out
     _check_given(stream, workspace)
     eps = float(eps)
     dtype = _dtype16(x, "x")

@@ -57,6 +57,10 @@ def pipe_quantize_mxfp4(x, codes=None, scales=None, stream=None):
     ties to the even code, and what passes 6 becomes 6. A block with a NaN or an
     infinity has a NaN scale."""
     fns = _setup()
+    if _l._fast and stream is None and codes is None and scales is None:
+        made = _l._fast.quantize_mxfp4(x)
+        if made is not NotImplemented:
+            return made
     _l._check_given(stream)
     dev = _device(x, "x")
     dtype = _wide_dtype(x.dtype, "x")
@@ -83,6 +87,10 @@ def pipe_dequantize_mxfp4(codes, scales, out_dtype=None, out=None, stream=None):
     default), float16 or float32. fp16 rounds what it cannot hold; bf16 and fp32
     hold every value below 2^128, and so all that pipe_quantize_mxfp4 makes."""
     fns = _setup()
+    if _l._fast and stream is None and out is None:
+        made = _l._fast.dequantize_mxfp4(codes, scales, out_dtype)
+        if made is not NotImplemented:
+            return made
     _l._check_given(stream)
     dev = _device(codes, "codes")
     M, K, ld_codes, ld_scales = _form(codes, scales, ("codes", "scales"), dev)
@@ -110,9 +118,13 @@ def pipe_gemm_mxfp4_workspace_bytes(M, N, K) -> int:
 def pipe_gemm_mxfp4(A, a_scales, W, w_scales, C=None, out_dtype=None, workspace=None, stream=None):
     """C = A @ W.T of M rows A and N rows W (a weight) in the microscaled 4-bit form,
     K columns each. C: (M, N) bfloat16 (the default), float16 or float32. The 32
-    products of two blocks add up exactly, the blocks in fp32. Pairs of rows and
-    pipe_layernorm's 4-bit output go in as they are."""
+    products of two blocks add up exactly, the blocks in fp32. What pipe_quantize_mxfp4
+    and pipe_layernorm give goes in as it is."""
     fns = _setup()
+    if _l._fast and stream is None and C is None and workspace is None:
+        made = _l._fast.gemm_mxfp4(A, a_scales, W, w_scales, out_dtype)
+        if made is not NotImplemented:
+            return made
     _l._check_given(stream, workspace)
     dev = _device(A, "A")
     M, K, lda, ld_as = _form(A, a_scales, ("A", "a_scales"), dev)
