@@ -30,6 +30,13 @@ namespace {
 
 constexpr int kBlock = 16;   // bytes of a block of 32 k's
 
+struct MxPackParams {
+  const uint8_t *a, *w;
+  uint8_t *to_a, *to_w;
+  int64_t ld_a, ld_w;
+  int32_t rows_a, rows_w, blocks_a, pairs;   // blocks of 64 rows
+};
+
 // acc + x y over 64 k's of 32 rows each; byte SEL of the scale words counts.
 template <int SEL>
 __device__ __forceinline__ f32x16 mx_mma(u32x4 x, u32x4 y, f32x16 acc, uint32_t sx, uint32_t sy) {
@@ -40,7 +47,11 @@ __device__ __forceinline__ f32x16 mx_mma(u32x4 x, u32x4 y, f32x16 acc, uint32_t 
 
 // A use of a sum ahead of a branch: the compiler would else move its MFMAs behind
 // it, out of the reads and loads they go with.
-__device__ __forceinline__ void keep_sum(f32x16 v) { asm volatile("" : : "v"(v)); }
+template <bool ACC>
+__device__ __forceinline__ void keep_sum(f32x16 v) {
+  if constexpr (ACC) asm volatile("" : : "a"(v));
+  else asm volatile("" : : "v"(v));
+}
 
 // ---------------------------------------------------------------------------
 // One to four rows of A. A lane keeps 32 k's of every row in registers, as fp16
@@ -333,19 +344,21 @@ __global__ void __launch_bounds__(512) gemm_mx_rows_kernel(MxGemmParams p) {
 // direct-to-LDS block; 16-byte chunk c of row r lies at place c ^ ((r >> 1) & 7),
 // which spreads the reads of one chunk of 16 consecutive rows over all 64 banks. A
 // stage is four MFMA steps of 64 k; half h (32 lanes) of step t's fragments takes
-// chunk 4 h + t, so that its four scales are one word.
+// chunk 2 t + h.
 //
 // The scales of a row and two stages are 16 bytes: one direct-to-LDS block a 64 rows
 // and pair of stages, into a ring of its own (S pairs: a product of K <= 256 has a
 // pair for each stage).
 //
-// Fragments are read one step ahead. Before the last step of a stage comes one
-// barrier: every wave has read all of this stage's slot, and its own loads of the
-// next stage have landed. The last step's MFMAs go with the loads of the stage S
-// ahead, into this stage's slot, and the reads of the next stage's first fragments
-// and scales. The loads near the end fetch the last stage again, so that the loop has
-// no branch and its wait one count (the scales' loads come on top of it, which only
-// makes the wait longer).
+// Fragments are read one step ahead, all within the first two MFMAs. Before the last
+// step of a stage comes one barrier: every wave has read all of this stage's slot, and
+// its own loads of the next stage have landed. The last step's MFMAs go with the loads
+// of the stage S ahead, into this stage's slot, and the reads of the next stage's
+// first fragments and scales; the third step's with the addresses of those loads,
+// without a branch but at an item's end. The loads near the end fetch the last stage
+// again, so that the wait has one count (the scales' loads come on top of it, which
+// only makes the wait longer). C's stores are non-temporal, and the first wait behind
+// an epilogue does not wait for them: they leave beside the next item's first stage.
 //
 // A load's address is a scalar base, which moves on, and a 32-bit offset a lane that
 // stays: rows of up to 2^24 bytes. Rows past M and N are read from the last row and
@@ -395,18 +408,10 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_mx_tile_kernel(MxGe
   const int chunk0 = (lane & 7) ^ (lane >> 4);
   int f_item = (int)blockIdx.x, f_stage, f_last;   // the item and stage that the next loads fetch
   int f_pair = 0;                                  // the slot of its scales
-  bool f_scales = true;                            // whether they are still to be fetched
+  bool f_scales = true, f_more = true;             // whether they are still to be fetched
   const uint8_t *ga, *gb;
   const uint8_t* gs[Tile::kScaleLoads];
-  uint32_t off[Tile::kLoads], scale_off[Tile::kScaleLoads], shift[2];
-  auto set_shift = [&](int tail) {   // tail: bytes of K in the stage
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int at = (chunk0 ^ (e << 2)) * kBlock;
-      shift[e] = at >= tail ? at : 0;
-    }
-  };
-  int f_k = 0;
+  uint32_t off[Tile::kLoads], scale_off[Tile::kScaleLoads], shift[2], last_shift[2];
   auto open = [&]() {
     int tm, tn, split;
     tile_item(p, f_item, items, tm, tn, split);
@@ -420,7 +425,7 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_mx_tile_kernel(MxGe
                    (uint32_t)(of_a ? p.lda : p.ldw) +
                (uint32_t)(chunk0 ^ ((q & 1) << 2)) * kBlock;
     }
-    f_k = split * per * kTileStage;
+    const int f_k = split * per * kTileStage;
     f_stage = 0;
     f_last = min(per, p.steps - split * per) - 1;   // >= 0: the host leaves no split empty
     ga = p.A + row_a * p.lda + f_k;
@@ -431,35 +436,46 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_mx_tile_kernel(MxGe
       // rows of W that are not used.
       const int r = (wave * Tile::kScaleLoads + j) * 64;
       const bool of_a = r < Tile::kRowsA;
-      gs[j] = (of_a ? p.a_scales + row_a * p.ld_as : p.w_scales + row_b * p.ld_ws) + f_k / kBlock;
+      const int64_t pair = f_k / (2 * kTileStage);
+      gs[j] = of_a ? p.a_scales + row_a * p.ld_as + pair * p.step_as
+                   : p.w_scales + row_b * p.ld_ws + pair * p.step_ws;
       scale_off[j] = (uint32_t)(of_a ? min(r + lane, p.M - row_a - 1)
                                      : min(r - Tile::kRowsA + lane, p.N - row_b - 1)) *
                      (uint32_t)(of_a ? p.ld_as : p.ld_ws);
     }
-    set_shift(p.bytes - f_k);
-  };
-  auto next_pair = [&]() { f_pair = f_pair + 1 == S ? 0 : f_pair + 1; };
-  auto advance = [&]() {
-    if (f_stage < f_last) {
-      ++f_stage;
-      f_k += kTileStage;
-      ga += kTileStage;
-      gb += kTileStage;
-      f_scales = (f_stage & 1) == 0;
-      if (f_scales) {
-        next_pair();
+    // Chunks past K of the last stage, as far back as its first one.
+    const int tail = p.bytes - f_k - f_last * kTileStage;
 #pragma unroll
-        for (int j = 0; j < Tile::kScaleLoads; ++j) gs[j] += 2 * kTileStage / kBlock;
-      }
-      if (f_stage == f_last) set_shift(p.bytes - f_k);
-    } else if (f_item + (int)gridDim.x < items) {
-      f_item += (int)gridDim.x;
-      f_scales = true;
-      next_pair();
-      open();
-    } else {
-      f_scales = false;
+    for (int e = 0; e < 2; ++e) {
+      const int at = (chunk0 ^ (e << 2)) * kBlock;
+      last_shift[e] = at >= tail ? at : 0;
     }
+  };
+  auto set_shift = [&]() {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) shift[e] = f_stage == f_last ? last_shift[e] : 0u;
+  };
+  // On to the next stage: of this item without a branch, then of the next one.
+  auto advance = [&]() {
+    const bool more = f_stage < f_last;
+    f_more = more;
+    f_stage += more ? 1 : 0;
+    ga += more ? kTileStage : 0;
+    gb += more ? kTileStage : 0;
+    f_scales = more && (f_stage & 1) == 0;
+    f_pair = f_scales ? (f_pair + 1 == S ? 0 : f_pair + 1) : f_pair;
+#pragma unroll
+    for (int j = 0; j < Tile::kScaleLoads; ++j)
+      gs[j] += !f_scales ? 0 : (wave * Tile::kScaleLoads + j) * 64 < Tile::kRowsA ? p.step_as : p.step_ws;
+    set_shift();
+  };
+  auto next_item = [&]() {
+    if (f_more || f_item + (int)gridDim.x >= items) return;
+    f_item += (int)gridDim.x;
+    f_scales = true;
+    f_pair = f_pair + 1 == S ? 0 : f_pair + 1;
+    open();
+    set_shift();
   };
   auto load = [&](int slot, int j) {
     if (j < Tile::kLoadsA)
@@ -477,36 +493,46 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_mx_tile_kernel(MxGe
   // Row 32 i + li of a wave's rows: (r >> 1) & 7 is (li >> 1) & 7 for every i.
   const uint8_t* frag_a = &ring[0][0] + (wm * FM * 32 + li) * kTileStage;
   const uint8_t* frag_b = &ring[0][0] + (Tile::kRowsA + wn * FN * 32 + li) * kTileStage;
-  const uint8_t* scale_a = &scale_ring[0][0] + (wm * FM * 32 + li) * 16 + lh * 4;
-  const uint8_t* scale_b = &scale_ring[0][0] + (Tile::kRowsA + wn * FN * 32 + li) * 16 + lh * 4;
+  const uint8_t* scale_a = &scale_ring[0][0] + (wm * FM * 32 + li) * 16;
+  const uint8_t* scale_b = &scale_ring[0][0] + (Tile::kRowsA + wn * FN * 32 + li) * 16;
   auto read = [&](const uint8_t* row, int t) {
-    return *reinterpret_cast<const u32x4*>(row + ((4 * lh + t) ^ ((li >> 1) & 7)) * kBlock);
+    return *reinterpret_cast<const u32x4*>(row + ((2 * t + lh) ^ ((li >> 1) & 7)) * kBlock);
   };
 
   open();
+  set_shift();
   for (int i = 0; i < S; ++i) {
     load_scales();
 #pragma unroll
     for (int j = 0; j < Tile::kLoads; ++j) load(i, j);
-    advance();
+    if (i < S - 1) {
+      advance();
+      next_item();
+    }
   }
   wait_vmcnt<(S - 1) * Tile::kLoads>();
   __syncthreads();
   u32x4 fa[2][FM], fb[2][FN];
   uint32_t sa[FM], sb[FN];
-  auto read_scales = [&](int pair, int stage, uint32_t(&a)[FM], uint32_t(&b)[FN]) {
+  u32x2 ra[FM], rb[FN];   // a stage's scales as read: eight a row, every second one this half's
+  auto read_scales = [&](int f, int pair, int stage) {
     const int at = pair * Tile::kScaleSlot + (stage & 1) * 8;
+    if (f < FN) rb[f] = *reinterpret_cast<const u32x2*>(scale_b + at + f * 32 * 16);
+    else ra[f - FN] = *reinterpret_cast<const u32x2*>(scale_a + at + (f - FN) * 32 * 16);
+  };
+  auto pick_scales = [&]() {
+    const uint32_t half = 0x06040200u + 0x01010101u * lh;
 #pragma unroll
-    for (int i = 0; i < FM; ++i) a[i] = *reinterpret_cast<const uint32_t*>(scale_a + at + i * 32 * 16);
+    for (int i = 0; i < FM; ++i) sa[i] = __builtin_amdgcn_perm(ra[i][1], ra[i][0], half);
 #pragma unroll
-    for (int j = 0; j < FN; ++j) b[j] = *reinterpret_cast<const uint32_t*>(scale_b + at + j * 32 * 16);
+    for (int j = 0; j < FN; ++j) sb[j] = __builtin_amdgcn_perm(rb[j][1], rb[j][0], half);
   };
 
   f32x16 acc[FM][FN];
   // The MFMAs of step T on its fragments, with the reads of the next step's
   // (`ahead` is its slot) and, in the last step, the loads into `slot`. W is
   // the first operand: a lane then holds four neighbouring columns of C's row.
-  auto step = [&](auto T, int slot, int ahead) {
+  auto step = [&](auto T, int slot, int ahead, int pair, int stage) {
     constexpr int t = decltype(T)::value;
     u32x4(&a)[FM] = fa[t & 1];
     u32x4(&b)[FN] = fb[t & 1];
@@ -520,14 +546,20 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_mx_tile_kernel(MxGe
       const int i = at / FN, j = at % FN;
       acc[i][j] = mx_mma<t>(b[j], a[i], acc[i][j], sb[j], sa[i]);
 #pragma unroll
-      for (int f = at * kReads / kBlocks; f < (at + 1) * kReads / kBlocks; ++f) {
-        if (f < FM) na[f] = read(next_a + f * 32 * kTileStage, (t + 1) & 3);
-        else nb[f - FM] = read(next_b + (f - FM) * 32 * kTileStage, (t + 1) & 3);
+      for (int f = at * 3; f < (at + 1) * 3 && f < kReads; ++f) {
+        if (f < FN) nb[f] = read(next_b + f * 32 * kTileStage, (t + 1) & 3);
+        else na[f - FN] = read(next_a + (f - FN) * 32 * kTileStage, (t + 1) & 3);
       }
       if constexpr (t == 3) {
 #pragma unroll
+        for (int f = (at - 2) * 3; f < (at - 1) * 3; ++f)
+          if (f >= 0 && f < kReads) read_scales(f, pair, stage);
+#pragma unroll
         for (int l = at * Tile::kLoads / kBlocks; l < (at + 1) * Tile::kLoads / kBlocks; ++l)
           load(slot, l);
+      }
+      if constexpr (t == 2) {
+        if (at == 3) advance();
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -536,17 +568,19 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_mx_tile_kernel(MxGe
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
-      for (int j = 0; j < FN; ++j) keep_sum(acc[i][j]);
+      for (int j = 0; j < FN; ++j) keep_sum<Tile::kWaves * PER_CU == 4>(acc[i][j]);
   };
 
+  constexpr int kStores = OUT == 2 ? 4 * FM * FN : 4 * FM;   // of a wave's whole part of C
+  bool behind = false;   // the last item's stores are, all of them, under way behind this stage's loads
   int slot = 0, pair = 0;
   for (int item = (int)blockIdx.x; item < items; item += (int)gridDim.x) {
     int tm, tn, split;
     tile_item(p, item, items, tm, tn, split);
     const int first = split * per, count = min(per, p.steps - first);
     // The last stage's scales inside K, of four blocks of this half.
-    const int inside = (p.bytes - (first + count - 1) * kTileStage) / kBlock - 4 * lh;
-    const uint32_t last_mask = inside >= 4 ? ~0u : inside <= 0 ? 0u : (1u << (8 * inside)) - 1;
+    const int inside = ((p.bytes - (first + count - 1) * kTileStage) / kBlock - lh + 1) >> 1;
+    const uint32_t last_mask = inside >= 4 ? ~0u : (1u << (8 * inside)) - 1;
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -561,33 +595,34 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_mx_tile_kernel(MxGe
 #pragma unroll
     for (int j = 0; j < FN; ++j)
       fb[0][j] = read(frag_b + slot * Tile::kStage + j * 32 * kTileStage, 0);
-    read_scales(pair, 0, sa, sb);
+#pragma unroll
+    for (int f = 0; f < FM + FN; ++f) read_scales(f, pair, 0);
     for (int ks = 0; ks < count; ++ks) {
       const int next = slot + 1 == S ? 0 : slot + 1;
-      const uint32_t mask = ks == count - 1 ? last_mask : ~0u;
+      pick_scales();
+      if (ks == count - 1) {
 #pragma unroll
-      for (int i = 0; i < FM; ++i) sa[i] &= mask;
+        for (int i = 0; i < FM; ++i) sa[i] &= last_mask;
 #pragma unroll
-      for (int j = 0; j < FN; ++j) sb[j] &= mask;
-      step(Step<0>{}, slot, slot);
-      step(Step<1>{}, slot, slot);
-      step(Step<2>{}, slot, slot);
-      wait_vmcnt<(S - 2) * Tile::kLoads>();
+        for (int j = 0; j < FN; ++j) sb[j] &= last_mask;
+      }
+      step(Step<0>{}, slot, slot, 0, 0);
+      step(Step<1>{}, slot, slot, 0, 0);
+      step(Step<2>{}, slot, slot, 0, 0);
+      keep_sums();
+      next_item();
+      if (behind)
+        wait_vmcnt<(S - 2) * Tile::kLoads + kStores>();
+      else
+        wait_vmcnt<(S - 2) * Tile::kLoads>();
+      behind = false;
       wait_lgkmcnt0();
       __syncthreads();
-      keep_sums();
       // Every second stage, and an item's last, ends its pair of scales.
       if ((ks & 1) == 1 || ks == count - 1) pair = pair + 1 == S ? 0 : pair + 1;
-      uint32_t na[FM], nb[FN];
-      read_scales(pair, ks + 1, na, nb);
       load_scales();
-      step(Step<3>{}, slot, next);   // after the last stage its reads are not used
+      step(Step<3>{}, slot, next, pair, ks + 1);   // after the last stage its reads are not used
       keep_sums();
-#pragma unroll
-      for (int i = 0; i < FM; ++i) sa[i] = na[i];
-#pragma unroll
-      for (int j = 0; j < FN; ++j) sb[j] = nb[j];
-      advance();
       slot = next;
     }
 
@@ -606,13 +641,14 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_mx_tile_kernel(MxGe
     const uint32_t row0 = (uint32_t)tm * Tile::kRowsA + wm * FM * 32;
     const int col0 = tn * Tile::kRowsB + wn * FN * 32;
     const int wrow = eli * 128, wswz = (eli >> 1) & 7;
+    behind = p.splits == 1 && row0 + FM * 32 <= (uint32_t)p.M && col0 + FN * 32 <= p.N;
     auto flush = [&](uint8_t* out, int64_t pitch, uint32_t row, int col, int per_chunk) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int r = 8 * k + (el >> 3), c = (el & 7) ^ ((r >> 1) & 7);
         const u32x4 v = *reinterpret_cast<const u32x4*>(mid + r * 128 + (el & 7) * 16);
         if (row + r < (uint32_t)p.M && col + c * per_chunk < p.N)
-          *reinterpret_cast<u32x4*>(out + (row + r) * pitch + (int64_t)col * (16 / per_chunk) + c * 16) = v;
+          __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(out + (row + r) * pitch + (int64_t)col * (16 / per_chunk) + c * 16));
       }
     };
     auto block32 = [&](int i, int j, uint8_t* out, int64_t pitch) {
@@ -662,6 +698,22 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_mx_tile_kernel(MxGe
   wait_vmcnt<0>();
 }
 
+// The scales of both operands as the tile kernel reads them fastest: the 16 bytes of
+// each row and pair of stages, all rows' of one pair side by side. In rows of their
+// own such 16 bytes cost the tile kernel a request for a cache line each, half as many
+// again as the codes'.
+__global__ void __launch_bounds__(256) mx_pack_scales_kernel(MxPackParams p) {
+  const int lane = (int)(threadIdx.x & 63), wave = (int)(threadIdx.x >> 6);
+  const bool of_a = (int)blockIdx.x < p.blocks_a;
+  const int rows = of_a ? p.rows_a : p.rows_w;
+  const int row = (of_a ? (int)blockIdx.x : (int)blockIdx.x - p.blocks_a) * 64 + lane;
+  if (row >= rows) return;
+  const uint8_t* src = of_a ? p.a + row * p.ld_a : p.w + row * p.ld_w;
+  u32x4* dst = reinterpret_cast<u32x4*>(of_a ? p.to_a : p.to_w) + row;
+  for (int q = (int)blockIdx.y * 16 + wave; q < p.pairs && q < ((int)blockIdx.y + 1) * 16; q += 4)
+    dst[(int64_t)q * rows] = *reinterpret_cast<const u32x4*>(src + q * 16);
+}
+
 // Sum of the splits' partial products in split order, rounded: four columns a
 // thread, four splits' loads together.
 template <int OUT>
@@ -686,40 +738,54 @@ enum MxKind { kVec, kRows, kTile128, kTile128Pair, kTile192, kTile256 };
 struct MxPlan {
   MxKind kind;
   int tiles_m, tiles_n, splits, steps;
-  bool wide;   // kRows: 64 columns
+  bool wide;     // kRows: 64 columns
+  bool packed;   // tile kernels: the scales are laid out anew
 };
 
 MxPlan mx_plan(int64_t M, int64_t N, int64_t bytes) {
-  MxPlan c{kVec, 0, 0, 1, 0, false};
+  MxPlan c{kVec, 0, 0, 1, 0, false, false};
   if (M <= 4) return c;
-  // The few-row kernel, also for more rows while its tiles of 64 x 32 all run at
-  // once and K is not long, and its tiles of 64 x 64 likewise.
+  // The few-row kernel, also for more rows, while its tiles all run at once: of 64 x
+  // 32 where K is not long, and of 64 x 64. 128 x 4096 x 4096 takes 7.4 us and in the
+  // large tiles 13.4, 256 x 4096 x 4096 9.4 and 13.4, 300 x 3000 x 2016 8.1 and 8.4;
+  // 128 x 8192 x 14336 26.1 and 24.6, and with more tiles than CUs 64 x 28672 x 8192
+  // 33.1 and 24.7, 16 x 28672 x 8192 25.0 and 23.6.
   const int64_t tall = (M + 63) / 64;
   const bool few32 = tall * ((N + 31) / 32) <= 256 && bytes <= 8192;
-  const bool few64 = tall * ((N + 63) / 64) <= 256 && bytes <= 4096;
-  if (M <= 64 || few32 || few64) {
+  const bool few64 = tall * ((N + 63) / 64) <= 256 && (M <= 64 || bytes <= 4096);
+  if (few32 || few64) {
     c.kind = kRows;
     c.tiles_m = ceil_div(M, 64);
     c.wide = M <= 64 ? N > 192 * 64 : !few32;
     c.tiles_n = ceil_div(N, c.wide ? 64 : 32);
     c.steps = ceil_div(bytes, kRowsStage);
     const int tiles = c.tiles_m * c.tiles_n;
-    const int most = tiles < 96 ? 192 / tiles : tiles <= 128 && c.steps >= 16 ? 2 : 1;
+    // K is split where that gives idle CUs enough stages to pay for the join: 16 x
+    // 4096 x 14336 takes 10.2 us in two parts and 11.4 whole, 40 x 2048 x 16384 10.2 in
+    // four and 12.1 in two; 32 x 4096 x 8192 8.9 in two and 8.8 whole, 8 x 4096 x 4096
+    // 6.5 and 5.2.
+    const int most = tiles < 96 ? 256 / tiles : tiles <= 128 && c.steps >= 14 ? 2 : 1;
     c.splits = c.steps >= 8 ? shares(c.steps, most, 2) : 1;
     return c;
   }
   // The tile kernels: of all tile shapes and splits of K, the least estimate of
-  // time. A workgroup takes so many us a stage with every CU at work. Partial
-  // products cost 2 us, and 8 bytes each at 8 TB/s.
+  // time. With every CU at work a workgroup takes so many us a stage, and so many
+  // more a tile (measured from K = 1024 to 8192): the larger tiles fetch less for each
+  // product, and their last round leaves more CUs idle. Two of 128 x 128 share a CU
+  // where there are more than 256 of them. Partial products cost 2 us, and 8 bytes
+  // each at 8 TB/s. 1500 x 8192 x 2048 takes 18.4 us in tiles of 256 x 256 (20.3 in
+  // pairs of 128 x 128), 2048 x 4096 x 4096 23.8 in those pairs (25.8 in 256 x 256),
+  // 1000 x 5000 x 4128 24.1 in 192 x 128 (25.4), 3000 x 1000 x 8192 23.5 in 128 x 128
+  // with a CU each (25.5).
   struct Shape {
     MxKind kind;
     int rows, cols, places, most;   // most: splits of K
-    float us;
+    float us, tile_us;
   };
-  static constexpr Shape kShapes[] = {{kTile256, 256, 256, 256, 1, 1.63f},
-                                      {kTile192, 192, 128, 256, 8, 0.70f},
-                                      {kTile128, 128, 128, 256, 16, 0.56f},
-                                      {kTile128Pair, 128, 128, 512, 16, 0.95f}};
+  static constexpr Shape kShapes[] = {{kTile256, 256, 256, 256, 1, 1.8f, 4.5f},
+                                      {kTile192, 192, 128, 256, 8, 1.0f, 2.f},
+                                      {kTile128, 128, 128, 256, 16, 0.62f, 2.5f},
+                                      {kTile128Pair, 128, 128, 512, 16, 1.16f, 2.f}};
   c.steps = ceil_div(bytes, kTileStage);
   float best = 0.f;
   for (const Shape& sh : kShapes) {
@@ -730,7 +796,9 @@ MxPlan mx_plan(int64_t M, int64_t N, int64_t bytes) {
       const int splits = shares(ceil_div(c.steps, 2), want, 2);
       if (splits != want) continue;
       const int64_t rounds = (tiles * splits + sh.places - 1) / sh.places;
-      float t = (float)rounds * (float)ceil_div(c.steps, splits) * sh.us;
+      const bool alone = sh.kind == kTile128Pair && tiles * splits <= 256;
+      float t = (float)rounds * ((float)ceil_div(c.steps, splits) * (alone ? 0.72f : sh.us) +
+                                 (alone ? 1.f : sh.tile_us));
       if (splits > 1) t += 2.f + (float)splits * (float)M * (float)N * 1e-6f;
       if (best == 0.f || t < best) {
         best = t;
@@ -738,6 +806,9 @@ MxPlan mx_plan(int64_t M, int64_t N, int64_t bytes) {
         c.tiles_m = tiles_m;
         c.tiles_n = tiles_n;
         c.splits = splits;
+        // Laying the scales out anew pays from some 64 stages a workgroup on: 8192^3 (128)
+        // takes 250 us without and 242 with it, 4096^3 (16) 37.5 and 39.4.
+        c.packed = sh.kind == kTile256 && rounds * c.steps >= 64;
       }
       if (tiles * splits >= sh.places) break;
     }
@@ -804,9 +875,14 @@ hipError_t launch_out(const MxGemmParams& p, MxKind kind, bool wide, hipStream_t
 
 }  // namespace
 
+// Bytes of an operand's packed scales.
+int64_t packed_bytes(int64_t rows, int64_t bytes) { return rows * ((bytes + 2 * kTileStage - 1) / (2 * kTileStage)) * 16; }
+
 int64_t gemm_mx_partials(int64_t M, int64_t N, int64_t K) {
   const MxPlan c = mx_plan(M, N, K / 2);
-  return c.splits > 1 ? (int64_t)c.splits * M * N : 0;
+  int64_t n = c.splits > 1 ? (int64_t)c.splits * M * N : 0;
+  if (c.packed) n += (packed_bytes(M, K / 2) + packed_bytes(N, K / 2)) / 4;
+  return n;
 }
 
 hipError_t launch_gemm_mx(MxGemmParams p, int out_type, hipStream_t stream) {
@@ -815,6 +891,30 @@ hipError_t launch_gemm_mx(MxGemmParams p, int out_type, hipStream_t stream) {
   p.tiles_n = c.tiles_n;
   p.splits = c.splits;
   p.steps = c.steps;
+  p.step_as = p.step_ws = 16;
+  if (c.packed) {
+    MxPackParams q{};
+    q.a = p.a_scales;
+    q.w = p.w_scales;
+    q.to_a = reinterpret_cast<uint8_t*>(p.partials);
+    q.to_w = q.to_a + packed_bytes(p.M, p.bytes);
+    q.ld_a = p.ld_as;
+    q.ld_w = p.ld_ws;
+    q.rows_a = p.M;
+    q.rows_w = p.N;
+    q.blocks_a = ceil_div(p.M, 64);
+    q.pairs = ceil_div(p.bytes, 2 * kTileStage);
+    hipLaunchKernelGGL(mx_pack_scales_kernel, dim3(q.blocks_a + ceil_div(p.N, 64), ceil_div(q.pairs, 16)),
+                       dim3(256), 0, stream, q);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    p.a_scales = q.to_a;
+    p.w_scales = q.to_w;
+    p.ld_as = p.ld_ws = 16;
+    p.step_as = (int64_t)p.M * 16;
+    p.step_ws = (int64_t)p.N * 16;
+    p.partials = reinterpret_cast<float*>(q.to_w + packed_bytes(p.N, p.bytes));
+  }
   if (out_type == 0) return launch_out<0>(p, c.kind, c.wide, stream);
   if (out_type == 1) return launch_out<1>(p, c.kind, c.wide, stream);
   return launch_out<2>(p, c.kind, c.wide, stream);

@@ -21,6 +21,7 @@ struct MxGemmParams {
   void* C;
   float* partials;                      // [splits][M][N] where splits > 1
   int64_t lda, ldw, ld_as, ld_ws, ldc;  // bytes, but ldc: elements
+  int64_t step_as, step_ws;             // bytes between the scales of two pairs of stages
   int32_t M, N, bytes;                  // bytes of a row: K / 2
   int32_t tiles_m, tiles_n, splits, steps;  // K steps of a whole row
 };

@@ -209,7 +209,8 @@ SHAPES = [(1, 8, 32), (1, 4096, 4096), (2, 24, 96), (3, 520, 544), (4, 200, 512)
           (65, 136, 16416), (129, 520, 18464), (257, 264, 16416), (130, 8, 16448), (500, 504, 26432), (66, 4104, 352),
           (1000, 1000, 416), (600, 2056, 4128), (65, 4088, 16384), (128, 4096, 2080), (1000, 504, 3104), (4100, 40, 96),
           (200, 4096, 3104), (1500, 520, 1056), (1300, 2000, 4128), (2000, 4120, 800), (24, 512, 16416), (40, 1000, 9248),
-          (6, 4096, 9216), (4104, 4096, 992), (4096, 4096, 4128), (1021, 5000, 1056)]
+          (6, 4096, 9216), (4104, 4096, 992), (4096, 4096, 4128), (1021, 5000, 1056), (20, 20000, 544), (64, 16640, 1056),
+          (8190, 8200, 4192), (4096, 4096, 16416)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
