@@ -2,8 +2,9 @@
 // output, and its gradient.
 //
 // Forward: h = x + residual (rounded to 16 bits), m = mean(h), r = rsqrt(mean((h -
-// m)^2) + eps), y = (h - m) r w + b. A row is read once and stays in registers,
-// packed as the 16 bits that h is rounded to anyway. The mean's rounding matters
+// m)^2) + eps), y = (h - m) r w + b. A row is read once and stays in registers, as
+// fp32 values (the packed 16 bits, unpacked in every turn, made it bound by the
+// vector units). The mean's rounding matters
 // where it is much larger than the deviations, so the sums of the second turn
 // correct it: with m0 the rounded mean, d = h - m0 and e = mean(d),
 // mean((h - m)^2) = mean(d^2) - e^2 and y = (d - e) r w + b; d is exact or nearly
@@ -69,7 +70,10 @@ __device__ __forceinline__ u32x4* chunk(uint8_t* row, int c) {
 }
 
 // One row per TPR threads, WG / TPR rows a workgroup; a thread holds CH chunks of
-// 8 elements, chunk index t + TPR * i. OUT: 0 the type of x, 1 e4m3, 2 4-bit.
+// 8 elements, chunk index t + TPR * i. OUT: 0 the type of x, 1 e4m3, 2 4-bit. 8192 x
+// 8192 with residual takes 76 us with e4m3 output (6.2 TB/s), 73 with 4-bit and 81 with
+// 16-bit output (6.6 TB/s, what a copy reaches); 1021 x 5000 9.9, where a launch and one
+// trip to memory are a third; one row of 4096 2.9, the two alone.
 template <class T, int TPR, int WG, int CH, bool RES, int OUT>
 __global__ void __launch_bounds__(WG) layernorm_kernel(LayerNormParams p) {
   constexpr int kRows = WG / TPR, kRowWaves = TPR / 64;
@@ -80,53 +84,50 @@ __global__ void __launch_bounds__(WG) layernorm_kernel(LayerNormParams p) {
   const int64_t row = long_block() * kRows + threadIdx.x / TPR;
   const bool live = row < p.M;
   const int64_t at = live ? row : p.M - 1;
-  const u32x4* x = reinterpret_cast<const u32x4*>(p.x + at * p.ld_x);
-  const u32x4* res = reinterpret_cast<const u32x4*>(p.residual + at * p.ld_residual);
-  const u32x4* w = reinterpret_cast<const u32x4*>(p.weight);
-  const u32x4* b = reinterpret_cast<const u32x4*>(p.bias);
+  const uint8_t* x = p.x + at * p.ld_x;
+  const uint8_t* res = p.residual + at * p.ld_residual;
+  const auto inside = [&](int i) { return min(t + TPR * i, p.chunks - 1); };
+  // Threads past the row's end hold its last chunk, and leave it out of every sum.
   u32x4 v[CH], a[RES ? CH : 1], wt[CH], bs[CH];
 #pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    const int c = t + TPR * i;
-    v[i] = u32x4{0, 0, 0, 0};
-    if (c < p.chunks) v[i] = __builtin_nontemporal_load(x + c);
-  }
+  for (int i = 0; i < CH; ++i) v[i] = __builtin_nontemporal_load(chunk(x, inside(i)));
   if constexpr (RES) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int c = t + TPR * i;
-      a[i] = u32x4{0, 0, 0, 0};
-      if (c < p.chunks) a[i] = __builtin_nontemporal_load(res + c);
-    }
+    for (int i = 0; i < CH; ++i) a[i] = __builtin_nontemporal_load(chunk(res, inside(i)));
   }
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    const int c = t + TPR * i;
-    wt[i] = bs[i] = u32x4{0, 0, 0, 0};
-    if (c < p.chunks) wt[i] = w[c];
-    if (b != nullptr && c < p.chunks) bs[i] = b[c];
+    wt[i] = *chunk(p.weight, inside(i));
+    bs[i] = u32x4{0, 0, 0, 0};
+    if (p.bias != nullptr) bs[i] = *chunk(p.bias, inside(i));
   }
+  float f[CH][8];   // h, then its deviations, then y
   float sum[1] = {0.f};
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
+    if constexpr (RES) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if constexpr (RES)
+      for (int e = 0; e < 4; ++e)
         v[i][e] = Pair<T>::pack(Pair<T>::lo(v[i][e]) + Pair<T>::lo(a[i][e]),
                                 Pair<T>::hi(v[i][e]) + Pair<T>::hi(a[i][e]));
-      sum[0] += Pair<T>::lo(v[i][e]);
-      sum[0] += Pair<T>::hi(v[i][e]);
+    }
+    unpack<T>(v[i], f[i]);
+    if (t + TPR * i < p.chunks) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[0] += f[i][e];
     }
   }
   row_sums(sum, first_sums);
-  keep_packed(v);
+  // The weight and the bias are here by now: the compiler would else load them where
+  // they are used, behind the stores.
+  keep_packed(wt);
+  keep_packed(bs);
   if constexpr (RES) {
     if (live) {
-      u32x4* h = reinterpret_cast<u32x4*>(p.h + row * p.ld_h);
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         const int c = t + TPR * i;
-        if (c < p.chunks) h[c] = v[i];
+        if (c < p.chunks) *chunk(p.h + row * p.ld_h, c) = v[i];
       }
     }
   }
@@ -135,41 +136,35 @@ __global__ void __launch_bounds__(WG) layernorm_kernel(LayerNormParams p) {
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     if (t + TPR * i < p.chunks) {
-      float f[8];
-      unpack<T>(v[i], f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float d = f[e] - mean;
-        dev[0] += d;
-        dev[1] += d * d;
+        f[i][e] -= mean;
+        dev[0] += f[i][e];
+        dev[1] += f[i][e] * f[i][e];
       }
     }
   }
   row_sums(dev, second_sums);
-  keep_packed(v);
-  keep_packed(wt);
-  keep_packed(bs);
   const float off = dev[0] * p.inv_n;
   const float r = 1.0f / sqrtf(fmaxf(dev[1] * p.inv_n - off * off, 0.f) + p.eps);
   const float shift = -off * r;
-  const auto value = [&](int i, float(&y)[8]) {
-    float f[8], wf[8], bf[8];
-    unpack<T>(v[i], f);
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    float wf[8], bf[8];
     unpack<T>(wt[i], wf);
     unpack<T>(bs[i], bf);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = fmaf(fmaf(f[e] - mean, r, shift), wf[e], bf[e]);
-  };
-  if constexpr (OUT == 1) {
-    uint32_t top = 0;
+    for (int e = 0; e < 8; ++e) f[i][e] = fmaf(fmaf(f[i][e], r, shift), wf[e], bf[e]);
+    if constexpr (OUT == 1) {
+      if (t + TPR * i < p.chunks) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      float y[8];
-      value(i, y);
-      if (t + TPR * i < p.chunks)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = max(top, abs_bits(y[e]));
+        for (int e = 0; e < 8; ++e) top = max(top, abs_bits(f[i][e]));
+      }
     }
+  }
+  float scale = 0.f;
+  if constexpr (OUT == 1) {
     top = wave_max(top);
     if constexpr (kRowWaves > 1) {
       const int wave = threadIdx.x >> 6;
@@ -179,48 +174,39 @@ __global__ void __launch_bounds__(WG) layernorm_kernel(LayerNormParams p) {
 #pragma unroll
       for (int i = 0; i < kRowWaves; ++i) top = max(top, tops[first + i]);
     }
-    if (!live) return;
-    keep_packed(v);
     // A NaN or an infinity makes the row NaN.
     float m = __uint_as_float(top >= 0x7F800000u ? 0x7FC00000u : top);
     m = m < kAmaxMin ? kAmaxMin : m;
-    const float inv = kE4m3Max / m;
-    if (t == 0) reinterpret_cast<float*>(p.scales)[row] = m / kE4m3Max;
-    u32x2* y8 = reinterpret_cast<u32x2*>(p.y + row * p.ld_y);
+    scale = kE4m3Max / m;
+    if (live && t == 0) reinterpret_cast<float*>(p.scales)[row] = m / kE4m3Max;
+  }
+  if (!live) return;
+  uint8_t* out = p.y + row * p.ld_y;
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int c = t + TPR * i;
-      float y[8];
-      value(i, y);
+  for (int i = 0; i < CH; ++i) {
+    const int c = t + TPR * i;
+    float(&y)[8] = f[i];
+    if constexpr (OUT == 1) {
       u32x2 o;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        int q = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * e] * inv, y[4 * e + 1] * inv, 0, false);
-        o[e] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * e + 2] * inv, y[4 * e + 3] * inv, q, true);
+        int q = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * e] * scale, y[4 * e + 1] * scale, 0, false);
+        o[e] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * e + 2] * scale, y[4 * e + 3] * scale, q, true);
       }
-      if (c < p.chunks) y8[c] = o;
-    }
-  } else {
-    if (!live) return;
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int c = t + TPR * i;
-      float y[8];
-      value(i, y);
-      if constexpr (OUT == 2) {
-        // A block of 32 is that of four lanes, all inside the row or all past it.
-        const uint32_t exponent = mx_exponent(mx_top(y));
-        const uint32_t codes = mx_codes(y, mx_scale(exponent));
-        if (c < p.chunks) {
-          reinterpret_cast<uint32_t*>(p.y + row * p.ld_y)[c] = codes;
-          if ((t & 3) == 0) p.scales[row * p.ld_scales + (c >> 2)] = (uint8_t)exponent;
-        }
-      } else {
-        u32x4 o;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = Pair<T>::pack(y[2 * e], y[2 * e + 1]);
-        if (c < p.chunks) reinterpret_cast<u32x4*>(p.y + row * p.ld_y)[c] = o;
+      if (c < p.chunks) reinterpret_cast<u32x2*>(out)[c] = o;
+    } else if constexpr (OUT == 2) {
+      // A block of 32 is that of four lanes, all inside the row or all past it.
+      const uint32_t exponent = mx_exponent(mx_top(y));
+      const uint32_t codes = mx_codes(y, mx_scale(exponent));
+      if (c < p.chunks) {
+        reinterpret_cast<uint32_t*>(out)[c] = codes;
+        if ((t & 3) == 0) p.scales[row * p.ld_scales + (c >> 2)] = (uint8_t)exponent;
       }
+    } else {
+      u32x4 o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = Pair<T>::pack(y[2 * e], y[2 * e + 1]);
+      if (c < p.chunks) *chunk(out, c) = o;
     }
   }
 }
@@ -235,22 +221,31 @@ hipError_t launch_norm_shape(const LayerNormParams& p, int out, hipStream_t stre
   return hipGetLastError();
 }
 
-// Rows of up to 2048 elements: one wave each, no exchange between waves. Wider
-// rows: a workgroup each, of as many threads as leave each at most 4 chunks.
+// One or two chunks a thread where the workgroup's 1024 threads allow it: few values
+// in a thread leave many waves to a CU, and short rows to many threads. 500 x 2048 with
+// 4-bit output takes 3.8 us with 256 threads a row, 4.1 with 128 and 5.0 with 64 (16384
+// x 2048 43.6, 43.5, 45.3), 2000 x 16384 43.7 with 1024 and 52.2 with 512, 8192 x 8192 with
+// e4m3 output 76 with 512 and 84 with 256, 1021 x 5000 9.9 with 384 and 10.3 with 512.
 template <class T, bool RES>
 hipError_t launch_norm_type(const LayerNormParams& p, int out, hipStream_t stream) {
   if (p.chunks <= 64) return launch_norm_shape<T, 64, 256, 1, RES>(p, out, stream);
-  if (p.chunks <= 128) return launch_norm_shape<T, 64, 256, 2, RES>(p, out, stream);
-  if (p.chunks <= 256) return launch_norm_shape<T, 64, 256, 4, RES>(p, out, stream);
-  if (p.chunks <= 512) return launch_norm_shape<T, 256, 256, 2, RES>(p, out, stream);
+  if (p.chunks <= 128) return launch_norm_shape<T, 128, 256, 1, RES>(p, out, stream);
+  if (p.chunks <= 256) return launch_norm_shape<T, 256, 256, 1, RES>(p, out, stream);
+  if (p.chunks <= 512) return launch_norm_shape<T, 512, 512, 1, RES>(p, out, stream);
+  if (p.chunks <= 768) return launch_norm_shape<T, 384, 384, 2, RES>(p, out, stream);
   if (p.chunks <= 1024) return launch_norm_shape<T, 512, 512, 2, RES>(p, out, stream);
-  if (p.chunks <= 2048) return launch_norm_shape<T, 512, 512, 4, RES>(p, out, stream);
+  if (p.chunks <= 2048) return launch_norm_shape<T, 1024, 1024, 2, RES>(p, out, stream);
   return launch_norm_shape<T, 1024, 1024, 4, RES>(p, out, stream);
 }
 
 // ---------------------------------------------------------------------------
-// Gradient. A workgroup that fills its CU's registers (1024 threads of 128, or 512
-// of 256 for rows wider than 16384) keeps the columns' sums of dy in LDS, each
+// Gradient. 8192 x 8192 with the residual stream's gradient takes 95 us and 4.5 for the
+// sum of the partials (5.4 TB/s in all; the values unpacked once instead of in every
+// turn, and no row's last chunk left to branches, took it from 105); 1021 x 2048 6.9 and
+// 2.5: launches, one trip to memory, two exchanges.
+//
+// A workgroup that fills its CU's registers (1024 threads of 128, or 512 of 256 for rows
+// wider than 16384) keeps the columns' sums of dy in LDS, each
 // thread its own, and reads dh where it is used; with eight chunks a thread a row's
 // loads go out only when the row ahead of it is done, and the weight's with them
 // and, from the caches, once more.
@@ -265,14 +260,12 @@ __global__ void __launch_bounds__(WG) layernorm_grad_kernel(LayerNormGradParams 
   const int t = threadIdx.x % TPR;
   const int sub = kRows == 1 ? 0 : threadIdx.x / TPR;
   u32x4 wt[CH];
-  const auto weight = [&](const uint8_t* from, int c) {
-    return c < p.chunks ? *chunk(from, c) : u32x4{0, 0, 0, 0};
-  };
+  // Threads past the row's end hold its last chunk, and leave it out of every sum.
+  const auto inside = [&](int i) { return min(t + TPR * i, p.chunks - 1); };
   float dw[CH][8], db[kFull ? 1 : CH][8];
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    const int c = t + TPR * i;
-    if constexpr (!kWide) wt[i] = weight(p.weight, c);
+    if constexpr (!kWide) wt[i] = *chunk(p.weight, inside(i));
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       dw[i][e] = 0.f;
@@ -285,7 +278,7 @@ __global__ void __launch_bounds__(WG) layernorm_grad_kernel(LayerNormGradParams 
   // they take the last one again: a branch around them would make the compiler
   // wait for them with the row in use.
   constexpr int kHeld = RES && !kFull ? CH : 1;
-  u32x4 h[CH], d[CH], s[kHeld], nh[CH], nd[CH], ns[kHeld];
+  u32x4 s[kHeld], nh[CH], nd[CH], ns[kHeld];
   const auto load = [&](int64_t row) {
     const int64_t at = row < p.M ? row : p.M - 1;
     const uint8_t* dy = p.dy + at * p.ld_dy;
@@ -293,21 +286,13 @@ __global__ void __launch_bounds__(WG) layernorm_grad_kernel(LayerNormGradParams 
     const uint8_t* dh = p.dh + at * p.ld_dh;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int c = t + TPR * i;
-      if constexpr (kWide) wt[i] = weight(p.weight, c);
-      nh[i] = nd[i] = u32x4{0, 0, 0, 0};
-      if (c < p.chunks) {
-        nh[i] = __builtin_nontemporal_load(chunk(x, c));
-        nd[i] = __builtin_nontemporal_load(chunk(dy, c));
-      }
+      if constexpr (kWide) wt[i] = *chunk(p.weight, inside(i));
+      nh[i] = __builtin_nontemporal_load(chunk(x, inside(i)));
+      nd[i] = __builtin_nontemporal_load(chunk(dy, inside(i)));
     }
     if constexpr (RES && !kFull) {
 #pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        const int c = t + TPR * i;
-        ns[i] = u32x4{0, 0, 0, 0};
-        if (c < p.chunks) ns[i] = __builtin_nontemporal_load(chunk(dh, c));
-      }
+      for (int i = 0; i < CH; ++i) ns[i] = __builtin_nontemporal_load(chunk(dh, inside(i)));
     }
   };
   const int64_t step = (int64_t)gridDim.x * kRows;
@@ -315,30 +300,49 @@ __global__ void __launch_bounds__(WG) layernorm_grad_kernel(LayerNormGradParams 
   for (int64_t base = (int64_t)blockIdx.x * kRows; base < p.M; base += step) {
     const int64_t row = base + sub;
     if constexpr (kWide) load(row);
+    // The values in fp32, once; with eight chunks a thread, unpacked in every turn.
+    float fv[kWide ? 1 : CH][8], gv[kWide ? 1 : CH][8];
+    const auto values = [&](int i, float(&f)[8], float(&g)[8], float(&wf)[8]) {
+      if constexpr (kWide) {
+        unpack<T>(nh[i], f);
+        unpack<T>(nd[i], g);
+      } else {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      h[i] = nh[i];
-      d[i] = nd[i];
-      if constexpr (RES && !kFull) s[i] = ns[i];
+        for (int e = 0; e < 8; ++e) {
+          f[e] = fv[i][e];
+          g[e] = gv[i][e];
+        }
+      }
+      unpack<T>(wt[i], wf);
+    };
+    if constexpr (!kWide) {
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        unpack<T>(nh[i], fv[i]);
+        unpack<T>(nd[i], gv[i]);
+        if constexpr (RES && !kFull) s[i] = ns[i];
+      }
+      load(row + step);
     }
-    if constexpr (!kWide) load(row + step);
     float one[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       float f[8], g[8], wf[8];
-      unpack<T>(h[i], f);
-      unpack<T>(d[i], g);
-      unpack<T>(wt[i], wf);
+      values(i, f, g, wf);
+      if (t + TPR * i < p.chunks) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        one[0] += f[e];
-        one[1] += g[e] * wf[e];
+        for (int e = 0; e < 8; ++e) {
+          one[0] += f[e];
+          one[1] += g[e] * wf[e];
+        }
       }
       if constexpr (kFull) __builtin_amdgcn_sched_barrier(0);   // one chunk's values at a time
     }
     row_sums(one, first_sums);
-    keep_packed(h);
-    keep_packed(d);
+    if constexpr (kWide) {
+      keep_packed(nh);
+      keep_packed(nd);
+    }
     keep_packed(wt);
     const float mean = one[0] * p.inv_n;
     float two[3] = {0.f, 0.f, 0.f};
@@ -346,12 +350,11 @@ __global__ void __launch_bounds__(WG) layernorm_grad_kernel(LayerNormGradParams 
     for (int i = 0; i < CH; ++i) {
       if (t + TPR * i < p.chunks) {
         float f[8], g[8], wf[8];
-        unpack<T>(h[i], f);
-        unpack<T>(d[i], g);
-        unpack<T>(wt[i], wf);
+        values(i, f, g, wf);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float v = f[e] - mean;
+          if constexpr (!kWide) fv[i][e] = v;
           two[0] += v;
           two[1] += v * v;
           two[2] += g[e] * wf[e] * v;
@@ -360,8 +363,10 @@ __global__ void __launch_bounds__(WG) layernorm_grad_kernel(LayerNormGradParams 
       if constexpr (kFull) __builtin_amdgcn_sched_barrier(0);   // one chunk's values at a time
     }
     row_sums(two, second_sums);
-    keep_packed(h);
-    keep_packed(d);
+    if constexpr (kWide) {
+      keep_packed(nh);
+      keep_packed(nd);
+    }
     keep_packed(wt);
     if (row < p.M) {
       const float off = two[0] * p.inv_n;
@@ -369,6 +374,7 @@ __global__ void __launch_bounds__(WG) layernorm_grad_kernel(LayerNormGradParams 
       const float shift = -off * r;
       const float mean_g = one[1] * p.inv_n;
       const float along = (two[2] * p.inv_n - off * mean_g) * r;
+      const float less = mean_g * r, tilt = along * r;
       // The address and the place made anew for the compiler, which would else keep
       // the values.
       const uint8_t* from = p.weight;
@@ -382,14 +388,12 @@ __global__ void __launch_bounds__(WG) layernorm_grad_kernel(LayerNormGradParams 
       for (int i = 0; i < CH; ++i) {
         const int c = place + TPR * i;
         float f[8], g[8], wf[8], o[8];
-        unpack<T>(h[i], f);
-        unpack<T>(d[i], g);
-        if constexpr (kWide) wt[i] = weight(from, c);
-        unpack<T>(wt[i], wf);
+        if constexpr (kWide) wt[i] = *chunk(from, min(c, p.chunks - 1));
+        values(i, f, g, wf);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float u = fmaf(f[e] - mean, r, shift);
-          o[e] = r * (g[e] * wf[e] - mean_g - u * along);
+          const float u = fmaf(kWide ? f[e] - mean : f[e], r, shift);
+          o[e] = fmaf(g[e] * wf[e], r, -less) - u * tilt;
           dw[i][e] += g[e] * u;
           if constexpr (!kFull) db[i][e] += g[e];
         }
@@ -401,8 +405,7 @@ __global__ void __launch_bounds__(WG) layernorm_grad_kernel(LayerNormGradParams 
           float sf[8];
           u32x4 stream = {0, 0, 0, 0};
           if constexpr (!kFull) stream = s[i];
-          else if (c < p.chunks)
-            stream = __builtin_nontemporal_load(chunk(p.dh + row * p.ld_dh, c));
+          else stream = __builtin_nontemporal_load(chunk(p.dh + row * p.ld_dh, min(c, p.chunks - 1)));
           unpack<T>(stream, sf);
 #pragma unroll
           for (int e = 0; e < 8; ++e) o[e] += sf[e];
@@ -465,49 +468,55 @@ __global__ void __launch_bounds__(WG) layernorm_grad_kernel(LayerNormGradParams 
 }
 
 // dweight and dbias: the partials' sums, rows of 2 n floats of which the first n
-// are dweight's. A workgroup takes 32 columns (8 threads of four) and 32
-// interleaved sets of partials, each summed in order, then the 32 sums in order.
+// are dweight's. A workgroup takes 32 columns (8 lanes of four) and 32 interleaved
+// sets of partials, each summed in order; then the 8 sets of a wave, then the waves.
 __global__ void __launch_bounds__(256) layernorm_columns_kernel(const float* __restrict__ partials,
                                                                 float* __restrict__ dweight,
                                                                 float* __restrict__ dbias, int count,
                                                                 int n) {
-  __shared__ f32x4 part[32][8];
+  __shared__ f32x4 part[4][8];
   const int lane = threadIdx.x & 7, set = threadIdx.x >> 3;
   const int col = blockIdx.x * 32 + lane * 4;
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   if (col < 2 * n) {
     const float* src = partials + col;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = set; i < count; i += 32)
       acc += *reinterpret_cast<const f32x4*>(src + (int64_t)i * 2 * n);
   }
-  part[set][lane] = acc;
+#pragma unroll
+  for (int step = 8; step < 64; step *= 2)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] += __shfl_xor(acc[e], step, 64);
+  if ((set & 7) == 0) part[set >> 3][lane] = acc;
   __syncthreads();
   if (set == 0 && col < 2 * n) {
-    acc = part[0][lane];
-    for (int i = 1; i < 32; ++i) acc += part[i][lane];
+    acc = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
     *reinterpret_cast<f32x4*>(col < n ? dweight + col : dbias + (col - n)) = acc;
   }
 }
 
 struct GradShape {
-  bool tall;     // many rows: one row in flight a workgroup of 256 up to 8192 columns
+  bool tall;     // many rows: with up to four chunks a thread
   int64_t grid;
 };
 
-// Each workgroup writes a row of partials, so few rows want few workgroups with
-// several rows in flight each, of 1024 threads. The few take equal numbers of
-// turns, a multiple of 8 of them for the XCDs' sake. A lone workgroup writes
-// dweight and dbias itself.
+// Each workgroup writes its partials, so there is one a CU, with several rows in
+// flight: 4096 x 1024 takes 13.3 us with 256 workgroups of eight rows and 14.8 with 512
+// of four, 8192 x 4096 52.6 and 54.1; two a CU for rows of 4104 to 8192, of which
+// two in one workgroup have too few registers. Few rows have more threads each
+// instead. The few take equal numbers of turns, a multiple of 8 of
+// workgroups for the XCDs' sake. A lone workgroup writes dweight and dbias itself.
 GradShape grad_shape(int64_t M, int64_t chunks) {
   GradShape g;
-  g.tall = chunks <= 256 || M >= 4096;
-  const int rows = chunks <= 256 ? 4 : g.tall ? 1 : chunks <= 512 ? 4 : chunks <= 1024 ? 2 : 1;
+  g.tall = chunks <= 256 ? M >= 2048 : M >= 4096;
+  int rows = chunks <= 512 ? 4 : chunks <= 1024 ? 2 : 1;
+  if (g.tall) rows = chunks <= 256 ? 8 : chunks <= 512 ? 2 : 1;
   const int64_t need = (M + rows - 1) / rows;
-  const int64_t fill = g.tall && chunks <= 1024 ? 512 : 256;
+  const int64_t fill = g.tall && chunks > 512 && chunks <= 1024 ? 512 : 256;
   g.grid = need < fill ? need : fill;
-  if (!g.tall && need > fill) {
-    const int64_t turns = (need + fill - 1) / fill;
+  if (!g.tall && need > 256) {
+    const int64_t turns = (need + 255) / 256;
     g.grid = ((need + turns - 1) / turns + 7) / 8 * 8;
   }
   return g;
@@ -523,16 +532,22 @@ hipError_t launch_grad_shape(const LayerNormGradParams& p, int64_t grid, hipStre
 
 template <class T>
 hipError_t launch_grad_type(const LayerNormGradParams& p, const GradShape& g, hipStream_t stream) {
-  if (p.chunks <= 64) return launch_grad_shape<T, 64, 256, 1>(p, g.grid, stream);
-  if (p.chunks <= 128) return launch_grad_shape<T, 64, 256, 2>(p, g.grid, stream);
-  if (p.chunks <= 256) return launch_grad_shape<T, 64, 256, 4>(p, g.grid, stream);
+  if (p.chunks <= 64)
+    return g.tall ? launch_grad_shape<T, 64, 512, 1>(p, g.grid, stream)
+                  : launch_grad_shape<T, 64, 256, 1>(p, g.grid, stream);
+  if (p.chunks <= 128)
+    return g.tall ? launch_grad_shape<T, 64, 512, 2>(p, g.grid, stream)
+                  : launch_grad_shape<T, 128, 512, 1>(p, g.grid, stream);
+  if (p.chunks <= 256)
+    return g.tall ? launch_grad_shape<T, 64, 512, 4>(p, g.grid, stream)
+                  : launch_grad_shape<T, 128, 512, 2>(p, g.grid, stream);
   if (p.chunks <= 512)
-    return g.tall ? launch_grad_shape<T, 256, 256, 2>(p, g.grid, stream)
+    return g.tall ? launch_grad_shape<T, 256, 512, 2>(p, g.grid, stream)
                   : launch_grad_shape<T, 256, 1024, 2>(p, g.grid, stream);
   if (p.chunks <= 1024)
     return g.tall ? launch_grad_shape<T, 256, 256, 4>(p, g.grid, stream)
                   : launch_grad_shape<T, 512, 1024, 2>(p, g.grid, stream);
-  if (p.chunks <= 2048) return launch_grad_shape<T, 1024, 1024, 2>(p, g.grid, stream);
+  if (p.chunks <= 2048) return launch_grad_shape<T, 512, 512, 4>(p, g.grid, stream);
   return launch_grad_shape<T, 512, 512, 8>(p, g.grid, stream);
 }
 

@@ -126,7 +126,8 @@ def check_norm(x, w, b, res, out, eps=1e-5, **kw):
 
 
 @pytest.mark.parametrize("M,N", [(1, 8), (1, 32), (1, 4096), (3, 504), (3, 512), (5, 520), (4, 1024), (7, 1056), (2, 2048), (3, 2080),
-                                 (2, 4128), (1, 8192), (3, 8224), (1, 16384), (2, 16416), (2, 32768), (1021, 256), (600, 5024)])
+                                 (2, 4128), (1, 8192), (3, 8224), (1, 16384), (2, 16416), (2, 32768), (1021, 256), (600, 5024),
+                                 (5, 6144), (3, 6176), (2, 10016), (3, 20000), (9, 1536)])
 @pytest.mark.parametrize("dtype,out,residual,bias", [(BF, BF, True, True), (HF, HF, False, True), (BF, E4, True, False),
                                                      (HF, E4, False, True), (BF, BF, False, False), (BF, F4, True, True),
                                                      (HF, F4, False, False), (HF, HF, True, False)])
@@ -283,7 +284,8 @@ def check_grad(dy, x, w, dh, eps=1e-5):
 
 @pytest.mark.parametrize("M,N", [(1, 8), (1, 4096), (5, 512), (6, 1000), (5, 2048), (3, 4096), (4, 8200), (2, 16384), (3, 16400),
                                  (2, 32768), (2100, 264), (1500, 2056), (1021, 2048), (16, 512), (17, 512), (18, 4096), (9, 8192),
-                                 (700, 5000), (4100, 2056), (4099, 8192), (600, 16384), (300, 24008)])
+                                 (700, 5000), (4100, 2056), (4099, 8192), (600, 16384), (300, 24008),
+                                 (2047, 1000), (2049, 1000), (2050, 2048), (3001, 512), (2048, 504), (4097, 4104), (4096, 5000), (700, 1024)])
 @pytest.mark.parametrize("dtype,residual", [(BF, True), (HF, False), (HF, True), (BF, False)])
 def test_grad(M, N, dtype, residual):
     w = (1 + 0.1 * normal((N,), F32, 20)).to(dtype)
