@@ -375,8 +375,9 @@ struct MxTile {
   static constexpr int kLoadsA = kRowsA / 8 / kWaves, kLoadsB = kRowsB / 8 / kWaves;
   static constexpr int kLoads = kLoadsA + kLoadsB;   // blocks a wave and stage
   static constexpr int kStage = (kRowsA + kRowsB) * kTileStage;
-  static constexpr int kScaleLoads = ((kRowsA + kRowsB) / 64 + kWaves - 1) / kWaves;   // a wave and pair
-  static constexpr int kScaleSlot = kScaleLoads * kWaves * kBlockBytes;
+  static constexpr int kScaleBlocks = (kRowsA + kRowsB) / 64;                       // a pair
+  static constexpr int kScaleLoads = (kScaleBlocks + kWaves - 1) / kWaves;           // a wave and pair, at most
+  static constexpr int kScaleSlot = kScaleBlocks * kBlockBytes;
   static_assert(kRowsA % (16 * kWaves) == 0 && kRowsB % (16 * kWaves) == 0,
                 "a wave loads an even number of blocks of each operand");
   static_assert(kRowsA % 64 == 0 && kRowsB % 64 == 0, "a block of scales is one operand's");
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_mx_tile_kernel(MxGe
   const int li = lane & 31, lh = lane >> 5;
   const int wm = wave / WN, wn = wave % WN;
   const uint32_t base = uniform(lds_addr(&ring[0][0]));
-  const uint32_t scale_base = uniform(lds_addr(&scale_ring[0][0])) + wave * Tile::kScaleLoads * kBlockBytes;
+  const uint32_t scale_base = uniform(lds_addr(&scale_ring[0][0])) + wave * kBlockBytes;
   const int items = p.tiles_m * p.tiles_n * p.splits;  // < 2^31, checked by the host
   // A split's first stage is the first of a pair.
   const int per = p.splits == 1 ? p.steps : ((p.steps + p.splits - 1) / p.splits + 1) & ~1;
@@ -432,9 +433,7 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_mx_tile_kernel(MxGe
     gb = p.W + row_b * p.ldw + f_k;
 #pragma unroll
     for (int j = 0; j < Tile::kScaleLoads; ++j) {
-      // Blocks past the last rows, where the waves have more than there are, load
-      // rows of W that are not used.
-      const int r = (wave * Tile::kScaleLoads + j) * 64;
+      const int r = (j * Tile::kWaves + wave) * 64;
       const bool of_a = r < Tile::kRowsA;
       const int64_t pair = f_k / (2 * kTileStage);
       gs[j] = of_a ? p.a_scales + row_a * p.ld_as + pair * p.step_as
@@ -466,7 +465,7 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_mx_tile_kernel(MxGe
     f_pair = f_scales ? (f_pair + 1 == S ? 0 : f_pair + 1) : f_pair;
 #pragma unroll
     for (int j = 0; j < Tile::kScaleLoads; ++j)
-      gs[j] += !f_scales ? 0 : (wave * Tile::kScaleLoads + j) * 64 < Tile::kRowsA ? p.step_as : p.step_ws;
+      gs[j] += !f_scales ? 0 : (j * Tile::kWaves + wave) * 64 < Tile::kRowsA ? p.step_as : p.step_ws;
     set_shift();
   };
   auto next_item = [&]() {
@@ -488,7 +487,8 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_mx_tile_kernel(MxGe
     if (!f_scales) return;
 #pragma unroll
     for (int j = 0; j < Tile::kScaleLoads; ++j)
-      dma_block_at(gs[j], scale_off[j], scale_base + f_pair * Tile::kScaleSlot + j * kBlockBytes);
+      if ((j + 1) * Tile::kWaves <= Tile::kScaleBlocks || j * Tile::kWaves + wave < Tile::kScaleBlocks)
+        dma_block_at(gs[j], scale_off[j], scale_base + f_pair * Tile::kScaleSlot + j * Tile::kWaves * kBlockBytes);
   };
   // Row 32 i + li of a wave's rows: (r >> 1) & 7 is (li >> 1) & 7 for every i.
   const uint8_t* frag_a = &ring[0][0] + (wm * FM * 32 + li) * kTileStage;
@@ -637,17 +637,17 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_mx_tile_kernel(MxGe
     asm volatile("" : "+v"(el));
     const int eli = el & 15, ehalf = (el >> 4) & 1, elh = el >> 5;
     uint8_t* mid = &staging[wave][0];
-    // Unsigned: the last tile of 192 rows may end past 2^31.
+    // Unsigned: the last tiles may end past 2^31.
     const uint32_t row0 = (uint32_t)tm * Tile::kRowsA + wm * FM * 32;
-    const int col0 = tn * Tile::kRowsB + wn * FN * 32;
+    const uint32_t col0 = (uint32_t)tn * Tile::kRowsB + wn * FN * 32;
     const int wrow = eli * 128, wswz = (eli >> 1) & 7;
-    behind = p.splits == 1 && row0 + FM * 32 <= (uint32_t)p.M && col0 + FN * 32 <= p.N;
-    auto flush = [&](uint8_t* out, int64_t pitch, uint32_t row, int col, int per_chunk) {
+    behind = p.splits == 1 && row0 + FM * 32 <= (uint32_t)p.M && col0 + FN * 32 <= (uint32_t)p.N;
+    auto flush = [&](uint8_t* out, int64_t pitch, uint32_t row, uint32_t col, int per_chunk) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int r = 8 * k + (el >> 3), c = (el & 7) ^ ((r >> 1) & 7);
         const u32x4 v = *reinterpret_cast<const u32x4*>(mid + r * 128 + (el & 7) * 16);
-        if (row + r < (uint32_t)p.M && col + c * per_chunk < p.N)
+        if (row + r < (uint32_t)p.M && col + c * per_chunk < (uint32_t)p.N)
           __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(out + (row + r) * pitch + (int64_t)col * (16 / per_chunk) + c * 16));
       }
     };
@@ -808,7 +808,7 @@ MxPlan mx_plan(int64_t M, int64_t N, int64_t bytes) {
         c.splits = splits;
         // Laying the scales out anew pays from some 64 stages a workgroup on: 8192^3 (128)
         // takes 250 us without and 242 with it, 4096^3 (16) 37.5 and 39.4.
-        c.packed = sh.kind == kTile256 && rounds * c.steps >= 64;
+        c.packed = sh.kind == kTile256 && rounds * c.steps >= 64 && M + N < int64_t(1) << 29;
       }
       if (tiles * splits >= sh.places) break;
     }
