@@ -19,7 +19,7 @@
 // in fp32.
 //
 // Few rows: the call is bound by reading W once, from memory straight into registers
-// for up to four (gemv_mx_kernel), through an LDS ring for up to 64 and for more of
+// for one and two (gemv_mx_kernel), through an LDS ring for up to 64 and for more of
 // small layers (gemm_mx_rows_kernel). Many rows: gemm_mx_tile_kernel.
 #include "pipe_gemm_tiles.hpp"
 #include "pipe_mx.hpp"
@@ -54,12 +54,14 @@ __device__ __forceinline__ void keep_sum(f32x16 v) {
 }
 
 // ---------------------------------------------------------------------------
-// One to four rows of A. A lane keeps 32 k's of every row in registers, as fp16
+// One or two rows of A. A lane keeps 32 k's of every row in registers, as fp16
 // pairs (e2m1 values are fp16 values), and meets them with the same k's of kVecRows
 // rows of W, one 16-byte load each: a wave reads 1 KiB of a row at a time (LPR lanes
 // make up a row where K is shorter) and all loads of its rows are in flight
 // together. v_dot2 adds up two products at a time in fp32, exactly; a block's sum is
-// scaled by the sum of the two exponents.
+// scaled by the sum of the two exponents. One row of 28672 x 8192 takes 21.3 us from HBM
+// (5.9 TB/s), of 8192 x 8192 9.1 and of 4096 x 4096 5.3, of which a launch and one trip
+// to memory are 4.
 // ---------------------------------------------------------------------------
 constexpr int kVecRows = 8;
 constexpr int kVecWaves = 8;    // at most, each with slices of K of its own
@@ -162,14 +164,16 @@ __global__ void __launch_bounds__(64 * kVecWaves) gemv_mx_kernel(MxGemmParams p)
 }
 
 // ---------------------------------------------------------------------------
-// Five to 64 rows, and more of small layers: bound by reading W once, through few
+// Two to 64 rows, and more of small layers: bound by reading W once, through few
 // CUs' worth of tiles. A workgroup of 8 waves computes 32 FM rows of A times 32 WN
 // rows of W. Stages of 1024 k (512 bytes of a row, and 32 of its scales) pass through
 // an LDS ring: data rows of 512 bytes, 16-byte chunk c of row r at place c ^ (r & 15),
 // 2 rows a direct-to-LDS block; behind them the scales, rows of 32 bytes, 32 rows a
 // block, which the first waves load. Wave (wn, wk) takes 32 rows of W and part wk of
 // the stage's k's. The parts' sums meet in LDS at the end. With few tiles a long K is
-// split over workgroups too.
+// split over workgroups too. 24 x 8192 x 8192 takes 10.4 us from HBM (36 MB: launch, first
+// trip and tail are 5), 8 x 16384 x 16384 26 (5.5 TB/s); W's loads are non-temporal (cached
+// 10.6 and 30).
 // ---------------------------------------------------------------------------
 constexpr int kRowsStage = 512;                            // bytes of a row
 constexpr int kRowsScales = kRowsStage / kBlock;           // of its scales
@@ -744,7 +748,11 @@ struct MxPlan {
 
 MxPlan mx_plan(int64_t M, int64_t N, int64_t bytes) {
   MxPlan c{kVec, 0, 0, 1, 0, false, false};
-  if (M <= 4) return c;
+  // Turning codes into pairs makes the vector units the bound from two rows on: one row
+  // of 512 x 8192 takes 3.9 us there and 6.1 in the few-row kernel, of 28672 x 8192 21.3 and
+  // 24; two rows of 1024 x 16384 5.7 and 7.5, but of 4096 x 4096 5.8 and 5.2, of 14336 x 4096
+  // 9.5 and 8.2.
+  if (M == 1 || (M == 2 && 2 * bytes > N)) return c;
   // The few-row kernel, also for more rows, while its tiles all run at once: of 64 x
   // 32 where K is not long, and of 64 x 64. 128 x 4096 x 4096 takes 7.4 us and in the
   // large tiles 13.4, 256 x 4096 x 4096 9.4 and 13.4, 300 x 3000 x 2016 8.1 and 8.4;
@@ -839,9 +847,7 @@ hipError_t launch_out(const MxGemmParams& p, MxKind kind, bool wide, hipStream_t
   const int items = p.tiles_m * p.tiles_n * p.splits;
   switch (kind) {
     case kVec:
-      if (p.M == 1) return launch_vec_k<1, OUT>(p, stream);
-      if (p.M == 2) return launch_vec_k<2, OUT>(p, stream);
-      return launch_vec_k<4, OUT>(p, stream);
+      return p.M == 1 ? launch_vec_k<1, OUT>(p, stream) : launch_vec_k<2, OUT>(p, stream);
     case kRows: {
       void (*k)(MxGemmParams) =
           p.M <= 32 ? (wide ? gemm_mx_rows_kernel<1, 2, OUT> : gemm_mx_rows_kernel<1, 1, OUT>)

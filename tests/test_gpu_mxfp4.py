@@ -210,7 +210,7 @@ SHAPES = [(1, 8, 32), (1, 4096, 4096), (2, 24, 96), (3, 520, 544), (4, 200, 512)
           (1000, 1000, 416), (600, 2056, 4128), (65, 4088, 16384), (128, 4096, 2080), (1000, 504, 3104), (4100, 40, 96),
           (200, 4096, 3104), (1500, 520, 1056), (1300, 2000, 4128), (2000, 4120, 800), (24, 512, 16416), (40, 1000, 9248),
           (6, 4096, 9216), (4104, 4096, 992), (4096, 4096, 4128), (1021, 5000, 1056), (20, 20000, 544), (64, 16640, 1056),
-          (8190, 8200, 4192), (4096, 4096, 16416)]
+          (8190, 8200, 4192), (4096, 4096, 16416), (2, 512, 96), (2, 88, 4128), (3, 20000, 96), (2, 20008, 1056), (4, 8, 16384)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
