@@ -239,10 +239,10 @@ hipError_t launch_norm_type(const LayerNormParams& p, int out, hipStream_t strea
 }
 
 // ---------------------------------------------------------------------------
-// Gradient. 8192 x 8192 with the residual stream's gradient takes 95 us and 4.5 for the
-// sum of the partials (5.4 TB/s in all; the values unpacked once instead of in every
-// turn, and no row's last chunk left to branches, took it from 105); 1021 x 2048 6.9 and
-// 2.5: launches, one trip to memory, two exchanges.
+// Gradient. 8192 x 8192 with the residual stream's gradient takes 94 us, 4.5 of them for
+// the sum of the partials (5.7 TB/s; 105 with the values unpacked in every turn and 512
+// workgroups' partials); 1021 x 2048 6.9 and 2.5: launches, one trip to memory, two
+// exchanges.
 //
 // A workgroup that fills its CU's registers (1024 threads of 128, or 512 of 256 for rows
 // wider than 16384) keeps the columns' sums of dy in LDS, each
@@ -277,8 +277,11 @@ __global__ void __launch_bounds__(WG) layernorm_grad_kernel(LayerNormGradParams 
   // A row's loads go out before the row ahead of it is reduced. Past the last row
   // they take the last one again: a branch around them would make the compiler
   // wait for them with the row in use.
+  // dh's loads go out a row ahead too, or with four chunks for each of 512 threads, which
+  // have no registers for that, ahead of the row's sums.
+  constexpr bool kTop = WG == 512 && CH == 4;
   constexpr int kHeld = RES && !kFull ? CH : 1;
-  u32x4 s[kHeld], nh[CH], nd[CH], ns[kHeld];
+  u32x4 s[kHeld], nh[CH], nd[CH], ns[kTop ? 1 : kHeld];
   const auto load = [&](int64_t row) {
     const int64_t at = row < p.M ? row : p.M - 1;
     const uint8_t* dy = p.dy + at * p.ld_dy;
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(WG) layernorm_grad_kernel(LayerNormGradParams 
       nh[i] = __builtin_nontemporal_load(chunk(x, inside(i)));
       nd[i] = __builtin_nontemporal_load(chunk(dy, inside(i)));
     }
-    if constexpr (RES && !kFull) {
+    if constexpr (RES && !kFull && !kTop) {
 #pragma unroll
       for (int i = 0; i < CH; ++i) ns[i] = __builtin_nontemporal_load(chunk(dh, inside(i)));
     }
@@ -320,7 +323,12 @@ __global__ void __launch_bounds__(WG) layernorm_grad_kernel(LayerNormGradParams 
       for (int i = 0; i < CH; ++i) {
         unpack<T>(nh[i], fv[i]);
         unpack<T>(nd[i], gv[i]);
-        if constexpr (RES && !kFull) s[i] = ns[i];
+        if constexpr (RES && !kFull && !kTop) s[i] = ns[i];
+      }
+      if constexpr (RES && kTop) {
+        const uint8_t* dh = p.dh + (row < p.M ? row : p.M - 1) * p.ld_dh;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) s[i] = __builtin_nontemporal_load(chunk(dh, inside(i)));
       }
       load(row + step);
     }
@@ -503,18 +511,16 @@ struct GradShape {
 
 // Each workgroup writes its partials, so there is one a CU, with several rows in
 // flight: 4096 x 1024 takes 13.3 us with 256 workgroups of eight rows and 14.8 with 512
-// of four, 8192 x 4096 52.6 and 54.1; two a CU for rows of 4104 to 8192, of which
-// two in one workgroup have too few registers. Few rows have more threads each
-// instead. The few take equal numbers of turns, a multiple of 8 of
+// of four, 8192 x 4096 52.6 and 54.1, 8192 x 8192 99.4 with 256 of two rows and 106 with
+// 512 of one. Few rows have more threads each instead. The few take equal numbers of turns, a multiple of 8 of
 // workgroups for the XCDs' sake. A lone workgroup writes dweight and dbias itself.
 GradShape grad_shape(int64_t M, int64_t chunks) {
   GradShape g;
   g.tall = chunks <= 256 ? M >= 2048 : M >= 4096;
   int rows = chunks <= 512 ? 4 : chunks <= 1024 ? 2 : 1;
-  if (g.tall) rows = chunks <= 256 ? 8 : chunks <= 512 ? 2 : 1;
+  if (g.tall) rows = chunks <= 256 ? 8 : chunks <= 1024 ? 2 : 1;
   const int64_t need = (M + rows - 1) / rows;
-  const int64_t fill = g.tall && chunks > 512 && chunks <= 1024 ? 512 : 256;
-  g.grid = need < fill ? need : fill;
+  g.grid = need < 256 ? need : 256;
   if (!g.tall && need > 256) {
     const int64_t turns = (need + 255) / 256;
     g.grid = ((need + turns - 1) / turns + 7) / 8 * 8;
@@ -545,7 +551,7 @@ hipError_t launch_grad_type(const LayerNormGradParams& p, const GradShape& g, hi
     return g.tall ? launch_grad_shape<T, 256, 512, 2>(p, g.grid, stream)
                   : launch_grad_shape<T, 256, 1024, 2>(p, g.grid, stream);
   if (p.chunks <= 1024)
-    return g.tall ? launch_grad_shape<T, 256, 256, 4>(p, g.grid, stream)
+    return g.tall ? launch_grad_shape<T, 256, 512, 4>(p, g.grid, stream)
                   : launch_grad_shape<T, 512, 1024, 2>(p, g.grid, stream);
   if (p.chunks <= 2048) return launch_grad_shape<T, 512, 512, 4>(p, g.grid, stream);
   return launch_grad_shape<T, 512, 512, 8>(p, g.grid, stream);
