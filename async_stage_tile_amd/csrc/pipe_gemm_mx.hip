@@ -705,17 +705,32 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) gemm_mx_tile_kernel(MxGe
 // The scales of both operands as the tile kernel reads them fastest: the 16 bytes of
 // each row and pair of stages, all rows' of one pair side by side. In rows of their
 // own such 16 bytes cost the tile kernel a request for a cache line each, half as many
-// again as the codes'.
+// again as the codes'. A workgroup turns 64 rows of 16 pairs over in LDS, so that both
+// sides are whole lines.
 __global__ void __launch_bounds__(256) mx_pack_scales_kernel(MxPackParams p) {
-  const int lane = (int)(threadIdx.x & 63), wave = (int)(threadIdx.x >> 6);
+  __shared__ u32x4 part[16][64 + 1];
   const bool of_a = (int)blockIdx.x < p.blocks_a;
   const int rows = of_a ? p.rows_a : p.rows_w;
-  const int row = (of_a ? (int)blockIdx.x : (int)blockIdx.x - p.blocks_a) * 64 + lane;
-  if (row >= rows) return;
-  const uint8_t* src = of_a ? p.a + row * p.ld_a : p.w + row * p.ld_w;
-  u32x4* dst = reinterpret_cast<u32x4*>(of_a ? p.to_a : p.to_w) + row;
-  for (int q = (int)blockIdx.y * 16 + wave; q < p.pairs && q < ((int)blockIdx.y + 1) * 16; q += 4)
-    dst[(int64_t)q * rows] = *reinterpret_cast<const u32x4*>(src + q * 16);
+  const int row0 = (of_a ? (int)blockIdx.x : (int)blockIdx.x - p.blocks_a) * 64;
+  const int pair0 = (int)blockIdx.y * 16;
+  const uint8_t* src = of_a ? p.a : p.w;
+  const int64_t ld = of_a ? p.ld_a : p.ld_w;
+  const int pair = (int)(threadIdx.x & 15), first = (int)(threadIdx.x >> 4);
+  u32x4 v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = *reinterpret_cast<const u32x4*>(src + min(row0 + first + 16 * i, rows - 1) * ld +
+                                           min(pair0 + pair, p.pairs - 1) * 16);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) part[pair][first + 16 * i] = v[i];
+  __syncthreads();
+  const int lane = (int)(threadIdx.x & 63), wave = (int)(threadIdx.x >> 6);
+  u32x4* dst = reinterpret_cast<u32x4*>(of_a ? p.to_a : p.to_w) + row0 + lane;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int q = wave + 4 * i;
+    if (row0 + lane < rows && pair0 + q < p.pairs) dst[(int64_t)(pair0 + q) * rows] = part[q][lane];
+  }
 }
 
 // Sum of the splits' partial products in split order, rounded: four columns a
