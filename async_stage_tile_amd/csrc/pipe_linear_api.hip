@@ -73,8 +73,8 @@ pipe_status_t mx_convert(const void* wide, const void* codes, const void* scales
   if (s != PIPE_OK) return s;
   p->ld_codes = ld_codes;
   p->ld_scales = ld_scales;
-  p->row_chunks = (uint32_t)(K / 8);
-  p->chunks = M * (K / 8);
+  p->row_chunks = (uint32_t)(K / (type == PIPE_FP32 ? 4 : 8));
+  p->chunks = M * p->row_chunks;
   p->reciprocal = (uint32_t)((uint64_t(1) << 32) / p->row_chunks);
   return PIPE_OK;
 }

@@ -7,11 +7,13 @@
 
 namespace pipe {
 
+constexpr int kMxBlock = 32;   // neighbours that share a scale
+
 struct MxQuantParams {
   const uint8_t *x, *codes_in, *scales_in;
   uint8_t *codes, *scales, *out;
   int64_t ld_x, ld_codes, ld_scales, ld_out;  // bytes
-  int64_t chunks;       // 8-element chunks in all
+  int64_t chunks;       // chunks of 16 bytes of the 16- or 32-bit side in all
   uint32_t row_chunks;  // in a row
   uint32_t reciprocal;  // floor(2^32 / row_chunks)
 };
@@ -42,21 +44,29 @@ __device__ __forceinline__ uint32_t mx_exponent(uint32_t top) {
 __device__ __forceinline__ float mx_scale(uint32_t e) {
   return __uint_as_float(e == 0 ? 0x00400000u : e == 255 ? 0x7FC00000u : e << 23);
 }
-// Largest of the magnitudes' bits over a block: 8 elements each of four lanes.
-__device__ __forceinline__ uint32_t mx_top(const float (&f)[8]) {
+// Largest of the magnitudes' bits over a block: 8 elements each of four lanes, or 4
+// of eight.
+template <int COUNT>
+__device__ __forceinline__ uint32_t mx_top(const float (&f)[COUNT]) {
   uint32_t top = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) top = max(top, abs_bits(f[e]));
+  for (int e = 0; e < COUNT; ++e) top = max(top, abs_bits(f[e]));
   top = dpp_max<0xB1, 0xF>(top);   // quad permutations [1,0,3,2] and [2,3,0,1]
-  return dpp_max<0x4E, 0xF>(top);
+  top = dpp_max<0x4E, 0xF>(top);
+  if constexpr (COUNT == 4) top = dpp_max<0x141, 0xF>(top);   // lane 7 - i of each eight
+  return top;
 }
-// Eight values divided by the scale and rounded to codes, to nearest, ties to the
-// even code; what passes 6 becomes 6.
-__device__ __forceinline__ uint32_t mx_codes(const float (&f)[8], float scale) {
+// Values divided by the scale and rounded to codes, to nearest, ties to the even
+// code; what passes 6 becomes 6.
+template <int COUNT>
+__device__ __forceinline__ uint32_t mx_codes(const float (&f)[COUNT], float scale) {
   uint32_t w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, f[0], f[1], scale, 0);
   w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[2], f[3], scale, 1);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[4], f[5], scale, 2);
-  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[6], f[7], scale, 3);
+  if constexpr (COUNT == 8) {
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[4], f[5], scale, 2);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[6], f[7], scale, 3);
+  }
+  return w;
 }
 
 }  // namespace pipe
