@@ -17,6 +17,8 @@
 // order.
 //
 // Both are bound by memory: some 12 and 20 fp32 operations an element.
+#include <type_traits>
+
 #include "pipe_mx.hpp"
 
 namespace pipe {
@@ -69,12 +71,31 @@ __device__ __forceinline__ u32x4* chunk(uint8_t* row, int c) {
   return reinterpret_cast<u32x4*>(row + (uint32_t)c * 16u);
 }
 
+// Rows that stay in the last-level cache (KEPT) are loaded through L2 and written past
+// it, others the other way round. With a residual
+// 1021 x 5000 takes 7.9 us so and 11.1 the other way, 4096 x 4096 20.6 and 24.0, 2500 x
+// 8192 (164 MB) 28.7 both, 4000 x 8192 46.3 and 43.4, 8192 x 8192 92.5 and 85.8; the
+// gradient of 1021 x 2048 10.0 and 10.7, of 4096 x 1024 11.4 and 12.6, of 8192 x 8192
+// 102 and 96.
+constexpr int64_t kKeptBytes = 160 << 20;
+bool kept(int64_t M, int64_t chunks, int sides) { return M * chunks * 16 * sides <= kKeptBytes; }
+template <bool KEPT>
+__device__ __forceinline__ u32x4 load_chunk(const u32x4* from) {
+  if constexpr (KEPT) return *from;
+  else return __builtin_nontemporal_load(from);
+}
+template <bool KEPT, class V>
+__device__ __forceinline__ void store_chunk(V v, V* to) {
+  if constexpr (KEPT) __builtin_nontemporal_store(v, to);
+  else *to = v;
+}
+
 // One row per TPR threads, WG / TPR rows a workgroup; a thread holds CH chunks of
 // 8 elements, chunk index t + TPR * i. OUT: 0 the type of x, 1 e4m3, 2 4-bit. 8192 x
 // 8192 with residual takes 76 us with e4m3 output (6.2 TB/s), 73 with 4-bit and 81 with
 // 16-bit output (6.6 TB/s, what a copy reaches); 1021 x 5000 9.9, where a launch and one
 // trip to memory are a third; one row of 4096 2.9, the two alone.
-template <class T, int TPR, int WG, int CH, bool RES, int OUT>
+template <class T, int TPR, int WG, int CH, bool RES, bool KEPT, int OUT>
 __global__ void __launch_bounds__(WG) layernorm_kernel(LayerNormParams p) {
   constexpr int kRows = WG / TPR, kRowWaves = TPR / 64;
   __shared__ RowSums<TPR, WG, 1> first_sums;
@@ -90,10 +111,10 @@ __global__ void __launch_bounds__(WG) layernorm_kernel(LayerNormParams p) {
   // Threads past the row's end hold its last chunk, and leave it out of every sum.
   u32x4 v[CH], a[RES ? CH : 1], wt[CH], bs[CH];
 #pragma unroll
-  for (int i = 0; i < CH; ++i) v[i] = __builtin_nontemporal_load(chunk(x, inside(i)));
+  for (int i = 0; i < CH; ++i) v[i] = load_chunk<KEPT>(chunk(x, inside(i)));
   if constexpr (RES) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) a[i] = __builtin_nontemporal_load(chunk(res, inside(i)));
+    for (int i = 0; i < CH; ++i) a[i] = load_chunk<KEPT>(chunk(res, inside(i)));
   }
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
@@ -127,7 +148,7 @@ __global__ void __launch_bounds__(WG) layernorm_kernel(LayerNormParams p) {
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         const int c = t + TPR * i;
-        if (c < p.chunks) *chunk(p.h + row * p.ld_h, c) = v[i];
+        if (c < p.chunks) store_chunk<KEPT>(v[i], chunk(p.h + row * p.ld_h, c));
       }
     }
   }
@@ -193,30 +214,30 @@ __global__ void __launch_bounds__(WG) layernorm_kernel(LayerNormParams p) {
         int q = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * e] * scale, y[4 * e + 1] * scale, 0, false);
         o[e] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * e + 2] * scale, y[4 * e + 3] * scale, q, true);
       }
-      if (c < p.chunks) reinterpret_cast<u32x2*>(out)[c] = o;
+      if (c < p.chunks) store_chunk<KEPT>(o, reinterpret_cast<u32x2*>(out) + c);
     } else if constexpr (OUT == 2) {
       // A block of 32 is that of four lanes, all inside the row or all past it.
       const uint32_t exponent = mx_exponent(mx_top(y));
       const uint32_t codes = mx_codes(y, mx_scale(exponent));
       if (c < p.chunks) {
-        reinterpret_cast<uint32_t*>(out)[c] = codes;
+        store_chunk<KEPT>(codes, reinterpret_cast<uint32_t*>(out) + c);
         if ((t & 3) == 0) p.scales[row * p.ld_scales + (c >> 2)] = (uint8_t)exponent;
       }
     } else {
       u32x4 o;
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[e] = Pair<T>::pack(y[2 * e], y[2 * e + 1]);
-      if (c < p.chunks) *chunk(out, c) = o;
+      if (c < p.chunks) store_chunk<KEPT>(o, chunk(out, c));
     }
   }
 }
 
-template <class T, int TPR, int WG, int CH, bool RES>
+template <class T, int TPR, int WG, int CH, bool RES, bool KEPT>
 hipError_t launch_norm_shape(const LayerNormParams& p, int out, hipStream_t stream) {
   const int64_t wgs = (p.M + WG / TPR - 1) / (WG / TPR);
-  void (*k)(LayerNormParams) = out == 2   ? layernorm_kernel<T, TPR, WG, CH, RES, 2>
-                               : out == 1 ? layernorm_kernel<T, TPR, WG, CH, RES, 1>
-                                          : layernorm_kernel<T, TPR, WG, CH, RES, 0>;
+  void (*k)(LayerNormParams) = out == 2   ? layernorm_kernel<T, TPR, WG, CH, RES, KEPT, 2>
+                               : out == 1 ? layernorm_kernel<T, TPR, WG, CH, RES, KEPT, 1>
+                                          : layernorm_kernel<T, TPR, WG, CH, RES, KEPT, 0>;
   hipLaunchKernelGGL(k, long_grid(wgs), dim3(WG), 0, stream, p);
   return hipGetLastError();
 }
@@ -226,16 +247,16 @@ hipError_t launch_norm_shape(const LayerNormParams& p, int out, hipStream_t stre
 // 4-bit output takes 3.8 us with 256 threads a row, 4.1 with 128 and 5.0 with 64 (16384
 // x 2048 43.6, 43.5, 45.3), 2000 x 16384 43.7 with 1024 and 52.2 with 512, 8192 x 8192 with
 // e4m3 output 76 with 512 and 84 with 256, 1021 x 5000 9.9 with 384 and 10.3 with 512.
-template <class T, bool RES>
+template <class T, bool RES, bool KEPT>
 hipError_t launch_norm_type(const LayerNormParams& p, int out, hipStream_t stream) {
-  if (p.chunks <= 64) return launch_norm_shape<T, 64, 256, 1, RES>(p, out, stream);
-  if (p.chunks <= 128) return launch_norm_shape<T, 128, 256, 1, RES>(p, out, stream);
-  if (p.chunks <= 256) return launch_norm_shape<T, 256, 256, 1, RES>(p, out, stream);
-  if (p.chunks <= 512) return launch_norm_shape<T, 512, 512, 1, RES>(p, out, stream);
-  if (p.chunks <= 768) return launch_norm_shape<T, 384, 384, 2, RES>(p, out, stream);
-  if (p.chunks <= 1024) return launch_norm_shape<T, 512, 512, 2, RES>(p, out, stream);
-  if (p.chunks <= 2048) return launch_norm_shape<T, 1024, 1024, 2, RES>(p, out, stream);
-  return launch_norm_shape<T, 1024, 1024, 4, RES>(p, out, stream);
+  if (p.chunks <= 64) return launch_norm_shape<T, 64, 256, 1, RES, KEPT>(p, out, stream);
+  if (p.chunks <= 128) return launch_norm_shape<T, 128, 256, 1, RES, KEPT>(p, out, stream);
+  if (p.chunks <= 256) return launch_norm_shape<T, 256, 256, 1, RES, KEPT>(p, out, stream);
+  if (p.chunks <= 512) return launch_norm_shape<T, 512, 512, 1, RES, KEPT>(p, out, stream);
+  if (p.chunks <= 768) return launch_norm_shape<T, 384, 384, 2, RES, KEPT>(p, out, stream);
+  if (p.chunks <= 1024) return launch_norm_shape<T, 512, 512, 2, RES, KEPT>(p, out, stream);
+  if (p.chunks <= 2048) return launch_norm_shape<T, 1024, 1024, 2, RES, KEPT>(p, out, stream);
+  return launch_norm_shape<T, 1024, 1024, 4, RES, KEPT>(p, out, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -250,7 +271,7 @@ hipError_t launch_norm_type(const LayerNormParams& p, int out, hipStream_t strea
 // loads go out only when the row ahead of it is done, and the weight's with them
 // and, from the caches, once more.
 // ---------------------------------------------------------------------------
-template <class T, int TPR, int WG, int CH, bool RES>
+template <class T, int TPR, int WG, int CH, bool RES, bool KEPT>
 __global__ void __launch_bounds__(WG) layernorm_grad_kernel(LayerNormGradParams p) {
   constexpr int kRows = WG / TPR;
   constexpr bool kWide = CH == 8, kFull = WG == 1024 || kWide;
@@ -290,12 +311,12 @@ __global__ void __launch_bounds__(WG) layernorm_grad_kernel(LayerNormGradParams 
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       if constexpr (kWide) wt[i] = *chunk(p.weight, inside(i));
-      nh[i] = __builtin_nontemporal_load(chunk(x, inside(i)));
-      nd[i] = __builtin_nontemporal_load(chunk(dy, inside(i)));
+      nh[i] = load_chunk<KEPT>(chunk(x, inside(i)));
+      nd[i] = load_chunk<KEPT>(chunk(dy, inside(i)));
     }
     if constexpr (RES && !kFull && !kTop) {
 #pragma unroll
-      for (int i = 0; i < CH; ++i) ns[i] = __builtin_nontemporal_load(chunk(dh, inside(i)));
+      for (int i = 0; i < CH; ++i) ns[i] = load_chunk<KEPT>(chunk(dh, inside(i)));
     }
   };
   const int64_t step = (int64_t)gridDim.x * kRows;
@@ -328,7 +349,7 @@ __global__ void __launch_bounds__(WG) layernorm_grad_kernel(LayerNormGradParams 
       if constexpr (RES && kTop) {
         const uint8_t* dh = p.dh + (row < p.M ? row : p.M - 1) * p.ld_dh;
 #pragma unroll
-        for (int i = 0; i < CH; ++i) s[i] = __builtin_nontemporal_load(chunk(dh, inside(i)));
+        for (int i = 0; i < CH; ++i) s[i] = load_chunk<KEPT>(chunk(dh, inside(i)));
       }
       load(row + step);
     }
@@ -413,7 +434,7 @@ __global__ void __launch_bounds__(WG) layernorm_grad_kernel(LayerNormGradParams 
           float sf[8];
           u32x4 stream = {0, 0, 0, 0};
           if constexpr (!kFull) stream = s[i];
-          else stream = __builtin_nontemporal_load(chunk(p.dh + row * p.ld_dh, min(c, p.chunks - 1)));
+          else stream = load_chunk<KEPT>(chunk(p.dh + row * p.ld_dh, min(c, p.chunks - 1)));
           unpack<T>(stream, sf);
 #pragma unroll
           for (int e = 0; e < 8; ++e) o[e] += sf[e];
@@ -421,7 +442,7 @@ __global__ void __launch_bounds__(WG) layernorm_grad_kernel(LayerNormGradParams 
         u32x4 packed;
 #pragma unroll
         for (int e = 0; e < 4; ++e) packed[e] = Pair<T>::pack(o[2 * e], o[2 * e + 1]);
-        if (c < p.chunks) *chunk(dx, c) = packed;
+        if (c < p.chunks) store_chunk<KEPT>(packed, chunk(dx, c));
         if constexpr (kFull) __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -504,67 +525,80 @@ __global__ void __launch_bounds__(256) layernorm_columns_kernel(const float* __r
   }
 }
 
+// Each workgroup writes its partials, so there is at most one a CU, with several rows
+// in flight (8192 x 8192 takes 96 us with 256 workgroups of two rows and 106 with 512 of
+// one), which take equal numbers of turns, a multiple of 8 of them for the XCDs' sake.
+// Few wide rows have a workgroup each: 16 x 4096 takes 5.7 us so, 6.8 in workgroups of
+// two and 8.5 of four (100 x 4096 8.0 and 7.8), 16 x 8192 7.1 and 8.8. Some hundred of
+// 4096 go four at a time: 1021 x 4096 14.7 us and 15.2 two at a time (256 10.4 and 10.3,
+// 2048 20.7 and 19.1). Many narrow ones go eight at a time: 16384 x 2048 48.8 us and 50.4
+// two at a time (3000 x 2048 15.4 and 14.2), 16384 x 512 16.8 and 19.6 four at a time
+// (3000 x 512 9.4 and 8.1). A lone workgroup writes dweight and dbias itself.
 struct GradShape {
-  bool tall;     // many rows: with up to four chunks a thread
+  bool few, many;   // a workgroup for a row; more rows a workgroup than else
   int64_t grid;
 };
 
-// Each workgroup writes its partials, so there is one a CU, with several rows in
-// flight: 4096 x 1024 takes 13.3 us with 256 workgroups of eight rows and 14.8 with 512
-// of four, 8192 x 4096 52.6 and 54.1, 8192 x 8192 99.4 with 256 of two rows and 106 with
-// 512 of one. Few rows have more threads each instead. The few take equal numbers of turns, a multiple of 8 of
-// workgroups for the XCDs' sake. A lone workgroup writes dweight and dbias itself.
 GradShape grad_shape(int64_t M, int64_t chunks) {
-  GradShape g;
-  g.tall = chunks <= 256 ? M >= 2048 : M >= 4096;
-  int rows = chunks <= 512 ? 4 : chunks <= 1024 ? 2 : 1;
-  if (g.tall) rows = chunks <= 256 ? 8 : chunks <= 1024 ? 2 : 1;
-  const int64_t need = (M + rows - 1) / rows;
-  g.grid = need < 256 ? need : 256;
-  if (!g.tall && need > 256) {
-    const int64_t turns = (need + 255) / 256;
-    g.grid = ((need + turns - 1) / turns + 7) / 8 * 8;
+  GradShape g{false, false, 0};
+  int rows = 1;
+  if (chunks <= 64) {
+    g.many = M >= 4096;
+    rows = g.many ? 8 : 4;
+  } else if (chunks <= 128) {
+    rows = 4;
+  } else if (chunks <= 256) {
+    g.many = M >= 8192;
+    rows = g.many ? 8 : 2;
+  } else if (chunks <= 1024) {
+    g.few = M <= 64;
+    g.many = chunks <= 512 && M > 256 && M < 2048;
+    rows = g.few ? 1 : g.many ? 4 : 2;
   }
+  const int64_t need = (M + rows - 1) / rows;
+  const int64_t turns = (need + 255) / 256;
+  g.grid = need <= 256 ? need : ((need + turns - 1) / turns + 7) / 8 * 8;
   return g;
 }
 
-template <class T, int TPR, int WG, int CH>
+template <class T, int TPR, int WG, int CH, bool KEPT>
 hipError_t launch_grad_shape(const LayerNormGradParams& p, int64_t grid, hipStream_t stream) {
-  void (*k)(LayerNormGradParams) = p.dh != nullptr ? layernorm_grad_kernel<T, TPR, WG, CH, true>
-                                                   : layernorm_grad_kernel<T, TPR, WG, CH, false>;
+  void (*k)(LayerNormGradParams) = p.dh != nullptr ? layernorm_grad_kernel<T, TPR, WG, CH, true, KEPT>
+                                                   : layernorm_grad_kernel<T, TPR, WG, CH, false, KEPT>;
   hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(WG), 0, stream, p);
   return hipGetLastError();
 }
 
-template <class T>
+template <class T, bool KEPT>
 hipError_t launch_grad_type(const LayerNormGradParams& p, const GradShape& g, hipStream_t stream) {
   if (p.chunks <= 64)
-    return g.tall ? launch_grad_shape<T, 64, 512, 1>(p, g.grid, stream)
-                  : launch_grad_shape<T, 64, 256, 1>(p, g.grid, stream);
-  if (p.chunks <= 128)
-    return g.tall ? launch_grad_shape<T, 64, 512, 2>(p, g.grid, stream)
-                  : launch_grad_shape<T, 128, 512, 1>(p, g.grid, stream);
+    return g.many ? launch_grad_shape<T, 64, 512, 1, KEPT>(p, g.grid, stream)
+                  : launch_grad_shape<T, 64, 256, 1, KEPT>(p, g.grid, stream);
+  if (p.chunks <= 128) return launch_grad_shape<T, 128, 512, 1, KEPT>(p, g.grid, stream);
   if (p.chunks <= 256)
-    return g.tall ? launch_grad_shape<T, 64, 512, 4>(p, g.grid, stream)
-                  : launch_grad_shape<T, 128, 512, 2>(p, g.grid, stream);
+    return g.many ? launch_grad_shape<T, 64, 512, 4, KEPT>(p, g.grid, stream)
+                  : launch_grad_shape<T, 256, 512, 1, KEPT>(p, g.grid, stream);
   if (p.chunks <= 512)
-    return g.tall ? launch_grad_shape<T, 256, 512, 2>(p, g.grid, stream)
-                  : launch_grad_shape<T, 256, 1024, 2>(p, g.grid, stream);
+    return g.few    ? launch_grad_shape<T, 512, 512, 1, KEPT>(p, g.grid, stream)
+           : g.many ? launch_grad_shape<T, 256, 1024, 2, KEPT>(p, g.grid, stream)
+                    : launch_grad_shape<T, 256, 512, 2, KEPT>(p, g.grid, stream);
   if (p.chunks <= 1024)
-    return g.tall ? launch_grad_shape<T, 256, 512, 4>(p, g.grid, stream)
-                  : launch_grad_shape<T, 512, 1024, 2>(p, g.grid, stream);
-  if (p.chunks <= 2048) return launch_grad_shape<T, 512, 512, 4>(p, g.grid, stream);
-  return launch_grad_shape<T, 512, 512, 8>(p, g.grid, stream);
+    return g.few ? launch_grad_shape<T, 512, 512, 2, KEPT>(p, g.grid, stream)
+                 : launch_grad_shape<T, 256, 512, 4, KEPT>(p, g.grid, stream);
+  if (p.chunks <= 2048) return launch_grad_shape<T, 512, 512, 4, KEPT>(p, g.grid, stream);
+  return launch_grad_shape<T, 512, 512, 8, KEPT>(p, g.grid, stream);
 }
 
 }  // namespace
 
 hipError_t launch_layernorm(const LayerNormParams& p, int type, int out, hipStream_t stream) {
-  const bool res = p.residual != nullptr;
-  if (type == 0)
-    return res ? launch_norm_type<__bf16, true>(p, out, stream) : launch_norm_type<__bf16, false>(p, out, stream);
-  return res ? launch_norm_type<_Float16, true>(p, out, stream)
-             : launch_norm_type<_Float16, false>(p, out, stream);
+  const bool res = p.residual != nullptr, keep = kept(p.M, p.chunks, res ? 4 : 2);
+  const auto launch = [&](auto f16) {
+    using T = std::conditional_t<decltype(f16)::value, _Float16, __bf16>;
+    if (keep) return (res ? launch_norm_type<T, true, true> : launch_norm_type<T, false, true>)(p, out, stream);
+    return (res ? launch_norm_type<T, true, false> : launch_norm_type<T, false, false>)(p, out, stream);
+  };
+  return type == 0 ? launch(std::false_type{}) : launch(std::true_type{});
 }
 
 int64_t layernorm_grad_partials(int64_t M, int64_t N) {
@@ -580,8 +614,10 @@ hipError_t launch_layernorm_grad(LayerNormGradParams p, float* partials, float* 
     p.sum_weight = g.grid == 1 ? dweight : partials;
     p.sum_bias = g.grid == 1 ? dbias : partials + n;
     p.sum_stride = 2 * (int64_t)n;
-    const hipError_t e = type == 0 ? launch_grad_type<__bf16>(p, g, stream)
-                                   : launch_grad_type<_Float16>(p, g, stream);
+    const bool keep = kept(p.M, p.chunks, p.dh != nullptr ? 4 : 3);
+    const hipError_t e =
+        type == 0 ? (keep ? launch_grad_type<__bf16, true> : launch_grad_type<__bf16, false>)(p, g, stream)
+                  : (keep ? launch_grad_type<_Float16, true> : launch_grad_type<_Float16, false>)(p, g, stream);
     if (e != hipSuccess || g.grid == 1) return e;
   }
   hipLaunchKernelGGL(layernorm_columns_kernel, dim3((2 * n + 31) / 32), dim3(256), 0, stream, partials,
