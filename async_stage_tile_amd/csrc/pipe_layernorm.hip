@@ -71,29 +71,25 @@ __device__ __forceinline__ u32x4* chunk(uint8_t* row, int c) {
   return reinterpret_cast<u32x4*>(row + (uint32_t)c * 16u);
 }
 
-// Rows that stay in the last-level cache (KEPT) are loaded through L2 and written past
-// it, others the other way round. With a residual
-// 1021 x 5000 takes 7.9 us so and 11.1 the other way, 4096 x 4096 20.6 and 24.0, 2500 x
-// 8192 (164 MB) 28.7 both, 4000 x 8192 46.3 and 43.4, 8192 x 8192 92.5 and 85.8; the
-// gradient of 1021 x 2048 10.0 and 10.7, of 4096 x 1024 11.4 and 12.6, of 8192 x 8192
-// 102 and 96.
-constexpr int64_t kKeptBytes = 160 << 20;
+// Rows that stay in the last-level cache (KEPT) are loaded through L2, others past it.
+// With a residual 1021 x 5000 takes 8.6 us so and 11.1 past it, in a chain where each
+// call reads the one before's y and h 8.7 and 9.7; 4096 x 4096 (134 MB) 21.8 and 22.2
+// there, 2500 x 8192 (164 MB) 31.9 and 24.9, 8192 x 8192 95 and 82. The next call reads
+// y and h: written past L2 the chain of 1021 x 5000 takes 10.5 us. The gradient's dx
+// meets its reader later: of rows that stay it is written past L2 (1021 x 2048 10.0 us
+// and 10.4, 4096 x 1024 11.4 and 12.5), of others not (8192 x 8192 96 us and 99).
+constexpr int64_t kKeptBytes = 128 << 20;
 bool kept(int64_t M, int64_t chunks, int sides) { return M * chunks * 16 * sides <= kKeptBytes; }
 template <bool KEPT>
 __device__ __forceinline__ u32x4 load_chunk(const u32x4* from) {
   if constexpr (KEPT) return *from;
   else return __builtin_nontemporal_load(from);
 }
-template <bool KEPT, class V>
-__device__ __forceinline__ void store_chunk(V v, V* to) {
-  if constexpr (KEPT) __builtin_nontemporal_store(v, to);
-  else *to = v;
-}
 
 // One row per TPR threads, WG / TPR rows a workgroup; a thread holds CH chunks of
 // 8 elements, chunk index t + TPR * i. OUT: 0 the type of x, 1 e4m3, 2 4-bit. 8192 x
 // 8192 with residual takes 76 us with e4m3 output (6.2 TB/s), 73 with 4-bit and 81 with
-// 16-bit output (6.6 TB/s, what a copy reaches); 1021 x 5000 9.9, where a launch and one
+// 16-bit output (6.6 TB/s, what a copy reaches); 1021 x 5000 8.6, where a launch and one
 // trip to memory are a third; one row of 4096 2.9, the two alone.
 template <class T, int TPR, int WG, int CH, bool RES, bool KEPT, int OUT>
 __global__ void __launch_bounds__(WG) layernorm_kernel(LayerNormParams p) {
@@ -148,7 +144,7 @@ __global__ void __launch_bounds__(WG) layernorm_kernel(LayerNormParams p) {
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         const int c = t + TPR * i;
-        if (c < p.chunks) store_chunk<KEPT>(v[i], chunk(p.h + row * p.ld_h, c));
+        if (c < p.chunks) *chunk(p.h + row * p.ld_h, c) = v[i];
       }
     }
   }
@@ -214,20 +210,20 @@ __global__ void __launch_bounds__(WG) layernorm_kernel(LayerNormParams p) {
         int q = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * e] * scale, y[4 * e + 1] * scale, 0, false);
         o[e] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * e + 2] * scale, y[4 * e + 3] * scale, q, true);
       }
-      if (c < p.chunks) store_chunk<KEPT>(o, reinterpret_cast<u32x2*>(out) + c);
+      if (c < p.chunks) reinterpret_cast<u32x2*>(out)[c] = o;
     } else if constexpr (OUT == 2) {
       // A block of 32 is that of four lanes, all inside the row or all past it.
       const uint32_t exponent = mx_exponent(mx_top(y));
       const uint32_t codes = mx_codes(y, mx_scale(exponent));
       if (c < p.chunks) {
-        store_chunk<KEPT>(codes, reinterpret_cast<uint32_t*>(out) + c);
+        reinterpret_cast<uint32_t*>(out)[c] = codes;
         if ((t & 3) == 0) p.scales[row * p.ld_scales + (c >> 2)] = (uint8_t)exponent;
       }
     } else {
       u32x4 o;
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[e] = Pair<T>::pack(y[2 * e], y[2 * e + 1]);
-      if (c < p.chunks) store_chunk<KEPT>(o, chunk(out, c));
+      if (c < p.chunks) *chunk(out, c) = o;
     }
   }
 }
@@ -260,10 +256,10 @@ hipError_t launch_norm_type(const LayerNormParams& p, int out, hipStream_t strea
 }
 
 // ---------------------------------------------------------------------------
-// Gradient. 8192 x 8192 with the residual stream's gradient takes 94 us, 4.5 of them for
-// the sum of the partials (5.7 TB/s; 105 with the values unpacked in every turn and 512
-// workgroups' partials); 1021 x 2048 6.9 and 2.5: launches, one trip to memory, two
-// exchanges.
+// Gradient. 8192 x 8192 with the residual stream's gradient takes 96 us, 4.5 of them for
+// the sum of the partials (5.6 TB/s; 105 with the values unpacked in every turn and 512
+// workgroups' partials); 1021 x 2048 9.8, 2.5 for the sum: launches, one trip to memory,
+// two exchanges.
 //
 // A workgroup that fills its CU's registers (1024 threads of 128, or 512 of 256 for rows
 // wider than 16384) keeps the columns' sums of dy in LDS, each
@@ -442,7 +438,10 @@ __global__ void __launch_bounds__(WG) layernorm_grad_kernel(LayerNormGradParams 
         u32x4 packed;
 #pragma unroll
         for (int e = 0; e < 4; ++e) packed[e] = Pair<T>::pack(o[2 * e], o[2 * e + 1]);
-        if (c < p.chunks) store_chunk<KEPT>(packed, chunk(dx, c));
+        if (c < p.chunks) {
+          if constexpr (KEPT) __builtin_nontemporal_store(packed, chunk(dx, c));
+          else *chunk(dx, c) = packed;
+        }
         if constexpr (kFull) __builtin_amdgcn_sched_barrier(0);
       }
     }

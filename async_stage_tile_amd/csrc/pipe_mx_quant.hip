@@ -6,12 +6,12 @@
 // of code and power of two is exact in fp32 and rounded once, to the output's
 // type. Both are bound by memory: a few operations for every byte moved.
 //
-// Into the form, 28672 x 8192 bf16 takes 95 us (6.2 TB/s) with four chunks a thread and
-// non-temporal loads and stores (99 with cached stores, 106 with cached loads, 105 and
-// 118 with two chunks and one); 28672 x 4096 fp32 93 us. On the way back, where most of
-// the bytes are written, 82 us (7.3 TB/s) with one chunk a thread, non-temporal stores
-// and cached loads (85 with four chunks, 100 with non-temporal loads, 105 with cached
-// stores); 28672 x 4096 fp32 73 us.
+// 28672 x 8192 bf16 there and back takes 173 to 185 us (6.4 TB/s or more): codes are
+// written and read through the caches, since what reads them comes next (212 with
+// non-temporal stores of them), wide rows past them (209 with cached stores on the way
+// back); 28672 x 4096 fp32 168 us (197 and 194). Into the form with four chunks a thread,
+// 99 us (100 with two, 104 with eight); back with one, 82 us over the same output again
+// (84 with two, 85 with four) and 114 over others.
 #include "pipe_mx.hpp"
 
 namespace pipe {
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kThreads) mx_quantize_kernel(MxQuantParams p) 
     const uint32_t exponent = mx_exponent(mx_top(f));
     const Codes codes = (Codes)mx_codes(f, mx_scale(exponent));
     if (first + threadIdx.x + kThreads * i < p.chunks) {
-      __builtin_nontemporal_store(codes, reinterpret_cast<Codes*>(p.codes + at[i].row * p.ld_codes) + at[i].col);
+      reinterpret_cast<Codes*>(p.codes + at[i].row * p.ld_codes)[at[i].col] = codes;
       if (threadIdx.x % kLanes == 0)
         p.scales[at[i].row * p.ld_scales + at[i].col / kLanes] = (uint8_t)exponent;
     }
