@@ -527,12 +527,14 @@ __global__ void __launch_bounds__(256) layernorm_columns_kernel(const float* __r
 // Each workgroup writes its partials, so there is at most one a CU, with several rows
 // in flight (8192 x 8192 takes 96 us with 256 workgroups of two rows and 106 with 512 of
 // one), which take equal numbers of turns, a multiple of 8 of them for the XCDs' sake.
-// Few wide rows have a workgroup each: 16 x 4096 takes 5.7 us so, 6.8 in workgroups of
-// two and 8.5 of four (100 x 4096 8.0 and 7.8), 16 x 8192 7.1 and 8.8. Some hundred of
-// 4096 go four at a time: 1021 x 4096 14.7 us and 15.2 two at a time (256 10.4 and 10.3,
-// 2048 20.7 and 19.1). Many narrow ones go eight at a time: 16384 x 2048 48.8 us and 50.4
-// two at a time (3000 x 2048 15.4 and 14.2), 16384 x 512 16.8 and 19.6 four at a time
-// (3000 x 512 9.4 and 8.1). A lone workgroup writes dweight and dbias itself.
+// Few wide rows have a workgroup each: 16 x 4096 takes 6.0 us so, 6.8 in workgroups of
+// two and 8.5 of four (256 x 4096 11.9 and 10.3), 16 x 8192 7.6 and 8.8. Some hundred of 4096 go four at a
+// time: 1021 x 4096 14.7 us and 15.2 two at a time (256 10.4 and 10.3, 2048 20.7 and
+// 19.1). Many short ones go eight at a time: 16384 x 512 16.8 us and 19.6 four at a time
+// (3000 x 512 9.4 and 8.1). The threads and chunks of a row depend on its width alone, so
+// that its dx does not depend on the other rows (64 threads of four chunks would take
+// 48.8 us for 16384 x 2048, 256 of one take 50.4). A lone workgroup writes dweight and
+// dbias itself.
 struct GradShape {
   bool few, many;   // a workgroup for a row; more rows a workgroup than else
   int64_t grid;
@@ -547,8 +549,7 @@ GradShape grad_shape(int64_t M, int64_t chunks) {
   } else if (chunks <= 128) {
     rows = 4;
   } else if (chunks <= 256) {
-    g.many = M >= 8192;
-    rows = g.many ? 8 : 2;
+    rows = 2;
   } else if (chunks <= 1024) {
     g.few = M <= 64;
     g.many = chunks <= 512 && M > 256 && M < 2048;
@@ -574,15 +575,13 @@ hipError_t launch_grad_type(const LayerNormGradParams& p, const GradShape& g, hi
     return g.many ? launch_grad_shape<T, 64, 512, 1, KEPT>(p, g.grid, stream)
                   : launch_grad_shape<T, 64, 256, 1, KEPT>(p, g.grid, stream);
   if (p.chunks <= 128) return launch_grad_shape<T, 128, 512, 1, KEPT>(p, g.grid, stream);
-  if (p.chunks <= 256)
-    return g.many ? launch_grad_shape<T, 64, 512, 4, KEPT>(p, g.grid, stream)
-                  : launch_grad_shape<T, 256, 512, 1, KEPT>(p, g.grid, stream);
+  if (p.chunks <= 256) return launch_grad_shape<T, 256, 512, 1, KEPT>(p, g.grid, stream);
   if (p.chunks <= 512)
-    return g.few    ? launch_grad_shape<T, 512, 512, 1, KEPT>(p, g.grid, stream)
+    return g.few    ? launch_grad_shape<T, 256, 256, 2, KEPT>(p, g.grid, stream)
            : g.many ? launch_grad_shape<T, 256, 1024, 2, KEPT>(p, g.grid, stream)
                     : launch_grad_shape<T, 256, 512, 2, KEPT>(p, g.grid, stream);
   if (p.chunks <= 1024)
-    return g.few ? launch_grad_shape<T, 512, 512, 2, KEPT>(p, g.grid, stream)
+    return g.few ? launch_grad_shape<T, 256, 256, 4, KEPT>(p, g.grid, stream)
                  : launch_grad_shape<T, 256, 512, 4, KEPT>(p, g.grid, stream);
   if (p.chunks <= 2048) return launch_grad_shape<T, 512, 512, 4, KEPT>(p, g.grid, stream);
   return launch_grad_shape<T, 512, 512, 8, KEPT>(p, g.grid, stream);

@@ -348,3 +348,22 @@ def test_grad_against_differences():
             quot = (loss(x.to(D) + t * e[0], w.to(D) + t * e[1], t * e[2]) -
                     loss(x.to(D) - t * e[0], w.to(D) - t * e[1], -t * e[2])) / (2 * t)
             assert abs(float(quot - grad)) <= float(bound) + 1e-5
+
+
+@pytest.mark.parametrize("residual", (True, False))
+@pytest.mark.parametrize("N", (512, 1024, 2048, 4096, 5000, 8192, 16384))
+def test_rows_do_not_depend_on_the_others(N, residual):
+    """A row's y, h and dx are the same bits however many rows the call has: threads and chunks go by the width."""
+    M = 9000 if N <= 4096 else 5000
+    x, dy, dh = (normal((M, N), BF, s) for s in (41, 42, 43))
+    w, b = normal((N,), BF, 44), normal((N,), BF, 45)
+    more = dh if residual else None
+    y, dx = pt.pipe_layernorm(x, w, b, residual=more), pt.pipe_layernorm_backward(dy, x, w, dh=more)[0]
+    for rows in (1, 40, 300, 1021, 2500):
+        few = None if more is None else more[:rows]
+        got = pt.pipe_layernorm(x[:rows], w, b, residual=few)
+        if residual:
+            assert torch.equal(got[0], y[0][:rows]) and torch.equal(got[1], y[1][:rows])
+        else:
+            assert torch.equal(got, y[:rows])
+        assert torch.equal(pt.pipe_layernorm_backward(dy[:rows], x[:rows], w, dh=few)[0], dx[:rows])
