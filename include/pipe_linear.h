@@ -181,7 +181,7 @@ pipe_status_t pipe_layernorm(const void* x, const void* residual, const void* we
                              pipe_dtype_t out_type, void* stream);
 
 /* Bytes of workspace pipe_layernorm_backward needs: fp32 partials of dweight and
- * dbias, none for a few rows. */
+ * dbias, none where one workgroup takes all rows. */
 pipe_status_t pipe_layernorm_backward_workspace_bytes(int64_t M, int64_t N, size_t* bytes);
 
 /* Gradient of y = u * weight + bias, u = (x - m) * r, r = rsqrt(mean((x - m)^2) +
@@ -191,7 +191,8 @@ pipe_status_t pipe_layernorm_backward_workspace_bytes(int64_t M, int64_t N, size
  *   dweight = sum over the rows of dy * u, dbias = sum over the rows of dy, fp32
  * dh (nullable) and overlaps as pipe_rmsnorm_backward's. M == 0 gives dweight =
  * dbias = 0; N == 0 is a no-op. Shapes, pitches and alignment as above; dweight,
- * dbias and workspace 16-byte aligned. One or two kernels are enqueued. */
+ * dbias and workspace 16-byte aligned. One or two kernels are enqueued. A row's dx
+ * does not depend on how many rows there are, nor do pipe_layernorm's y and h. */
 pipe_status_t pipe_layernorm_backward(const void* dy, const void* x, const void* weight,
                                       const void* dh, void* dx, float* dweight, float* dbias,
                                       int64_t M, int64_t N, int64_t ld_dy, int64_t ld_x,
