@@ -391,7 +391,8 @@ __global__ void __launch_bounds__(WG) layernorm_grad_kernel(LayerNormGradParams 
       keep_packed(nd);
     }
     keep_packed(wt);
-    const float mean = one[0] * p.inv_n;
+    float unit;
+    const float total = centre(one[0], p.inv_n, unit);
     float two[3] = {0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -400,9 +401,9 @@ __global__ void __launch_bounds__(WG) layernorm_grad_kernel(LayerNormGradParams 
         values(i, f, g, wf);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float v = f[e] - mean;
+          const float v = fmaf(-total, p.inv_n, f[e]);
           if constexpr (!kWide) fv[i][e] = v;
-          two[0] += v;
+          two[0] = fmaf(v, unit, two[0]);
           two[1] += v * v;
           two[2] += g[e] * wf[e] * v;
         }
@@ -416,8 +417,9 @@ __global__ void __launch_bounds__(WG) layernorm_grad_kernel(LayerNormGradParams 
     }
     keep_packed(wt);
     if (row < p.M) {
-      const float off = two[0] * p.inv_n;
-      const float r = 1.0f / sqrtf(fmaxf(two[1] * p.inv_n - off * off, 0.f) + p.eps);
+      float off = two[0] * p.inv_n;
+      float r = 1.0f / sqrtf(fmaxf(two[1] * p.inv_n - off * off, 0.f) + p.eps);
+      if (past_range(unit, two[0], two[1])) off = r = two[2] = 0.f;   // no gradient through u
       const float shift = -off * r;
       const float mean_g = one[1] * p.inv_n;
       const float along = (two[2] * p.inv_n - off * mean_g) * r;
@@ -439,7 +441,7 @@ __global__ void __launch_bounds__(WG) layernorm_grad_kernel(LayerNormGradParams 
         values(i, f, g, wf);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float u = fmaf(kWide ? f[e] - mean : f[e], r, shift);
+          const float u = fmaf(kWide ? fmaf(-total, p.inv_n, f[e]) : f[e], r, shift);
           o[e] = fmaf(g[e] * wf[e], r, -less) - u * tilt;
           dw[i][e] += g[e] * u;
           if constexpr (!kFull) db[i][e] += g[e];

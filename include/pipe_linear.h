@@ -194,7 +194,10 @@ pipe_status_t pipe_layernorm_backward_workspace_bytes(int64_t M, int64_t N, size
  * dh (nullable) and overlaps as pipe_rmsnorm_backward's. M == 0 gives dweight =
  * dbias = 0; N == 0 is a no-op. Shapes, pitches and alignment as above; dweight,
  * dbias and workspace 16-byte aligned. One or two kernels are enqueued. A row's dx
- * does not depend on how many rows there are, nor do pipe_layernorm's y and h. */
+ * does not depend on how many rows there are, nor do pipe_layernorm's y and h. A row
+ * of finite values whose squared deviations add up past fp32's range has u = 0 and
+ * dx = 0 (+ dh). dy * weight * (x - m) and its sum over a row are fp32 values: where
+ * one passes that range, the row's dx is not finite. */
 pipe_status_t pipe_layernorm_backward(const void* dy, const void* x, const void* weight,
                                       const void* dh, void* dx, float* dweight, float* dbias,
                                       int64_t M, int64_t N, int64_t ld_dy, int64_t ld_x,
