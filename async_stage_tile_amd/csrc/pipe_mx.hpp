@@ -21,7 +21,7 @@ struct MxQuantParams {
 struct MxGemmParams {
   const uint8_t *A, *W, *a_scales, *w_scales;
   void* C;
-  float* partials;                      // [splits][M][N] where splits > 1
+  float* partials;  // the workspace: scales laid out anew, if any, then [splits][M][N] where splits > 1
   int64_t lda, ldw, ld_as, ld_ws, ldc;  // bytes, but ldc: elements
   int64_t step_as, step_ws;             // bytes between the scales of two pairs of stages
   int32_t M, N, bytes;                  // bytes of a row: K / 2

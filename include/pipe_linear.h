@@ -205,7 +205,8 @@ pipe_status_t pipe_layernorm_backward(const void* dy, const void* x, const void*
                                       void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of workspace pipe_gemm_mxfp4 needs for a shape: fp32 partial products
- * where the K axis is split over workgroups, else 0. */
+ * where the K axis is split over workgroups, both operands' scales laid out anew
+ * for the largest products, else 0. */
 pipe_status_t pipe_gemm_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes);
 
 /* C[m][n] = sum_k A[m][k] * W[n][k], A (M x K) and W (N x K) in the form above
