@@ -242,7 +242,16 @@ PyObject* gemm_w4(PyObject* const* a) {
   return status != 0 ? nullptr : THPVariable_Wrap(C);
 }
 
-constexpr ScalarType kF4 = ScalarType::Float4_e2m1fn_x2, kE8 = ScalarType::Float8_e8m0fnu;
+// The 4-bit form's types; Undefined, which no tensor has, where torch lacks one.
+template <class T, class = void>
+struct Form {
+  static constexpr T kF4 = T::Undefined, kE8 = T::Undefined;
+};
+template <class T>
+struct Form<T, std::void_t<decltype(T::Float4_e2m1fn_x2), decltype(T::Float8_e8m0fnu)>> {
+  static constexpr T kF4 = T::Float4_e2m1fn_x2, kE8 = T::Float8_e8m0fnu;
+};
+constexpr ScalarType kF4 = Form<ScalarType>::kF4, kE8 = Form<ScalarType>::kE8;
 
 int code32(ScalarType t) { return t == ScalarType::Float ? 2 : code16(t); }
 
@@ -284,7 +293,7 @@ PyObject* layernorm(PyObject* const* a) {
   const ScalarType type = x->scalar_type(), out = dtype(a[5], type);
   const int code = code16(type);
   const bool q8 = out == ScalarType::Float8_e4m3fn, mx = out == kF4;
-  if (code < 0 || (!q8 && !mx && out != type)) return nullptr;
+  if (code < 0 || out == ScalarType::Undefined || (!q8 && !mx && out != type)) return nullptr;
   const int64_t M = x->size(0), N = x->size(1);
   if (mx && N % 32 != 0) return nullptr;
   const Tensor *w = tensor(a[1]), *b = nullptr, *res = nullptr;
@@ -350,7 +359,7 @@ PyObject* quantize(PyObject* const* a) {
   if (!begin(a[0], x, stream)) return nullptr;
   const int code = code32(x->scalar_type());
   const int64_t M = x->size(0), K = x->size(1);
-  if (code < 0 || K % 32 != 0) return nullptr;
+  if (kF4 == ScalarType::Undefined || code < 0 || K % 32 != 0) return nullptr;
   const Tensor c = make(*x, {M, K / 2}, kF4), s = make_scales(*x, M, K / 32);
   const int status = enqueue(entry.quantize, address(x), c.data_ptr(), s.data_ptr(), M, K, K, K / 2,
                              padded(K / 32), code, stream);

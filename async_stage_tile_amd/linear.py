@@ -53,6 +53,7 @@ _LINEAR_SIGS = {
     "pipe_gemm_mxfp4_workspace_bytes": [_L, _L, _L, _c.POINTER(_Z)],
     "pipe_gemm_mxfp4": [_V] * 5 + [_L] * 8 + [_I, _V, _Z, _V],
 }
+_FORM = ("float4_e2m1fn_x2", "float8_e8m0fnu")     # the 4-bit form's codes and scales in torch
 _FIRST = 7      # the C++ marshalling's bind() takes so many, bind_layer() the rest
 
 _fns = None
@@ -61,6 +62,7 @@ _torch = None
 _codes = {}         # torch dtype -> pipe_dtype_t
 _current_stream = None      # address of a device's current stream
 _fast = None                # the C++ marshalling, or None where it was not built
+_f4 = _e8 = None            # the 4-bit form's dtypes, None where torch lacks one of them
 
 
 def linear_symbols():
@@ -71,7 +73,7 @@ def linear_symbols():
 def _setup():
     """Loads the library once and binds the functions; torch is imported with
     the first call, as everywhere in this package."""
-    global _fns, _torch, _current_stream, _fast
+    global _fns, _torch, _current_stream, _fast, _f4, _e8
     with _lock:
         if _fns is None:
             L = _pt.lib()
@@ -87,8 +89,11 @@ def _setup():
                 setattr(fns, name, fn)
             import torch
             _codes.update({torch.bfloat16: PIPE_BF16, torch.float16: PIPE_FP16,
-                           torch.float32: PIPE_FP32, torch.float8_e4m3fn: PIPE_E4M3,
-                           torch.float4_e2m1fn_x2: PIPE_MXFP4})
+                           torch.float32: PIPE_FP32, torch.float8_e4m3fn: PIPE_E4M3})
+            form = [getattr(torch, name, None) for name in _FORM]
+            if None not in form:
+                _f4, _e8 = form
+                _codes[_f4] = PIPE_MXFP4
             # The address alone, without the Stream object around it (1 us a call).
             _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
                 lambda device: torch.cuda.current_stream(device).cuda_stream)
@@ -424,13 +429,13 @@ def _padded(n):
 
 def _make_scales(made, stream, like, rows, blocks):
     """e8m0 scales of rows that start at multiples of 16 bytes."""
-    return _make(made, stream, like, (rows, _padded(blocks)), _torch.float8_e8m0fnu)[:, :blocks]
+    return _make(made, stream, like, (rows, _padded(blocks)), _e8)[:, :blocks]
 
 
 def _scales(t, name, device, rows, blocks):
     """Pitch of a matrix of e8m0 scales. The kernels read its rows in groups of
     16 bytes, so the last row's group has to lie in the tensor's memory."""
-    pitch = _matrix(t, name, _torch.float8_e8m0fnu, device, (rows, blocks))[2]
+    pitch = _matrix(t, name, _e8, device, (rows, blocks))[2]
     if rows <= 1:
         pitch = _padded(blocks)
     if rows and t.storage_offset() + (rows - 1) * pitch + _padded(blocks) > t.untyped_storage().nbytes():
@@ -462,7 +467,7 @@ def pipe_layernorm(x, weight, bias=None, residual=None, eps=1e-5, out_dtype=None
     dev = x.get_device()
     M, N, ld_x = _matrix(x, "x", dtype, dev)
     out_dtype = out_dtype or (dtype if y is None else _tensor(y, "y").dtype)
-    q8, mx = out_dtype is _torch.float8_e4m3fn, out_dtype is _torch.float4_e2m1fn_x2
+    q8, mx = out_dtype is _torch.float8_e4m3fn, out_dtype is _f4
     if out_dtype is not dtype and not q8 and not mx:
         raise TypeError(f"out_dtype must be {dtype}, float8_e4m3fn or float4_e2m1fn_x2, not {out_dtype}")
     if mx and N % 32:

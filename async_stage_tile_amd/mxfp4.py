@@ -11,7 +11,8 @@ A matrix of M rows and K columns, K a multiple of 32, is held as
     scales  (M, K // 32) float8_e8m0fnu: the power of two that 32 neighbours of a
             row are multiplied by, as its exponent plus 127 (255: all 32 are NaN).
 
-Bytes that come from elsewhere take these types by ``.view(dtype)``. Rows of codes
+They need a PyTorch that has these types; the library's other operators do not.
+Bytes that come from elsewhere take them by ``.view(dtype)``. Rows of codes
 and of scales start at multiples of 16 bytes, and the memory of a row of scales
 reaches the next such multiple: the scales made here are views of wider rows where
 K // 32 is no multiple of 16.
@@ -28,7 +29,10 @@ from . import linear as _l
 
 
 def _setup():
-    return _l._fns or _l._setup()
+    fns = _l._fns or _l._setup()
+    if _l._f4 is None:
+        raise RuntimeError("the 4-bit form needs a PyTorch with " + " and ".join(f"torch.{n}" for n in _l._FORM))
+    return fns
 
 
 def _wide_dtype(dtype, name):
@@ -40,7 +44,7 @@ def _wide_dtype(dtype, name):
 
 def _form(codes, scales, names, device):
     """(rows, columns, pitch of codes, pitch of scales) of a matrix in the form."""
-    M, half, ld = _l._matrix(codes, names[0], _l._torch.float4_e2m1fn_x2, device)
+    M, half, ld = _l._matrix(codes, names[0], _l._f4, device)
     if half % 16:
         raise ValueError(f"{names[0]} hold {2 * half} values a row, no multiple of 32")
     return M, 2 * half, ld, _l._scales(scales, names[1], device, M, half // 16)
@@ -69,10 +73,10 @@ def pipe_quantize_mxfp4(x, codes=None, scales=None, stream=None):
         raise ValueError(f"rows of {K} columns have no 4-bit form: blocks are of 32")
     made = []
     if codes is None:
-        codes = _l._make(made, stream, x, (M, K // 2), _l._torch.float4_e2m1fn_x2)
+        codes = _l._make(made, stream, x, (M, K // 2), _l._f4)
         ld_codes = K // 2
     else:
-        ld_codes = _l._matrix(codes, "codes", _l._torch.float4_e2m1fn_x2, dev, (M, K // 2))[2]
+        ld_codes = _l._matrix(codes, "codes", _l._f4, dev, (M, K // 2))[2]
     if scales is None:
         scales = _l._make_scales(made, stream, x, M, K // 32)
     ld_scales = _l._scales(scales, "scales", dev, M, K // 32)
@@ -110,7 +114,7 @@ def pipe_dequantize_mxfp4(codes, scales, out_dtype=None, out=None, stream=None):
 
 def pipe_gemm_mxfp4_workspace_bytes(M, N, K) -> int:
     need = _l._Z(0)
-    st = _setup().pipe_gemm_mxfp4_workspace_bytes(M, N, K, ctypes.byref(need))
+    st = (_l._fns or _l._setup()).pipe_gemm_mxfp4_workspace_bytes(M, N, K, ctypes.byref(need))
     _pt._check(st, "pipe_gemm_mxfp4_workspace_bytes")
     return need.value
 
