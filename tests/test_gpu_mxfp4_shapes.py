@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import async_stage_tile_amd as pt
-from tests.test_gpu_mxfp4 import BF, F32, HF, operand, values
+from tests.test_gpu_mxfp4 import BF, F32, HF, SHAPES, operand, values
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +33,11 @@ def check_exact(M, N, K):
 def test_few_rows_by_columns(M, N, K):
     """Tiles of 32 columns up to 8192, of 64 past them."""
     check_exact(M, N, K)
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_sums_that_are_compared_bit_for_bit_are_exact(M, N, K):
+    """What makes every order of adding up right in test_exact_sums: all its sums of magnitudes stay below 2^20."""
+    (A, sa), (W, sw) = operand(M, K, 10), operand(N, K, 11)
+    a, w = values(A, sa).float().abs(), values(W, sw).float().abs()
+    assert float((a @ w.t()).max()) < 2 ** 20 * (1 - 2 ** -8)      # its fp32 sums are off by less
