@@ -593,19 +593,21 @@ hipError_t launch_grad_shape(const LayerNormGradParams& p, int64_t grid, hipStre
   return hipGetLastError();
 }
 
+// The shapes for few rows, of up to 512 columns for fewer than 4096, and of four rows a
+// workgroup have calls of 64 MiB at most: all stay in the cache.
 template <class T, bool KEPT>
 hipError_t launch_grad_type(const LayerNormGradParams& p, const GradShape& g, hipStream_t stream) {
   if (p.chunks <= 64)
     return g.many ? launch_grad_shape<T, 64, 512, 1, KEPT>(p, g.grid, stream)
-                  : launch_grad_shape<T, 64, 256, 1, KEPT>(p, g.grid, stream);
+                  : launch_grad_shape<T, 64, 256, 1, true>(p, g.grid, stream);
   if (p.chunks <= 128) return launch_grad_shape<T, 128, 512, 1, KEPT>(p, g.grid, stream);
   if (p.chunks <= 256) return launch_grad_shape<T, 256, 512, 1, KEPT>(p, g.grid, stream);
   if (p.chunks <= 512)
-    return g.few    ? launch_grad_shape<T, 256, 256, 2, KEPT>(p, g.grid, stream)
-           : g.many ? launch_grad_shape<T, 256, 1024, 2, KEPT>(p, g.grid, stream)
+    return g.few    ? launch_grad_shape<T, 256, 256, 2, true>(p, g.grid, stream)
+           : g.many ? launch_grad_shape<T, 256, 1024, 2, true>(p, g.grid, stream)
                     : launch_grad_shape<T, 256, 512, 2, KEPT>(p, g.grid, stream);
   if (p.chunks <= 1024)
-    return g.few ? launch_grad_shape<T, 256, 256, 4, KEPT>(p, g.grid, stream)
+    return g.few ? launch_grad_shape<T, 256, 256, 4, true>(p, g.grid, stream)
                  : launch_grad_shape<T, 256, 512, 4, KEPT>(p, g.grid, stream);
   if (p.chunks <= 2048) return launch_grad_shape<T, 512, 512, 4, KEPT>(p, g.grid, stream);
   return launch_grad_shape<T, 512, 512, 8, KEPT>(p, g.grid, stream);
