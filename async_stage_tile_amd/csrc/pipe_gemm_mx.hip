@@ -833,9 +833,10 @@ MxPlan mx_plan(int64_t M, int64_t N, int64_t bytes) {
         c.tiles_m = tiles_m;
         c.tiles_n = tiles_n;
         c.splits = splits;
-        // Laying the scales out anew pays from some 64 stages a workgroup on: 8192^3 (128)
-        // takes 244 us without and 240 with it, 4096 x 8192 x 8192 (64) 126 and 125, 4096 x
-        // 8192 x 4096 (32) 71.0 and 71.2, 4096^3 (16) 40.5 and 41.1.
+        // Laying the scales out anew pays from some 64 stages a workgroup on. Operands from
+        // memory: 8192^3 (128) takes 260 us without and 248 with it, 4096 x 8192 x 8192 (64)
+        // 134 and 130, 4096 x 8192 x 4096 (32) 77.0 and 75.4, 4096^3 (16) 39.8 and 40.6; from
+        // the last-level cache 244 and 240, 126 and 125, 71.0 and 71.2, 40.5 and 41.1.
         c.packed = sh.kind == kTile256 && rounds * c.steps >= 64 && M + N < int64_t(1) << 29;
       }
       if (tiles * splits >= sh.places) break;
