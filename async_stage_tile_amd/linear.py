@@ -455,7 +455,8 @@ def pipe_layernorm(x, weight, bias=None, residual=None, eps=1e-5, out_dtype=None
     max|y[m]| / 448; or torch.float4_e2m1fn_x2, the microscaled 4-bit form of
     pipe_quantize_mxfp4 (N a multiple of 32). Returns y; with e4m3 or 4 bits y,
     scales; with a residual the new stream h last: (y, h) or (y, scales, h).
-    h may be x or residual itself to update the stream in place."""
+    h may be x or residual itself to update the stream in place. Finite rows whose
+    squared deviations add up past fp32's range (bf16's largest values) give the bias."""
     fns = _fns or _setup()
     if _fast and stream is None and y is None and h is None and y_scales is None:
         out = _fast.layernorm(x, weight, bias, residual, eps, out_dtype)

@@ -167,7 +167,8 @@ pipe_status_t pipe_dequantize_mxfp4(const void* codes, const void* scales, void*
  *   m = mean(h), y = (h - m) * rsqrt(mean((h - m)^2) + eps) * weight + bias
  * with the sums in fp32 and the deviations from the mean itself; bias may be
  * NULL. A row with a NaN or an infinity is NaN; one of finite values whose squared
- * deviations add up past fp32's range (bf16's largest values) gives y = bias.
+ * deviations add up past fp32's range (bf16's largest values) gives y = bias; with
+ * eps == 0 one whose squared deviations are all zero in fp32 is not finite.
  * out_type == type: y rounded to it. PIPE_E4M3: y_scales are fp32, one a
  * row, as pipe_rmsnorm's. PIPE_MXFP4: y in the form above (N for K, y and ld_y
  * for codes and ld_codes, y_scales for scales), N % 32 == 0; y is rounded once,
