@@ -6,7 +6,7 @@
 // fp32 values (the packed 16 bits, unpacked in every turn, made it bound by the
 // vector units). The mean's rounding matters
 // where it is much larger than the deviations, so the sums of the second turn
-// correct it: with m0 the mean as computed, d = h - m0 and e = mean(d),
+// correct it: with m0 the rounded mean, d = h - m0 and e = mean(d),
 // mean((h - m)^2) = mean(d^2) - e^2 and y = (d - e) r w + b; d is exact or nearly
 // so, and e is tiny beside the deviations.
 //
@@ -57,16 +57,18 @@ __device__ __forceinline__ void row_sums(float (&v)[N], RowSums<TPR, WG, N>& x) 
   }
 }
 
-// The row's sum, as its deviations fmaf(-sum, 1 / N, h) take it. Where the mean or the
-// sum itself may pass fp32's range it is taken to be 0: the values are so large there
-// that their squares pass it, unless they are all the same. Below 2^119 no deviation
-// becomes infinite (the largest bf16 value is 2^128 - 2^120). `unit`, by which the
-// deviations are multiplied in their sum, is 1, or 0 there: the sum is then zero if all
-// values are finite, else NaN.
+// The rounded mean, which the row's deviations are taken from. Where it or the values'
+// sum may pass fp32's range it is taken to be 0: the values are so large there that
+// their squares pass it, unless they are all the same. Below 2^119 no deviation becomes
+// infinite (the largest bf16 value is 2^128 - 2^120). `unit`, by which the deviations are
+// multiplied in their sum, is 1, or 0 there: the sum is then zero if all values are
+// finite, else NaN. (The sum and 1 / N in its place would be a register more, which
+// the gradient of rows wider than 16384 does not have.)
 __device__ __forceinline__ float centre(float sum, float inv_n, float& unit) {
-  const bool fits = fabsf(sum * inv_n) < 0x1p119f;
+  const float mean = sum * inv_n;
+  const bool fits = fabsf(mean) < 0x1p119f;
   unit = fits ? 1.f : 0.f;
-  return fits ? sum : 0.f;
+  return fits ? mean : 0.f;
 }
 // Whether the squares of finite values' deviations pass fp32's range. Without a branch:
 // with one the gradient of 8192 x 1024 takes 20.6 us instead of 18.0.
@@ -169,14 +171,14 @@ __global__ void __launch_bounds__(WG) layernorm_kernel(LayerNormParams p) {
     }
   }
   float unit;
-  const float total = centre(sum[0], p.inv_n, unit);
+  const float mean = centre(sum[0], p.inv_n, unit);
   float dev[2] = {0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     if (t + TPR * i < p.chunks) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        f[i][e] = fmaf(-total, p.inv_n, f[i][e]);
+        f[i][e] -= mean;
         dev[0] = fmaf(f[i][e], unit, dev[0]);
         dev[1] += f[i][e] * f[i][e];
       }
@@ -392,7 +394,7 @@ __global__ void __launch_bounds__(WG) layernorm_grad_kernel(LayerNormGradParams 
     }
     keep_packed(wt);
     float unit;
-    const float total = centre(one[0], p.inv_n, unit);
+    const float mean = centre(one[0], p.inv_n, unit);
     float two[3] = {0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -401,7 +403,7 @@ __global__ void __launch_bounds__(WG) layernorm_grad_kernel(LayerNormGradParams 
         values(i, f, g, wf);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float v = fmaf(-total, p.inv_n, f[e]);
+          const float v = f[e] - mean;
           if constexpr (!kWide) fv[i][e] = v;
           two[0] = fmaf(v, unit, two[0]);
           two[1] += v * v;
@@ -441,7 +443,7 @@ __global__ void __launch_bounds__(WG) layernorm_grad_kernel(LayerNormGradParams 
         values(i, f, g, wf);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float u = fmaf(kWide ? fmaf(-total, p.inv_n, f[e]) : f[e], r, shift);
+          const float u = fmaf(kWide ? f[e] - mean : f[e], r, shift);
           o[e] = fmaf(g[e] * wf[e], r, -less) - u * tilt;
           dw[i][e] += g[e] * u;
           if constexpr (!kFull) db[i][e] += g[e];
